@@ -4,29 +4,20 @@
 // the HIP runtime, then enqueues kernels on the caller's stream and returns.
 #include <algorithm>
 #include <atomic>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 
 #include "../../include/mamba_mi355x.h"
+#include "api_check.h"
 #include "s6_internal.h"
 
 namespace {
 
-bool debug_enabled() {
-  static const bool on = [] {
-    const char* v = std::getenv("MAMBA_MI355X_DEBUG");
-    return v && v[0] && v[0] != '0';
-  }();
-  return on;
-}
-
-int fail(int status, const char* where, const char* what) {
-  if (debug_enabled()) std::fprintf(stderr, "[mamba_mi355x] %s: %s (%s)\n", where, mamba_status_string(status), what);
-  return status;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using s6::aligned16;
+using s6::fail;
+using s6::kMaxBatch;
+using s6::kMaxDim;
+using s6::PtrCheck;
 
 // ------------------------------------------------------------------ options
 
@@ -84,9 +75,6 @@ bool option_valid(int key, int64_t value) {
   }
 }
 
-constexpr int64_t kMaxBatch = 65535;
-constexpr int64_t kMaxDim = int64_t(1) << 22;
-
 // Shape and dtype checks shared by the entry points (MAMBA_OK if usable).
 int check_shape(const char* where, int64_t batch, int64_t seqlen, int64_t dim, int64_t dstate, int io) {
   if (io != MAMBA_IO_F32 && io != MAMBA_IO_BF16) return fail(MAMBA_ERR_DTYPE, where, "io_dtype");
@@ -99,18 +87,6 @@ int check_shape(const char* where, int64_t batch, int64_t seqlen, int64_t dim, i
   if (n > 4.0e18) return fail(MAMBA_ERR_DIM, where, "tensor too large");
   return MAMBA_OK;
 }
-
-struct PtrCheck {
-  const char* where;
-  int status = MAMBA_OK;
-  // A tensor that must be present when `needed`; any present pointer must be aligned.
-  void req(const void* p, bool needed, const char* name) {
-    if (status != MAMBA_OK) return;
-    if (!p && needed) status = fail(MAMBA_ERR_NULL, where, name);
-    else if (p && !aligned16(p)) status = fail(MAMBA_ERR_ALIGN, where, name);
-  }
-  void opt(const void* p, const char* name) { req(p, false, name); }
-};
 
 // Validation and launch shared by the real and complex decode steps.
 int state_update(bool cplx, const char* where, int64_t batch, int64_t dim, int64_t dstate, int io_dtype,

@@ -1,0 +1,85 @@
+// gated_device.h -- gfx950 numerics of the gated linear recurrence.
+//
+// Per token and channel, with kappa = c softplus(lam) of the channel:
+//     l = -kappa sigma(ra),  a = e^l,  s = sqrt(1 - a^2),  b = s sigma(rx) u,  h' = a h + b.
+// A slow channel has 1 - a near 1e-4 or less, so a is formed as 1 - m from
+// m = -expm1(l): the subtraction rounds once, without the bias that an exp near
+// 1 carries through thousands of products, and 1 - a^2 = m (2 - m) keeps its
+// relative accuracy where 1 - a*a would cancel.
+#pragma once
+
+#include "s6_device.h"
+
+namespace s6 {
+
+// m = 1 - e^y for y <= 0, relative error about 2e-7:
+//   y > -0.35 : -y (1 + y/2 (1 + y/3 (1 + ... y/7))), truncation below 2e-8
+//   otherwise : 1 - e^y, cancellation below 2^-24 * 0.7 / 0.3
+__device__ __forceinline__ float one_minus_exp(float y) {
+  float p = __builtin_fmaf(y, 1.0f / 5040.0f, 1.0f / 720.0f);
+  p = __builtin_fmaf(y, p, 1.0f / 120.0f);
+  p = __builtin_fmaf(y, p, 1.0f / 24.0f);
+  p = __builtin_fmaf(y, p, 1.0f / 6.0f);
+  p = __builtin_fmaf(y, p, 0.5f);
+  p = __builtin_fmaf(y, p, 1.0f);
+  const float far = 1.0f - ex2(y * kLog2e);
+  return y > -0.35f ? -y * p : far;
+}
+
+// sigma(v) and 1 - sigma(v), each to a few ulp relative; saturates without NaN.
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-v * kLog2e)); }
+__device__ __forceinline__ void sigmoid_pair(float v, float& sg, float& om) {
+  const float e = ex2(fminf(-v * kLog2e, 126.0f));  // finite, so that e * sg is a number
+  sg = rcp(1.0f + e);
+  om = e * sg;
+}
+
+// Decay and input of one token: h' = a h + b.
+__device__ __forceinline__ void gated_token(float ra, float rx, float u, float kappa, bool reset, float& a, float& b) {
+  const float m = one_minus_exp(-kappa * sigmoid(ra));
+  const float s = __builtin_amdgcn_sqrtf(m * (2.0f - m));
+  const float x = sigmoid(rx) * u;
+  a = reset ? 0.0f : 1.0f - m;
+  b = reset ? x : s * x;
+}
+
+// The same with what the backward needs:
+//   s, sx = sigma(rx), ox = 1 - sx, oa = 1 - sigma(ra), l (0 on a reset), and
+//   q = a^2 l / s, 0 where s is 0 (l/s -> 0 with l) and on a reset.
+struct GatedGrad {
+  float a, s, sx, ox, oa, l, q;
+};
+__device__ __forceinline__ GatedGrad gated_grad(float ra, float rx, float kappa, bool reset) {
+  GatedGrad g;
+  float sa;
+  sigmoid_pair(ra, sa, g.oa);
+  sigmoid_pair(rx, g.sx, g.ox);
+  const float l = -kappa * sa;
+  const float m = one_minus_exp(l);
+  const float s2 = m * (2.0f - m);
+  const float a = 1.0f - m;
+  const float s = __builtin_amdgcn_sqrtf(s2);
+  const float q = s > 0.0f ? a * a * (l * rcp(s)) : 0.0f;
+  g.a = reset ? 0.0f : a;
+  g.s = reset ? 1.0f : s;
+  g.l = reset ? 0.0f : l;
+  g.q = reset ? 0.0f : q;
+  return g;
+}
+
+// d kappa / d lam / kappa = sigma(lam) / softplus(lam); the sums of e = dL/dl * l times this are dlam.
+// Where softplus underflows, e^lam / e^lam = 1.
+__device__ __forceinline__ float dlam_factor(float lam) {
+  const float sp = softplus(lam);
+  return sp > 0.0f ? sigmoid(lam) / sp : 1.0f;
+}
+
+// SiLU(z) and its derivative sigma(z) (1 + z (1 - sigma(z))).
+__device__ __forceinline__ void silu_pair(float z, float& f, float& df) {
+  float sg, om;
+  sigmoid_pair(z, sg, om);
+  f = z * sg;
+  df = sg * __builtin_fmaf(z, om, 1.0f);
+}
+
+}  // namespace s6
