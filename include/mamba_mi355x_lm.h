@@ -24,7 +24,7 @@ extern "C" {
 #endif
 
 /* Tokens between two states that mamba_gated_scan_fwd saves for the backward. */
-#define MAMBA_GATED_STATE_CHUNK 64
+#define MAMBA_GATED_STATE_CHUNK 8
 
 /*
  * Gated linear recurrence.  Per batch row and channel d, with sigma the logistic
@@ -39,13 +39,14 @@ extern "C" {
  *   c                         : decay rate, finite and > 0 (host value)
  *   reset                     : (batch, seqlen)       bytes, nullable
  *   h0, last_state            : (batch, dim)          float, nullable
- *   states                    : (batch, ceil(seqlen / 64), dim) float, nullable:
- *                               the state entering every 64th token (the first is
+ *   states                    : (batch, ceil(seqlen / 8), dim) float, nullable:
+ *                               the state entering every 8th token (the first is
  *                               h0 or zero), for mamba_gated_scan_bwd
  *   workspace                 : mamba_gated_scan_fwd_workspace_size() bytes of
  *                               scratch (may be NULL when that is 0)
- * Limits: 0 <= batch <= 65535, seqlen >= 0, 0 <= dim <= 4194304; a c out of range
- * is MAMBA_ERR_OPTION.  seqlen == 0 writes only last_state (= h0 or zero).
+ * Limits: 0 <= batch <= 65535, seqlen >= 0, 0 <= dim <= 4194304, and
+ * batch * ceil(dim / 64) * ceil(seqlen / 64) < 2^31; a c out of range is
+ * MAMBA_ERR_OPTION.  seqlen == 0 writes only last_state (= h0 or zero).
  * Where a sequence is split over workgroups they hand their states over in
  * bounded waits as mamba_scan_fwd's chunks do: mamba_stream_status reports one
  * that gave up, and what follows it is NaN.

@@ -29,7 +29,8 @@ int check_gated(const char* where, int64_t batch, int64_t seqlen, int64_t dim, i
   if (batch > kMaxBatch) return fail(MAMBA_ERR_DIM, where, "batch > 65535");
   if (dim > kMaxDim) return fail(MAMBA_ERR_DIM, where, "dim > 4194304");
   if (seqlen > (int64_t(1) << 40)) return fail(MAMBA_ERR_DIM, where, "seqlen > 2^40");
-  if ((double)batch * (double)seqlen * (double)dim > 1.0e18) return fail(MAMBA_ERR_DIM, where, "tensor too large");
+  if ((double)batch * (double)seqlen * (double)dim > 1.0e18 || !s6::gated_fits(batch, seqlen, dim))
+    return fail(MAMBA_ERR_DIM, where, "tensor too large");
   return MAMBA_OK;
 }
 

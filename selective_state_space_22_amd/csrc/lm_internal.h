@@ -12,7 +12,7 @@ namespace s6 {
 
 // ---------------------------------------------------------------- gated recurrence (gated_scan.hip)
 
-constexpr int kGatedStateChunk = 64;  // tokens between two saved states (MAMBA_GATED_STATE_CHUNK)
+constexpr int kGatedStateChunk = 8;  // tokens between two saved states (MAMBA_GATED_STATE_CHUNK)
 
 struct GatedArgs {
   const void* u;
@@ -54,6 +54,7 @@ struct GatedStepArgs {
   float c;
 };
 
+bool gated_fits(int64_t batch, int64_t L, int64_t D);  // false: more work items than a launch can count
 size_t gated_fwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int io);
 hipError_t launch_gated_fwd(const GatedArgs& a, int io, void* workspace, hipStream_t stream);
 size_t gated_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int io);

@@ -10,7 +10,7 @@ import ctypes
 
 from .binding import MambaError, _check_status, _io_dtype, _ptr, _stream, load_library
 
-MAMBA_GATED_STATE_CHUNK = 64
+MAMBA_GATED_STATE_CHUNK = 8
 
 _typed = None
 
@@ -74,7 +74,7 @@ def mamba_gated_scan_fwd(u, gate_a, gate_x, lam, z=None, h0=None, reset=None, c=
 
     u, gate_a, gate_x, z: (batch, L, D) float32 or bfloat16; lam: (D,) float32; h0: (batch, D) float32;
     reset: (batch, L) bool or uint8.  Returns (out, last_state), and with return_states=True also the
-    states that mamba_gated_scan_bwd takes, (batch, ceil(L / 64), D) float32.
+    states that mamba_gated_scan_bwd takes, (batch, ceil(L / 8), D) float32.
     check=True synchronises the stream and raises MambaError if a wait between sequence chunks gave up."""
     import torch
 

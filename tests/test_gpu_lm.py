@@ -75,7 +75,7 @@ def _check_gated(p, opt, dout, dlast, io, c=8.0, label="", states_too=True):
         wg = R.gated_bwd(**p64, c=c, dout=dout, dlast=dlast, **opt)
     out, last, states = lib.mamba_gated_scan_fwd(*args, c=c, **kw, return_states=True, check=True)
     errs = {"out": parity_error(_host(out), want), "last": parity_error(_host(last), wlast),
-            "states": parity_error(_host(states), wstates[:, :-1][:, ::64])}
+            "states": parity_error(_host(states), wstates[:, :-1][:, ::lib.MAMBA_GATED_STATE_CHUNK])}
     assert errs["out"] <= tol and errs["last"] <= 1e-4 and errs["states"] <= 1e-4, (label, errs)
     for given in (states, None) if states_too else (states,):
         g = lib.mamba_gated_scan_bwd(*args, _dev(dout, io), c=c, **kw, states=given, dlast_state=_dev(dlast),
@@ -87,7 +87,7 @@ def _check_gated(p, opt, dout, dlast, io, c=8.0, label="", states_too=True):
     return out, last, g
 
 
-# lengths around the 64-token states and the tiles, widths that are and are not multiples of the vector
+# lengths around the saved states and the tiles, widths that are and are not multiples of the vector
 GATED = [(1, 1, 1), (2, 2, 3), (1, 63, 64), (3, 64, 65), (2, 65, 130), (1, 127, 8), (2, 129, 256), (1, 1000, 48),
          (5, 257, 1), (1, 4100, 72), (2, 700, 520), (1, 20011, 16)]
 
