@@ -12,10 +12,10 @@ namespace {
 
 // ---------------------------------------------------------------- rows of a wave's tokens
 //
-// A lane owns one channel.  The rows of a wave's tokens are reached through
-// bounds-checked buffer resources: a load outside (a token past the end, a lane past the
-// last channel, an absent tensor of 0 bytes) returns 0 and a store is dropped, with no
-// branch around either.
+// A lane owns C channels (two where bf16 pairs share a 32-bit word, else one).  The rows of
+// a wave's tokens are reached through bounds-checked buffer resources: a load outside (a
+// token past the end, a lane past the last channel, an absent tensor of 0 bytes) returns 0
+// and a store is dropped, with no branch around either.
 
 constexpr int kBufferDword3 = 0x00027000;   // raw, 32-bit data format
 constexpr uint32_t kNowhere = 0x80000000u;  // a lane offset beyond every resource here
@@ -35,20 +35,32 @@ struct Rows {
   __device__ __forceinline__ uint32_t at(int i) const { return (uint32_t)(i < n ? i : n) * stride; }
 };
 
-template <typename IO>
+// C channels of one token as loaded, and as numbers.
+template <typename IO, int C>
 __device__ __forceinline__ uint32_t fetch(const Rows& w, int i, uint32_t off) {
-  if constexpr (sizeof(IO) == 2) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, off, w.at(i), 0);
+  if constexpr (sizeof(IO) * C == 2) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, off, w.at(i), 0) << 16;
   else return __builtin_amdgcn_raw_buffer_load_b32(w.r, off, w.at(i), 0);
 }
-template <typename IO>
-__device__ __forceinline__ float value(uint32_t raw) {
-  if constexpr (sizeof(IO) == 2) return bf16_lo(raw);
-  else return __uint_as_float(raw);
+template <int C>
+__device__ __forceinline__ float value(uint32_t raw, int c) {
+  return C == 2 && c == 0 ? bf16_lo(raw) : C == 2 ? bf16_hi(raw) : __uint_as_float(raw);
+}
+template <typename IO, int C>
+__device__ __forceinline__ void put(const Rows& w, int i, uint32_t off, const float (&v)[C]) {
+  if constexpr (C == 2)
+    __builtin_amdgcn_raw_buffer_store_b32(f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16, w.r, off, w.at(i), 0);
+  else if constexpr (sizeof(IO) == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v[0]), w.r, off, w.at(i), 0);
+  else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), w.r, off, w.at(i), 0);
 }
 template <typename IO>
-__device__ __forceinline__ void put(const Rows& w, int i, uint32_t off, float v) {
-  if constexpr (sizeof(IO) == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v), w.r, off, w.at(i), 0);
-  else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), w.r, off, w.at(i), 0);
+__device__ __forceinline__ void put1(const Rows& w, int i, uint32_t off, float v) {
+  const float a[1] = {v};
+  put<IO, 1>(w, i, off, a);
+}
+template <int C>
+__device__ __forceinline__ void put_state(const Rows& w, int i, uint32_t off, const float (&v)[C]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[c]), w.r, off + 4 * c, w.at(i), 0);
 }
 
 // Has a value formed at this point.  A token's raw values are taken when its turn comes and
@@ -63,14 +75,19 @@ __device__ __forceinline__ void fix(V& v) { asm volatile("" : "+v"(v)); }
 // A workgroup takes work items of 64 channels and some tokens per wave (wave after wave).
 // Each wave scans its tokens from zero and leaves their affine map h -> A h + H in LDS.
 // The workgroup publishes the map of all its tokens, composes the maps of its
-// predecessors back to one whose end state is known (or to the initial state), publishes
-// its own end state, and only then runs its recurrence from the state that enters, from
-// decays and inputs still in registers: every input is read once.  The loads of the next
-// item are in flight during the look back and the recurrence of the present one.
+// predecessors back to one that depends on nothing older, publishes its own end state as
+// such a map (A = 0) in the place of the first, and only then runs its recurrence from the
+// state that enters, from decays and inputs still in registers: every input is read once.
+// The loads of the next item are in flight during the look back and the recurrence of the
+// present one.
 //
-// A published word is its own flag: the workspace starts as all ones, a NaN that no
-// publisher writes (its NaNs are replaced by the standard one), so a reader needs no
-// separate flag and no cache write-back orders the two.  Items are handed out by a
+// Which of the two a reader meets depends on timing, so maps are never composed with each
+// other: the state is taken through them one by one, oldest first, which gives the bits
+// that the chain of end states has wherever it starts.
+//
+// A published {A, H} is one 64-bit word and its own flag: the workspace starts as all
+// ones, and an A of all ones is a NaN that no publisher writes (its NaNs are replaced by
+// the standard one), so a reader needs no separate flag and no cache write-back.  Items are handed out by a
 // counter, level after level.  A workgroup holds one item that it works on and the next
 // one that it only loads; the unfinished item that was handed out first is one that its
 // holder works on (the holder's present item came before), and it waits for nothing
@@ -78,95 +95,113 @@ __device__ __forceinline__ void fix(V& v) { asm volatile("" : "+v"(v)); }
 // A decay of exactly 0 (a reset) drops the older state, whatever it is.
 
 constexpr int kMaxWaves = 8;
-constexpr int kLook = 2;  // predecessors per wave and round of the look back
+constexpr int kRounds = 3;  // rounds of the look back in which every wave reads one predecessor
+constexpr int kDepth = 1 + kRounds * kMaxWaves;
 constexpr uint32_t kEmpty = 0xffffffffu;
 
+// x / d for x < 2^31 by a multiplication: m = floor(2^(31 + s) / d) + 1, 2^s >= d.
+struct Divisor {
+  uint32_t m;
+  int s;
+  __device__ __forceinline__ uint32_t of(uint32_t x) const { return (uint32_t)(((uint64_t)x * m) >> (31 + s)); }
+};
+
 struct Link {
-  unsigned long long* map;  // (levels, blocks, 64) of {A, H}
-  uint32_t* end;            // (levels, blocks, 64)
+  unsigned long long* map;  // (levels, blocks, 64 * C) of {A, H}
   uint32_t* ticket;
   uint32_t* err;
   uint32_t spin_limit;
   int levels, blocks, row_blocks;
+  Divisor by_blocks, by_row;
 };
 
 // Arrays that consecutive items write without a barrier between them are doubled.
+template <int C>
 struct ScanShared {
-  float A[2][kMaxWaves][64], H[2][kMaxWaves][64];    // the waves' maps
-  float sA[kMaxWaves][64], sH[kMaxWaves][64];        // the look back's segments
-  int closed[kMaxWaves];
+  float A[2][kMaxWaves][64 * C], H[2][kMaxWaves][64 * C];  // the waves' maps
+  float backA[kDepth][64 * C], backH[kDepth][64 * C];      // the predecessors' maps, nearest first
   uint32_t item[2];
 };
 
 __device__ __forceinline__ uint32_t published(float v) { return v != v ? 0x7fc00000u : __float_as_uint(v); }
 
-// (A, H) after (a, h): the older map applied first.
-__device__ __forceinline__ void compose(float& A, float& H, float a, float h) {
-  H = A == 0.0f ? H : __builtin_fmaf(A, h, H);
-  A = A == 0.0f ? 0.0f : A * a;
-}
 __device__ __forceinline__ float apply(float A, float H, float h) { return A == 0.0f ? H : __builtin_fmaf(A, h, H); }
 
-__device__ __forceinline__ void read_words(const Link& k, int level, int blk, uint32_t lane, uint32_t& end,
-                                           unsigned long long& map) {
-  const size_t row = ((size_t)level * k.blocks + blk) * 64;
-  end = __hip_atomic_load(k.end + row + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  map = __hip_atomic_load(k.map + row + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+template <int C>
+__device__ __forceinline__ void read_map(const Link& k, int level, int blk, uint32_t lane, unsigned long long (&m)[C]) {
+  const unsigned long long* from = k.map + ((size_t)level * k.blocks + blk) * 64 * C;
+#pragma unroll
+  for (int c = 0; c < C; ++c) m[c] = __hip_atomic_load(from + (lane * C + c), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <int C>
+__device__ __forceinline__ void write_map(const Link& k, int level, int blk, uint32_t lane, const float (&A)[C],
+                                          const float (&H)[C]) {
+  unsigned long long* to = k.map + ((size_t)level * k.blocks + blk) * 64 * C;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    __hip_atomic_store(to + (lane * C + c), published(A[c]) | (unsigned long long)published(H[c]) << 32,
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// State entering `level` (> 0) of a block (init: the one entering level 0).  All waves call.
-__device__ __forceinline__ float look_back(const Link& k, int level, int blk, int wave, uint32_t lane, float init,
-                                           ScanShared& sm) {
-  const int waves = blockDim.x >> 6;
-  float A = 1.0f, H = 0.0f;
-  for (int newest = level - 1;; newest -= waves * kLook) {
-    float a = 1.0f, h = 0.0f;
-    int closed = 0;
-    const int e0 = newest - wave * kLook;
-    unsigned long long m[kLook];
-    uint32_t x[kLook];
+// Brings the map of level e (-1: the initial state) into slot `to` of sm.  final: only a map
+// that depends on nothing older will do.
+template <int C>
+__device__ __forceinline__ void look_at(const Link& k, int e, int blk, uint32_t lane, const float (&init)[C],
+                                        bool final, int to, ScanShared<C>& sm) {
+  float A[C], H[C];
 #pragma unroll
-    for (int j = 0; j < kLook; ++j) read_words(k, e0 - j > 0 ? e0 - j : 0, blk, lane, x[j], m[j]);
+  for (int c = 0; c < C; ++c) A[c] = 0.0f, H[c] = init[c];
+  for (uint32_t polls = 0; e >= 0; ++polls) {
+    unsigned long long m[C];
+    read_map<C>(k, e, blk, lane, m);
+    bool there = true;
 #pragma unroll
-    for (int j = 0; j < kLook; ++j) {
-      if (closed || e0 - j < -1) continue;
-      if (e0 - j == -1) {
-        h = apply(a, h, init);
-        closed = 1;
-        continue;
-      }
-      for (uint32_t polls = 0;; ++polls) {
-        if (__all(x[j] != kEmpty)) {
-          h = apply(a, h, __uint_as_float(x[j]));
-          closed = 1;
-          break;
+    for (int c = 0; c < C; ++c) {
+      A[c] = __uint_as_float((uint32_t)m[c]), H[c] = __uint_as_float((uint32_t)(m[c] >> 32));
+      there &= final ? A[c] == 0.0f : (uint32_t)m[c] != kEmpty;
+    }
+    if (__all(there)) break;
+    if (polls >= k.spin_limit) {  // never expected: report, and go on from NaN
+      if (lane == 0) __hip_atomic_store(k.err, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int c = 0; c < C; ++c) A[c] = 0.0f, H[c] = __uint_as_float(0x7fc00000u);
+      break;
+    }
+    __builtin_amdgcn_s_sleep(1);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) sm.backA[to][lane * C + c] = A[c], sm.backH[to][lane * C + c] = H[c];
+}
+
+// State entering `level` (> 0) of a block (init: the one entering level 0).  All waves
+// call.  The first wave looks at the nearest predecessor alone, which is all there is to
+// do unless many levels are in flight; then all waves look at one each, kRounds times, and
+// the last of these waits for an end state.
+template <int C>
+__device__ __forceinline__ void look_back(const Link& k, int level, int blk, int wave, uint32_t lane,
+                                          const float (&init)[C], float (&state)[C], ScanShared<C>& sm) {
+  int slot = 0;
+  for (int lookers = 1;; lookers = blockDim.x >> 6) {
+    const bool last = slot + lookers + kMaxWaves > kDepth;
+    const int e = level - 1 - slot - wave;
+    if (wave < lookers && e >= -1) look_at<C>(k, e, blk, lane, init, last && wave == lookers - 1, slot + wave, sm);
+    __syncthreads();
+    const int end = slot + lookers < level + 1 ? slot + lookers : level + 1;
+    for (bool closed = false; slot < end && !closed; ++slot) {
+      closed = true;
+#pragma unroll
+      for (int c = 0; c < C; ++c) closed &= sm.backA[slot][lane * C + c] == 0.0f;
+      closed = __all(closed);
+      if (closed) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) state[c] = sm.backH[slot][lane * C + c];
+        for (int j = slot - 1; j >= 0; --j) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) state[c] = apply(sm.backA[j][lane * C + c], sm.backH[j][lane * C + c], state[c]);
         }
-        if (__all((uint32_t)m[j] != kEmpty)) {
-          compose(a, h, __uint_as_float((uint32_t)m[j]), __uint_as_float((uint32_t)(m[j] >> 32)));
-          break;
-        }
-        if (polls >= k.spin_limit) {  // never expected: report, and go on from NaN
-          if (lane == 0) __hip_atomic_store(k.err, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          h = __uint_as_float(0x7fc00000u);
-          closed = 1;
-          break;
-        }
-        __builtin_amdgcn_s_sleep(1);
-        read_words(k, e0 - j, blk, lane, x[j], m[j]);
+        return;
       }
     }
-    sm.sA[wave][lane] = a;
-    sm.sH[wave][lane] = h;
-    if (lane == 0) sm.closed[wave] = closed;
-    __syncthreads();
-    bool done = false;
-#pragma unroll 1
-    for (int w = 0; w < waves && !done; ++w) {
-      compose(A, H, sm.sA[w][lane], sm.sH[w][lane]);
-      done = sm.closed[w] != 0;
-    }
-    if (done) return H;
-    __syncthreads();
   }
 }
 
@@ -175,22 +210,25 @@ __device__ __forceinline__ float look_back(const Link& k, int level, int blk, in
 struct Place {
   int level, blk, n;  // n: tokens of the wave's run inside the sequence
   int64_t bt, run, t0, row;
-  uint32_t d;    // the lane's channel (0 where it is past the last)
-  uint32_t off;  // the lane's offset in elements, or kNowhere
-  template <int T, bool REVERSE>
-  __device__ __forceinline__ void set(const Link& k, uint32_t item, int wave, uint32_t lane, int64_t L, int64_t D) {
+  uint32_t d;    // the lane's first channel (0 where it is past the last)
+  uint32_t off;  // the same as an offset in elements, or kNowhere
+  template <int T, int C, bool REVERSE>
+  __device__ __forceinline__ void set(const Link& k, uint32_t item, bool real, int wave, uint32_t lane, int64_t L,
+                                      int64_t D) {
     const int waves = blockDim.x >> 6;
-    level = (int)(item / (uint32_t)k.blocks);
-    blk = (int)(item % (uint32_t)k.blocks);
-    bt = blk / k.row_blocks;
-    const uint32_t c = (uint32_t)(blk % k.row_blocks) * 64 + lane;
+    level = (int)k.by_blocks.of(item);
+    blk = (int)(item - (uint32_t)level * (uint32_t)k.blocks);
+    const uint32_t b = k.by_row.of((uint32_t)blk);
+    bt = b;
+    const uint32_t c = ((uint32_t)(blk - b * k.row_blocks) * 64 + lane) * C;
     const bool act = c < (uint32_t)D;
     d = act ? c : 0;
     off = act ? c : kNowhere;
     run = REVERSE ? (int64_t)(k.levels - 1 - level) * waves + (waves - 1 - wave) : (int64_t)level * waves + wave;
+    const int64_t left = real ? L - run * T : 0;
+    n = __builtin_amdgcn_readfirstlane((int)(left < T ? (left > 0 ? left : 0) : T));
+    if (n == 0) run = 0;  // (nothing is read or written there)
     t0 = run * T;
-    n = __builtin_amdgcn_readfirstlane((int)(L - t0 < T ? (L - t0 > 0 ? L - t0 : 0) : T));
-    if (n == 0) run = t0 = 0;  // (nothing is read or written there)
     row = bt * L + t0;
   }
 };
@@ -200,51 +238,62 @@ __device__ __forceinline__ uint32_t bytes(uint32_t off) { return off == kNowhere
 
 // The workgroup's first item, and its request for the next (thread 0's answer is stored
 // into sm.item before the barrier of the waves' maps).
-__device__ __forceinline__ uint32_t first_item(const Link& k, ScanShared& sm) {
+__device__ __forceinline__ uint32_t first_item(const Link& k, uint32_t* shared_item) {
   if (k.levels == 1) return blockIdx.x;
-  if (threadIdx.x == 0) sm.item[1] = atomicAdd(k.ticket, 1u);
+  if (threadIdx.x == 0) *shared_item = atomicAdd(k.ticket, 1u);
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(sm.item[1]);
+  return __builtin_amdgcn_readfirstlane(*shared_item);
 }
 __device__ __forceinline__ uint32_t request_item(const Link& k, uint32_t item) {
   if (k.levels == 1) return item + gridDim.x;
   return threadIdx.x == 0 ? atomicAdd(k.ticket, 1u) : 0u;
 }
 
-// The map of the waves before this one, in slot s of sm; the last wave publishes the
-// level's map.
-__device__ __forceinline__ void publish_map(const Link& k, const Place& p, int s, int wave, uint32_t lane, float A,
-                                            float H, float& Ap, float& Hp, ScanShared& sm) {
-  const int waves = blockDim.x >> 6;
-  Ap = 1.0f, Hp = 0.0f;
-  float a[kMaxWaves - 1], h[kMaxWaves - 1];
+// The map (Ap, Hp) of the waves before this one, in slot s of sm, and of this one with them
+// (Aw, Hw): in the last wave the level's map, which it publishes.
+template <int C>
+__device__ __forceinline__ void publish_map(const Link& k, const Place& p, int s, int wave, uint32_t lane,
+                                            const float (&A)[C], const float (&H)[C], float (&Ap)[C], float (&Hp)[C],
+                                            float (&Aw)[C], float (&Hw)[C], const ScanShared<C>& sm) {
 #pragma unroll
-  for (int w = 0; w < kMaxWaves - 1; ++w) a[w] = sm.A[s][w][lane], h[w] = sm.H[s][w][lane];
+  for (int c = 0; c < C; ++c) Ap[c] = 1.0f, Hp[c] = 0.0f;
 #pragma unroll
   for (int w = 0; w < kMaxWaves - 1; ++w)
     if (w < wave) {
-      Hp = apply(a[w], h[w], Hp);
-      Ap = a[w] == 0.0f ? 0.0f : Ap * a[w];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float a = sm.A[s][w][lane * C + c];
+        Hp[c] = apply(a, sm.H[s][w][lane * C + c], Hp[c]);
+        Ap[c] = a == 0.0f ? 0.0f : Ap[c] * a;
+      }
     }
-  if (wave == waves - 1 && p.level > 0 && p.level + 1 < k.levels) {
-    const float m = A == 0.0f ? 0.0f : Ap * A;
-    __hip_atomic_store(k.map + ((size_t)p.level * k.blocks + p.blk) * 64 + lane,
-                       published(m) | (unsigned long long)published(apply(A, H, Hp)) << 32, __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) Aw[c] = A[c] == 0.0f ? 0.0f : Ap[c] * A[c], Hw[c] = apply(A[c], H[c], Hp[c]);
+  if (wave == (int)(blockDim.x >> 6) - 1 && p.level > 0 && p.level + 1 < k.levels)
+    write_map<C>(k, p.level, p.blk, lane, Aw, Hw);
 }
 
-// State entering the wave's tokens; the last wave publishes the level's end state and
-// returns it in `end`.
-__device__ __forceinline__ float enter(const Link& k, const Place& p, int wave, uint32_t lane, float A, float H,
-                                       float Ap, float Hp, float init, float& end, ScanShared& sm) {
-  const float in = p.level == 0 ? init : look_back(k, p.level, p.blk, wave, lane, init, sm);
-  const float carry = apply(Ap, Hp, in);
-  end = apply(A, H, carry);
-  if (wave == (int)(blockDim.x >> 6) - 1 && p.level + 1 < k.levels)
-    __hip_atomic_store(k.end + ((size_t)p.level * k.blocks + p.blk) * 64 + lane, published(end), __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-  return carry;
+// State entering the wave's tokens (from init at level 0); the last wave publishes the
+// level's end state and has it in `end`.
+template <int C>
+__device__ __forceinline__ void enter(const Link& k, const Place& p, int wave, uint32_t lane, const float (&Ap)[C],
+                                      const float (&Hp)[C], const float (&Aw)[C], const float (&Hw)[C],
+                                      const float (&init)[C], float (&carry)[C], float (&end)[C], ScanShared<C>& sm) {
+  float in[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) in[c] = init[c];
+  if (p.level > 0) look_back<C>(k, p.level, p.blk, wave, lane, init, in, sm);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    carry[c] = apply(Ap[c], Hp[c], in[c]);
+    end[c] = apply(Aw[c], Hw[c], in[c]);  // the bits that a reader of the level's map gets
+  }
+  if (wave == (int)(blockDim.x >> 6) - 1 && p.level + 1 < k.levels) {
+    float none[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) none[c] = 0.0f;
+    write_map<C>(k, p.level, p.blk, lane, none, end);
+  }
 }
 
 __global__ __launch_bounds__(256) void gated_clear_kernel(uint32_t* ticket, uint32_t* words, int64_t n) {
@@ -255,43 +304,49 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(uint32_t* ticket, uint
 
 // ---------------------------------------------------------------- forward
 
-constexpr int kTokF = 16;  // tokens per wave
+// Tokens per wave: 16 elements a lane (decays and inputs, 32 registers, and the next run's
+// raw values beside them) is what 128 registers hold.
+template <int C>
+constexpr int kTokF = 16 / C;
 
 // A run as loaded (z, which is needed last, is loaded when the run's turn comes).
-template <typename IO, bool HASR, int T>
+template <typename IO, int C, bool HASR, int T>
 struct FwdRaw {
   uint32_t ra[T], rx[T], u[T], reset;
-  float lam, init;
+  float lam[C], init[C];
   __device__ __forceinline__ void load(const GatedArgs& g, const Place& p, uint32_t lane) {
     const uint32_t stride = (uint32_t)g.D * sizeof(IO), off = bytes<IO>(p.off);
     const size_t skip = (size_t)p.row * stride;
     const Rows r_ra(g.ra, skip, stride, p.n), r_rx(g.rx, skip, stride, p.n), r_u(g.u, skip, stride, p.n);
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-      ra[i] = fetch<IO>(r_ra, i, off);
-      rx[i] = fetch<IO>(r_rx, i, off);
-      u[i] = fetch<IO>(r_u, i, off);
+      ra[i] = fetch<IO, C>(r_ra, i, off);
+      rx[i] = fetch<IO, C>(r_rx, i, off);
+      u[i] = fetch<IO, C>(r_u, i, off);
     }
     if (HASR) reset = (int)lane < p.n ? g.reset[p.row + lane] : 0;
-    lam = g.lam[p.d];
-    init = g.h0 && p.level == 0 ? g.h0[p.bt * g.D + p.d] : 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      lam[c] = g.lam[p.d + c];
+      init[c] = g.h0 && p.level == 0 ? g.h0[p.bt * g.D + p.d + c] : 0.0f;
+    }
   }
 };
 
-template <typename IO, bool HASZ, bool HASR>
+template <typename IO, int C, bool HASZ, bool HASR>
 __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_fwd_kernel(GatedArgs g, Link k) {
-  constexpr int T = kTokF;
-  __shared__ ScanShared sm;
+  constexpr int T = kTokF<C>;
+  __shared__ ScanShared<C> sm;
   const uint32_t lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t items = (uint32_t)k.levels * (uint32_t)k.blocks;
   const int64_t nst = (g.L + kGatedStateChunk - 1) / kGatedStateChunk;
   const uint32_t stride = (uint32_t)g.D * sizeof(IO), sstride = (uint32_t)g.D * 4;
-  uint32_t item = first_item(k, sm);
+  uint32_t item = first_item(k, &sm.item[1]);
   if (item >= items) return;
   Place p;
-  p.set<T, false>(k, item, wave, lane, g.L, g.D);
-  FwdRaw<IO, HASR, T> raw;
+  p.set<T, C, false>(k, item, true, wave, lane, g.L, g.D);
+  FwdRaw<IO, C, HASR, T> raw;
   raw.load(g, p, lane);
   for (int s = 0;; s ^= 1) {
     uint32_t next = request_item(k, item);
@@ -300,51 +355,61 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_fwd_kernel(GatedArgs 
     if (HASZ) {
       const Rows r_z(g.z, (size_t)p.row * stride, stride, p.n);
 #pragma unroll
-      for (int i = 0; i < T; ++i) z[i] = fetch<IO>(r_z, i, off);
+      for (int i = 0; i < T; ++i) z[i] = fetch<IO, C>(r_z, i, off);
     }
-    const float kappa = g.c * softplus(raw.lam), init = raw.init;
+    float kappa[C], init[C], A[C], H[C], a[T][C], b[T][C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      kappa[c] = g.c * softplus(raw.lam[c]), init[c] = raw.init[c], A[c] = 1.0f, H[c] = 0.0f;
     const uint32_t reset = HASR ? (uint32_t)__ballot(raw.reset != 0) : 0;
     // Decays and inputs, and the run's map from zero.  A token past the end has loaded
     // zeros: it adds nothing, and no token after it is kept.
-    float a[T], b[T], A = 1.0f, H = 0.0f;
 #pragma unroll
     for (int i = 0; i < T; ++i) {
       const bool cut = HASR && ((reset >> i) & 1);
       fix(raw.ra[i]), fix(raw.rx[i]), fix(raw.u[i]);
-      gated_token(value<IO>(raw.ra[i]), value<IO>(raw.rx[i]), value<IO>(raw.u[i]), kappa, cut, a[i], b[i]);
-      H = cut ? b[i] : __builtin_fmaf(a[i], H, b[i]);
-      A = cut ? 0.0f : A * a[i];
-      fix(a[i]), fix(b[i]);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        gated_token(value<C>(raw.ra[i], c), value<C>(raw.rx[i], c), value<C>(raw.u[i], c), kappa[c], cut, a[i][c],
+                    b[i][c]);
+        H[c] = cut ? b[i][c] : __builtin_fmaf(a[i][c], H[c], b[i][c]);
+        A[c] = cut ? 0.0f : A[c] * a[i][c];
+        fix(a[i][c]), fix(b[i][c]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
-    sm.A[s][wave][lane] = A;
-    sm.H[s][wave][lane] = H;
+#pragma unroll
+    for (int c = 0; c < C; ++c) sm.A[s][wave][lane * C + c] = A[c], sm.H[s][wave][lane * C + c] = H[c];
     if (threadIdx.x == 0) sm.item[s] = next;
     __syncthreads();
     next = __builtin_amdgcn_readfirstlane(sm.item[s]);
-    float Ap, Hp, end;
-    publish_map(k, p, s, wave, lane, A, H, Ap, Hp, sm);
-    const bool more = next < items;
+    float Ap[C], Hp[C], Aw[C], Hw[C], h[C], end[C];
+    publish_map<C>(k, p, s, wave, lane, A, H, Ap, Hp, Aw, Hw, sm);
+    const bool more = next < items;  // (else the loads below are of no tokens)
     Place q;
-    if (more) {
-      q.set<T, false>(k, next, wave, lane, g.L, g.D);
-      raw.load(g, q, lane);
-    }
-    float h = enter(k, p, wave, lane, A, H, Ap, Hp, init, end, sm);
+    q.set<T, C, false>(k, more ? next : item, more, wave, lane, g.L, g.D);
+    raw.load(g, q, lane);
+    enter<C>(k, p, wave, lane, Ap, Hp, Aw, Hw, init, h, end, sm);
 
     // the recurrence from the state that enters
     const Rows r_out(g.out, (size_t)p.row * stride, stride, p.n);
     const Rows r_st(g.states, (size_t)(p.bt * nst + p.t0 / kGatedStateChunk) * sstride, sstride,
                     (p.n + kGatedStateChunk - 1) / kGatedStateChunk);
     const int last_token = g.last && p.t0 + T >= g.L ? p.n - 1 : -1;
+    const Rows r_last(g.last, (size_t)p.bt * sstride, sstride, 1);
 #pragma unroll
     for (int i = 0; i < T; ++i) {
       const bool cut = HASR && ((reset >> i) & 1);
-      if (i % kGatedStateChunk == 0) put<float>(r_st, i / kGatedStateChunk, soff, h);
-      h = cut ? b[i] : __builtin_fmaf(a[i], h, b[i]);
+      if (i % kGatedStateChunk == 0) put_state<C>(r_st, i / kGatedStateChunk, soff, h);
       if (HASZ) fix(z[i]);
-      put<IO>(r_out, i, off, HASZ ? h * silu(value<IO>(z[i])) : h);
-      if (i == last_token) put<float>(Rows(g.last, (size_t)p.bt * sstride, sstride, 1), 0, soff, h);
+      float o[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        h[c] = cut ? b[i][c] : __builtin_fmaf(a[i][c], h[c], b[i][c]);
+        o[c] = HASZ ? h[c] * silu(value<C>(z[i], c)) : h[c];
+      }
+      put<IO, C>(r_out, i, off, o);
+      if (i == last_token) put_state<C>(r_last, 0, soff, h);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (!more) break;
@@ -385,15 +450,15 @@ struct BwdRaw {
         r_do(g.dout, skip, stride, p.n);
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-      ra[i] = fetch<IO>(r_ra, i, off);
-      rx[i] = fetch<IO>(r_rx, i, off);
-      u[i] = fetch<IO>(r_u, i, off);
-      dout[i] = fetch<IO>(r_do, i, off);
+      ra[i] = fetch<IO, 1>(r_ra, i, off);
+      rx[i] = fetch<IO, 1>(r_rx, i, off);
+      u[i] = fetch<IO, 1>(r_u, i, off);
+      dout[i] = fetch<IO, 1>(r_do, i, off);
     }
     if (HASZ) {
       const Rows r_z(f.z, skip, stride, p.n);
 #pragma unroll
-      for (int i = 0; i < T; ++i) z[i] = fetch<IO>(r_z, i, off);
+      for (int i = 0; i < T; ++i) z[i] = fetch<IO, 1>(r_z, i, off);
     }
     if (HASR) reset = (int)lane < p.n ? f.reset[p.row + lane] : 0;
     lam = f.lam[p.d];
@@ -407,16 +472,16 @@ template <typename IO, bool HASZ, bool HASR>
 __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdArgs g, Link k, float* pl) {
   constexpr int T = kTokB;
   const GatedArgs& f = g.f;
-  __shared__ ScanShared sm;
+  __shared__ ScanShared<1> sm;
   __shared__ float sums[2][kMaxWaves][64];
   const uint32_t lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const uint32_t items = (uint32_t)k.levels * (uint32_t)k.blocks;
   const uint32_t stride = (uint32_t)f.D * sizeof(IO), sstride = (uint32_t)f.D * 4;
-  uint32_t item = first_item(k, sm);
+  uint32_t item = first_item(k, &sm.item[1]);
   if (item >= items) return;
   Place p;
-  p.set<T, true>(k, item, wave, lane, f.L, f.D);
+  p.set<T, 1, true>(k, item, true, wave, lane, f.L, f.D);
   BwdRaw<IO, HASZ, HASR, T> raw;
   raw.load(g, p, lane);
   for (int s = 0;; s ^= 1) {
@@ -433,8 +498,8 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdAr
       const bool cut = HASR && ((reset >> i) & 1);
       fix(raw.ra[i]), fix(raw.rx[i]), fix(raw.u[i]), fix(raw.dout[i]);
       if (HASZ) fix(raw.z[i]);
-      const GatedGrad q = gated_grad(value<IO>(raw.ra[i]), value<IO>(raw.rx[i]), kappa, cut);
-      const float x = q.sx * value<IO>(raw.u[i]), b = q.s * x;
+      const GatedGrad q = gated_grad(value<1>(raw.ra[i], 0), value<1>(raw.rx[i], 0), kappa, cut);
+      const float x = q.sx * value<1>(raw.u[i], 0), b = q.s * x;
       const float ah = cut ? 0.0f : q.a * h;
       h = ah + b;
       a[i] = q.a;
@@ -442,40 +507,40 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdAr
       p2[i] = b * q.ox;
       e0[i] = __builtin_fmaf(ah, q.l, -q.q * x);
       oa[i] = q.oa;
-      dy[i] = value<IO>(raw.dout[i]);
+      dy[i] = value<1>(raw.dout[i], 0);
       if (HASZ) {
         float sz, dsz;
-        silu_pair(value<IO>(raw.z[i]), sz, dsz);
-        put<IO>(r_dz, i, off, dy[i] * h * dsz);
+        silu_pair(value<1>(raw.z[i], 0), sz, dsz);
+        put1<IO>(r_dz, i, off, dy[i] * h * dsz);
         dy[i] *= sz;
       }
       dy[i] += i == raw.last_token ? raw.dlast : 0.0f;
       fix(a[i]), fix(p1[i]), fix(p2[i]), fix(e0[i]), fix(oa[i]), fix(dy[i]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    float A = 1.0f, H = 0.0f;
+    float A[1] = {1.0f}, H[1] = {0.0f};
 #pragma unroll
     for (int i = T - 1; i >= 0; --i) {
       const bool cut = HASR && ((reset >> i) & 1);
-      H = cut ? 0.0f : a[i] * (dy[i] + H);
-      A = cut ? 0.0f : A * a[i];
+      H[0] = cut ? 0.0f : a[i] * (dy[i] + H[0]);
+      A[0] = cut ? 0.0f : A[0] * a[i];
     }
-    sm.A[s][wave][lane] = A;
-    sm.H[s][wave][lane] = H;
+    sm.A[s][wave][lane] = A[0];
+    sm.H[s][wave][lane] = H[0];
     if (threadIdx.x == 0) sm.item[s] = next;
     __syncthreads();
     next = __builtin_amdgcn_readfirstlane(sm.item[s]);
-    float Ap, Hp, end;
-    publish_map(k, p, s, wave, lane, A, H, Ap, Hp, sm);
-    const bool more = next < items;
+    float Ap[1], Hp[1], Aw[1], Hw[1], enter_at[1], end[1], sum = 0.0f;
+    const float zero[1] = {0.0f};
+    publish_map<1>(k, p, s, wave, lane, A, H, Ap, Hp, Aw, Hw, sm);
+    const bool more = next < items;  // (else the loads below are of no tokens)
     Place q;
-    if (more) {
-      q.set<T, true>(k, next, wave, lane, f.L, f.D);
-      raw.load(g, q, lane);
-    }
-    float cg = enter(k, p, wave, lane, A, H, Ap, Hp, 0.0f, end, sm), sum = 0.0f;
+    q.set<T, 1, true>(k, more ? next : item, more, wave, lane, f.L, f.D);
+    raw.load(g, q, lane);
+    enter<1>(k, p, wave, lane, Ap, Hp, Aw, Hw, zero, enter_at, end, sm);
     if (g.dh0 && p.level == k.levels - 1 && wave == waves - 1)
-      put<float>(Rows(g.dh0, (size_t)p.bt * sstride, sstride, 1), 0, soff, end);
+      put_state<1>(Rows(g.dh0, (size_t)p.bt * sstride, sstride, 1), 0, soff, end);
+    float cg = enter_at[0];
 
     // the way back from the gradient that enters
     const Rows r_du(g.du, (size_t)p.row * stride, stride, p.n), r_drx(g.drx, (size_t)p.row * stride, stride, p.n),
@@ -487,18 +552,18 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdAr
       const float e = cut ? 0.0f : G * e0[i];
       sum += e;
       cg = cut ? 0.0f : a[i] * G;
-      put<IO>(r_du, i, off, G * p1[i]);
-      put<IO>(r_drx, i, off, G * p2[i]);
-      put<IO>(r_dra, i, off, e * oa[i]);
+      put1<IO>(r_du, i, off, G * p1[i]);
+      put1<IO>(r_drx, i, off, G * p2[i]);
+      put1<IO>(r_dra, i, off, e * oa[i]);
       __builtin_amdgcn_sched_barrier(0);
     }
     sums[s][wave][lane] = sum;
     __syncthreads();
     if (wave == 0) {
-      float v = 0.0f;
+      float v[1] = {0.0f};
 #pragma unroll 1
-      for (int w = 0; w < waves; ++w) v += sums[s][w][lane];
-      put<float>(Rows(pl, (size_t)(p.bt * k.levels + p.level) * sstride, sstride, 1), 0, soff, v);
+      for (int w = 0; w < waves; ++w) v[0] += sums[s][w][lane];
+      put_state<1>(Rows(pl, (size_t)(p.bt * k.levels + p.level) * sstride, sstride, 1), 0, soff, v);
     }
     if (!more) break;
     p = q;
@@ -545,29 +610,40 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepArgs g) {
 
 size_t al256(size_t v) { return (v + 255) / 256 * 256; }
 
-// How a sequence is cut: levels of waves * tok tokens, blocks of 64 channels.
+// How a sequence is cut: levels of waves * tok tokens, blocks of 64 * vec channels.
 struct GatedPlan {
-  int waves, row_blocks;
+  int vec, waves, row_blocks;
   int64_t levels, blocks;
-  size_t words, off_end, off_map, bytes;  // workspace: the ticket, `end` and `map` words (none for one level)
+  size_t words, bytes;  // workspace: the ticket in 256 bytes, then the map's words (none for one level)
 };
 
-GatedPlan plan_gated(int64_t batch, int64_t L, int64_t D, int tok) {
+GatedPlan plan_gated(int64_t batch, int64_t L, int64_t D, int tok, int vec) {
   GatedPlan p{};
   if (batch == 0 || L == 0 || D == 0) return p;
-  p.row_blocks = (int)((D + 63) / 64);
+  p.vec = vec;
+  p.row_blocks = (int)((D + 64 * vec - 1) / (64 * vec));
   p.blocks = batch * p.row_blocks;
   const int64_t runs = (L + tok - 1) / tok;
   p.waves = (int)std::min<int64_t>(runs, kMaxWaves);
   p.levels = (runs + p.waves - 1) / p.waves;
   if (p.levels > 1) {
-    const size_t n = (size_t)p.levels * p.blocks * 64;
-    p.off_end = 256;
-    p.off_map = p.off_end + al256(n * 4);
-    p.bytes = p.off_map + al256(n * 8);
-    p.words = (p.bytes - p.off_end) / 4;
+    const size_t n = (size_t)p.levels * p.blocks * 64 * vec;
+    p.words = n * 2;
+    p.bytes = 256 + al256(n * 8);
   }
   return p;
+}
+
+// The forward's plan: pairs of bf16 channels where rows stay 4-byte aligned.
+GatedPlan plan_gated_fwd(int64_t batch, int64_t L, int64_t D, int io) {
+  return io == kIoBF16 && D % 2 == 0 ? plan_gated(batch, L, D, kTokF<2>, 2) : plan_gated(batch, L, D, kTokF<1>, 1);
+}
+
+Divisor divisor(int64_t d) {
+  Divisor r{0, 0};
+  while ((int64_t(1) << r.s) < d) ++r.s;
+  r.m = (uint32_t)((uint64_t(1) << (31 + r.s)) / (uint64_t)d + 1);
+  return r;
 }
 
 // Workgroups of a launch: as many as the chip holds (256 units of two; fewer waves, more
@@ -582,16 +658,17 @@ hipError_t prepare_link(const GatedPlan& p, void* ws, Link& k, hipStream_t st) {
   k.levels = (int)p.levels;
   k.blocks = (int)p.blocks;
   k.row_blocks = p.row_blocks;
+  k.by_blocks = divisor(p.blocks);
+  k.by_row = divisor(p.row_blocks);
   if (p.levels == 1) return hipSuccess;
   uint8_t* w = static_cast<uint8_t*>(ws);
   k.ticket = reinterpret_cast<uint32_t*>(w);
-  k.end = reinterpret_cast<uint32_t*>(w + p.off_end);
-  k.map = reinterpret_cast<unsigned long long*>(w + p.off_map);
+  k.map = reinterpret_cast<unsigned long long*>(w + 256);
   k.err = wait_status_ptr();
   if (k.err == nullptr) return hipErrorInvalidSymbol;
   k.spin_limit = (uint32_t)option(kOptSpinLimit);
   hipLaunchKernelGGL(gated_clear_kernel, dim3((unsigned)std::min<size_t>((p.words + 1023) / 1024, 4096)), dim3(256), 0,
-                     st, k.ticket, k.end, (int64_t)p.words);
+                     st, k.ticket, reinterpret_cast<uint32_t*>(w + 256), (int64_t)p.words);
   return hipGetLastError();
 }
 
@@ -599,27 +676,28 @@ size_t states_bytes(int64_t batch, int64_t L, int64_t D) {
   return al256((size_t)batch * ((L + kGatedStateChunk - 1) / kGatedStateChunk) * D * 4);
 }
 
-#define S6_PICK_GATED(name)                                                                \
-  template <typename IO>                                                                   \
-  auto* pick_##name(const void* z, const void* reset) {                                    \
-    return z ? (reset ? name##_kernel<IO, true, true> : name##_kernel<IO, true, false>)    \
-             : (reset ? name##_kernel<IO, false, true> : name##_kernel<IO, false, false>); \
-  }
-S6_PICK_GATED(gated_fwd)
-S6_PICK_GATED(gated_bwd)
-#undef S6_PICK_GATED
+template <typename IO, int C>
+auto* pick_fwd(const GatedArgs& a) {
+  return a.z ? (a.reset ? gated_fwd_kernel<IO, C, true, true> : gated_fwd_kernel<IO, C, true, false>)
+             : (a.reset ? gated_fwd_kernel<IO, C, false, true> : gated_fwd_kernel<IO, C, false, false>);
+}
+template <typename IO>
+auto* pick_bwd(const GatedArgs& a) {
+  return a.z ? (a.reset ? gated_bwd_kernel<IO, true, true> : gated_bwd_kernel<IO, true, false>)
+             : (a.reset ? gated_bwd_kernel<IO, false, true> : gated_bwd_kernel<IO, false, false>);
+}
 
 }  // namespace
 
 // Work items are counted in 32 bits.
 bool gated_fits(int64_t batch, int64_t L, int64_t D) {
-  const GatedPlan p = plan_gated(batch, L, D, kTokB);
+  const GatedPlan p = plan_gated(batch, L, D, kTokB, 1);
   return p.levels < (int64_t(1) << 31) && p.blocks < (int64_t(1) << 31) &&
          (double)p.levels * (double)p.blocks < 2147483648.0;
 }
 
-size_t gated_fwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int) {
-  return plan_gated(batch, L, D, kTokF).bytes;
+size_t gated_fwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int io) {
+  return plan_gated_fwd(batch, L, D, io).bytes;
 }
 
 hipError_t launch_gated_fwd(const GatedArgs& a, int io, void* ws, hipStream_t st) {
@@ -629,12 +707,12 @@ hipError_t launch_gated_fwd(const GatedArgs& a, int io, void* ws, hipStream_t st
                                    dim3(256), 0, st, a.h0, a.last, n);
     return hipGetLastError();
   }
-  const GatedPlan p = plan_gated(a.batch, a.L, a.D, kTokF);
+  const GatedPlan p = plan_gated_fwd(a.batch, a.L, a.D, io);
   Link k;
   const hipError_t e = prepare_link(p, ws, k, st);
   if (e != hipSuccess) return e;
   const dim3 grid(grid_of(p)), block(64 * p.waves);
-  auto* kernel = io == kIoBF16 ? pick_gated_fwd<uint16_t>(a.z, a.reset) : pick_gated_fwd<float>(a.z, a.reset);
+  auto* kernel = p.vec == 2 ? pick_fwd<uint16_t, 2>(a) : io == kIoBF16 ? pick_fwd<uint16_t, 1>(a) : pick_fwd<float, 1>(a);
   hipLaunchKernelGGL(kernel, grid, block, 0, st, a, k);
   return hipGetLastError();
 }
@@ -650,14 +728,14 @@ struct GatedBwdPlan {
   size_t off_sum, off_sum2, off_states, bytes;
 };
 
-GatedBwdPlan plan_gated_bwd(int64_t batch, int64_t L, int64_t D) {
+GatedBwdPlan plan_gated_bwd(int64_t batch, int64_t L, int64_t D, int io) {
   GatedBwdPlan p{};
   if (batch == 0 || D == 0 || L == 0) return p;
-  p.link = plan_gated(batch, L, D, kTokB);
+  p.link = plan_gated(batch, L, D, kTokB, 1);
   const int64_t n = batch * p.link.levels;
   p.rows = std::max<int64_t>(64, (n + 255) / 256);
   p.stages = (n + p.rows - 1) / p.rows;
-  p.off_sum = al256(std::max(p.link.bytes, plan_gated(batch, L, D, kTokF).bytes));
+  p.off_sum = al256(std::max(p.link.bytes, plan_gated_fwd(batch, L, D, io).bytes));
   p.off_sum2 = p.off_sum + al256((size_t)n * D * 4);
   p.off_states = p.off_sum2 + al256((size_t)p.stages * D * 4);
   p.bytes = p.off_states + states_bytes(batch, L, D);
@@ -678,14 +756,14 @@ hipError_t empty_bwd(const GatedBwdArgs& a, hipStream_t st) {
 
 }  // namespace
 
-size_t gated_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int) {
-  return plan_gated_bwd(batch, L, D).bytes;
+size_t gated_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int io) {
+  return plan_gated_bwd(batch, L, D, io).bytes;
 }
 
 hipError_t launch_gated_bwd(const GatedBwdArgs& a, int io, void* ws, hipStream_t st) {
   const GatedArgs& f = a.f;
   if (f.batch == 0 || f.L == 0) return empty_bwd(a, st);
-  const GatedBwdPlan p = plan_gated_bwd(f.batch, f.L, f.D);
+  const GatedBwdPlan p = plan_gated_bwd(f.batch, f.L, f.D, io);
   uint8_t* w = static_cast<uint8_t*>(ws);
   GatedBwdArgs g = a;
   hipError_t e;
@@ -703,7 +781,7 @@ hipError_t launch_gated_bwd(const GatedBwdArgs& a, int io, void* ws, hipStream_t
   float* pl = reinterpret_cast<float*>(w + p.off_sum);
   float* pl2 = reinterpret_cast<float*>(w + p.off_sum2);
   const dim3 grid(grid_of(p.link)), block(64 * p.link.waves);
-  auto* kernel = io == kIoBF16 ? pick_gated_bwd<uint16_t>(f.z, f.reset) : pick_gated_bwd<float>(f.z, f.reset);
+  auto* kernel = io == kIoBF16 ? pick_bwd<uint16_t>(f) : pick_bwd<float>(f);
   hipLaunchKernelGGL(kernel, grid, block, 0, st, g, k, pl);
   const int64_t n = f.batch * p.link.levels;
   const unsigned cols = (unsigned)((f.D + 63) / 64);

@@ -204,11 +204,14 @@ def test_gated_scan_empty_sequences():
     assert not g["dlam"].any()
 
 
-def test_gated_scan_repeats_bit_for_bit_on_another_stream():
+@pytest.mark.parametrize("shape", [(2, 3000, 264, "bf16"), (1, 60000, 64, "f32"), (3, 5000, 1500, "bf16")])
+def test_gated_scan_repeats_bit_for_bit_on_another_stream(shape):
+    """Few and many sequence chunks in flight: what a chunk finds published differs from run to run."""
     lib = _lib()
-    p, opt, dout, dlast = _gated_inputs(2, 3000, 264, "bf16", 13)
-    args, kw = _gated_dev(p, opt, "bf16")
-    dev = _dev(dout, "bf16")
+    io = shape[3]
+    p, opt, dout, dlast = _gated_inputs(*shape, 13, reset=0.001)
+    args, kw = _gated_dev(p, opt, io)
+    dev = _dev(dout, io)
 
     def both():
         out, last, states = lib.mamba_gated_scan_fwd(*args, **kw, return_states=True)
@@ -219,11 +222,29 @@ def test_gated_scan_repeats_bit_for_bit_on_another_stream():
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        again = [both() for _ in range(3)]
+        again = [both() for _ in range(12)]
     torch.cuda.current_stream().wait_stream(side)
     for a in again:
         for k in first:
             assert torch.equal(first[k], a[k]), k
+
+
+def test_gated_scan_reports_a_wait_that_gives_up():
+    """With no polls allowed a chunk gives up at once where its predecessor is not ready: then the call
+    reports it, and without a report the results are right."""
+    lib = _lib()
+    p, opt, _, _ = _gated_inputs(1, 20000, 64, "f32", 14, False, 0, False)
+    args, kw = _gated_dev(p, opt, "f32")
+    want, wlast = lib.mamba_gated_scan_fwd(*args, **kw, check=True)
+    with library_option(binding.MAMBA_OPT_SPIN_LIMIT, 0):
+        out, last = lib.mamba_gated_scan_fwd(*args, **kw)
+        status = binding.mamba_stream_status()
+    assert status in (0, binding.MAMBA_ERR_TIMEOUT)
+    same = torch.isnan(out) | (out == want)
+    assert same.all()
+    assert torch.isfinite(out).all() or status == binding.MAMBA_ERR_TIMEOUT
+    out, last = lib.mamba_gated_scan_fwd(*args, **kw, check=True)
+    assert torch.equal(out, want) and torch.equal(last, wlast)
 
 
 # ------------------------------------------------------------------------------------------ embedding
