@@ -12,18 +12,35 @@
 
 namespace s6 {
 
+// Two bf16 values in a word, the first in the low half (one instruction).
+__device__ __forceinline__ uint32_t f32x2_to_bf16(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
 // m = 1 - e^y for y <= 0, relative error about 2e-7:
 //   y > -0.35 : -y (1 + y/2 (1 + y/3 (1 + ... y/7))), truncation below 2e-8
 //   otherwise : 1 - e^y, cancellation below 2^-24 * 0.7 / 0.3
-__device__ __forceinline__ float one_minus_exp(float y) {
+// near: the caller knows the first to hold in the whole wave (kappa < 0.35 bounds -l, the
+// usual case: a channel that forgets within a few tokens is rare), which saves 6 of some
+// 40 instruction slots per element.
+constexpr float kNearExp = 0.35f;
+__device__ __forceinline__ float one_minus_exp(float y, bool near) {
   float p = __builtin_fmaf(y, 1.0f / 5040.0f, 1.0f / 720.0f);
   p = __builtin_fmaf(y, p, 1.0f / 120.0f);
   p = __builtin_fmaf(y, p, 1.0f / 24.0f);
   p = __builtin_fmaf(y, p, 1.0f / 6.0f);
   p = __builtin_fmaf(y, p, 0.5f);
   p = __builtin_fmaf(y, p, 1.0f);
-  const float far = 1.0f - ex2(y * kLog2e);
-  return y > -0.35f ? -y * p : far;
+  float m = -y * p;
+  if (!near) {
+    float far = 1.0f - ex2(y * kLog2e);
+    asm volatile("" : "+v"(far));  // a branch, not a select
+    m = y > -kNearExp ? m : far;
+  }
+  return m;
 }
 
 // sigma(v) and 1 - sigma(v), each to a few ulp relative; saturates without NaN.
@@ -34,9 +51,10 @@ __device__ __forceinline__ void sigmoid_pair(float v, float& sg, float& om) {
   om = e * sg;
 }
 
-// Decay and input of one token: h' = a h + b.
-__device__ __forceinline__ void gated_token(float ra, float rx, float u, float kappa, bool reset, float& a, float& b) {
-  const float m = one_minus_exp(-kappa * sigmoid(ra));
+// Decay and input of one token: h' = a h + b.  slow: kappa < kNearExp in the whole wave.
+__device__ __forceinline__ void gated_token(float ra, float rx, float u, float kappa, bool slow, bool reset, float& a,
+                                            float& b) {
+  const float m = one_minus_exp(-kappa * sigmoid(ra), slow);
   const float s = __builtin_amdgcn_sqrtf(m * (2.0f - m));
   const float x = sigmoid(rx) * u;
   a = reset ? 0.0f : 1.0f - m;
@@ -49,13 +67,13 @@ __device__ __forceinline__ void gated_token(float ra, float rx, float u, float k
 struct GatedGrad {
   float a, s, sx, ox, oa, l, q;
 };
-__device__ __forceinline__ GatedGrad gated_grad(float ra, float rx, float kappa, bool reset) {
+__device__ __forceinline__ GatedGrad gated_grad(float ra, float rx, float kappa, bool slow, bool reset) {
   GatedGrad g;
   float sa;
   sigmoid_pair(ra, sa, g.oa);
   sigmoid_pair(rx, g.sx, g.ox);
   const float l = -kappa * sa;
-  const float m = one_minus_exp(l);
+  const float m = one_minus_exp(l, slow);
   const float s2 = m * (2.0f - m);
   const float a = 1.0f - m;
   const float s = __builtin_amdgcn_sqrtf(s2);

@@ -47,8 +47,7 @@ __device__ __forceinline__ float value(uint32_t raw, int c) {
 }
 template <typename IO, int C>
 __device__ __forceinline__ void put(const Rows& w, int i, uint32_t off, const float (&v)[C]) {
-  if constexpr (C == 2)
-    __builtin_amdgcn_raw_buffer_store_b32(f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16, w.r, off, w.at(i), 0);
+  if constexpr (C == 2) __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16(v[0], v[1]), w.r, off, w.at(i), 0);
   else if constexpr (sizeof(IO) == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v[0]), w.r, off, w.at(i), 0);
   else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), w.r, off, w.at(i), 0);
 }
@@ -362,6 +361,10 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_fwd_kernel(GatedArgs 
     for (int c = 0; c < C; ++c)
       kappa[c] = g.c * softplus(raw.lam[c]), init[c] = raw.init[c], A[c] = 1.0f, H[c] = 0.0f;
     const uint32_t reset = HASR ? (uint32_t)__ballot(raw.reset != 0) : 0;
+    bool slow = true;
+#pragma unroll
+    for (int c = 0; c < C; ++c) slow &= kappa[c] < kNearExp;
+    slow = __all(slow);
     // Decays and inputs, and the run's map from zero.  A token past the end has loaded
     // zeros: it adds nothing, and no token after it is kept.
 #pragma unroll
@@ -370,11 +373,11 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_fwd_kernel(GatedArgs 
       fix(raw.ra[i]), fix(raw.rx[i]), fix(raw.u[i]);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        gated_token(value<C>(raw.ra[i], c), value<C>(raw.rx[i], c), value<C>(raw.u[i], c), kappa[c], cut, a[i][c],
-                    b[i][c]);
+        gated_token(value<C>(raw.ra[i], c), value<C>(raw.rx[i], c), value<C>(raw.u[i], c), kappa[c], slow, cut,
+                    a[i][c], b[i][c]);
+        fix(a[i][c]), fix(b[i][c]);
         H[c] = cut ? b[i][c] : __builtin_fmaf(a[i][c], H[c], b[i][c]);
         A[c] = cut ? 0.0f : A[c] * a[i][c];
-        fix(a[i][c]), fix(b[i][c]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -487,6 +490,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdAr
   for (int s = 0;; s ^= 1) {
     uint32_t next = request_item(k, item);
     const float kappa = f.c * softplus(raw.lam);
+    const bool slow = __all(kappa < kNearExp);
     const uint32_t reset = HASR ? (uint32_t)__ballot(raw.reset != 0) : 0;
     const Rows r_dz(g.dz, (size_t)p.row * stride, stride, p.n);
     const uint32_t off = bytes<IO>(p.off), soff = bytes<float>(p.off);
@@ -498,7 +502,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdAr
       const bool cut = HASR && ((reset >> i) & 1);
       fix(raw.ra[i]), fix(raw.rx[i]), fix(raw.u[i]), fix(raw.dout[i]);
       if (HASZ) fix(raw.z[i]);
-      const GatedGrad q = gated_grad(value<1>(raw.ra[i], 0), value<1>(raw.rx[i], 0), kappa, cut);
+      const GatedGrad q = gated_grad(value<1>(raw.ra[i], 0), value<1>(raw.rx[i], 0), kappa, slow, cut);
       const float x = q.sx * value<1>(raw.u[i], 0), b = q.s * x;
       const float ah = cut ? 0.0f : q.a * h;
       h = ah + b;
@@ -602,7 +606,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepArgs g) {
   const bool reset = g.reset && g.reset[bt] != 0;
   float a, b;
   gated_token(load_io((const IO*)g.ra, i), load_io((const IO*)g.rx, i), load_io((const IO*)g.u, i),
-              g.c * softplus(g.lam[d]), reset, a, b);
+              g.c * softplus(g.lam[d]), false, reset, a, b);
   const float h = reset ? b : __builtin_fmaf(a, g.state[i], b);
   g.state[i] = h;
   store_io((IO*)g.out, i, g.z ? h * silu(load_io((const IO*)g.z, i)) : h);
