@@ -43,6 +43,11 @@ __device__ __forceinline__ float one_minus_exp(float y, bool near) {
   return m;
 }
 
+// The decay e^y of a whole run from the sum y of its l (-inf after a reset: exactly 0).  A
+// product of the run's decays would lose the second-order terms that are below an ulp of 1,
+// all with the same sign, which a channel of long memory adds up over the sequence.
+__device__ __forceinline__ float run_decay(float y) { return 1.0f - one_minus_exp(y, false); }
+
 // sigma(v) and 1 - sigma(v), each to a few ulp relative; saturates without NaN.
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-v * kLog2e)); }
 __device__ __forceinline__ void sigmoid_pair(float v, float& sg, float& om) {
@@ -52,9 +57,11 @@ __device__ __forceinline__ void sigmoid_pair(float v, float& sg, float& om) {
 }
 
 // Decay and input of one token: h' = a h + b.  slow: kappa < kNearExp in the whole wave.
+// l: the decay's logarithm (not that of a reset).
 __device__ __forceinline__ void gated_token(float ra, float rx, float u, float kappa, bool slow, bool reset, float& a,
-                                            float& b) {
-  const float m = one_minus_exp(-kappa * sigmoid(ra), slow);
+                                            float& b, float& l) {
+  l = -kappa * sigmoid(ra);
+  const float m = one_minus_exp(l, slow);
   const float s = __builtin_amdgcn_sqrtf(m * (2.0f - m));
   const float x = sigmoid(rx) * u;
   a = reset ? 0.0f : 1.0f - m;
@@ -76,8 +83,9 @@ __device__ __forceinline__ GatedGrad gated_grad(float ra, float rx, float kappa,
   const float m = one_minus_exp(l, slow);
   const float s2 = m * (2.0f - m);
   const float a = 1.0f - m;
-  const float s = __builtin_amdgcn_sqrtf(s2);
-  const float q = s > 0.0f ? a * a * (l * rcp(s)) : 0.0f;
+  const float rs = __builtin_amdgcn_rsqf(fmaxf(s2, 1.0e-37f));  // l and s2 are 0 together, then so are s and q
+  const float s = s2 * rs;
+  const float q = a * a * (l * rs);
   g.a = reset ? 0.0f : a;
   g.s = reset ? 1.0f : s;
   g.l = reset ? 0.0f : l;

@@ -18,6 +18,7 @@ namespace {
 // and a store is dropped, with no branch around either.
 
 constexpr int kBufferDword3 = 0x00027000;   // raw, 32-bit data format
+constexpr int kStreamed = 2;                // non-temporal: every row is used once (2 to 4% of the time)
 constexpr uint32_t kNowhere = 0x80000000u;  // a lane offset beyond every resource here
 
 // One resource of n rows, row i by the scalar offset at(i).  A token past the end gets the
@@ -38,8 +39,8 @@ struct Rows {
 // C channels of one token as loaded, and as numbers.
 template <typename IO, int C>
 __device__ __forceinline__ uint32_t fetch(const Rows& w, int i, uint32_t off) {
-  if constexpr (sizeof(IO) * C == 2) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, off, w.at(i), 0) << 16;
-  else return __builtin_amdgcn_raw_buffer_load_b32(w.r, off, w.at(i), 0);
+  if constexpr (sizeof(IO) * C == 2) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, off, w.at(i), kStreamed) << 16;
+  else return __builtin_amdgcn_raw_buffer_load_b32(w.r, off, w.at(i), kStreamed);
 }
 template <int C>
 __device__ __forceinline__ float value(uint32_t raw, int c) {
@@ -47,9 +48,9 @@ __device__ __forceinline__ float value(uint32_t raw, int c) {
 }
 template <typename IO, int C>
 __device__ __forceinline__ void put(const Rows& w, int i, uint32_t off, const float (&v)[C]) {
-  if constexpr (C == 2) __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16(v[0], v[1]), w.r, off, w.at(i), 0);
-  else if constexpr (sizeof(IO) == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v[0]), w.r, off, w.at(i), 0);
-  else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), w.r, off, w.at(i), 0);
+  if constexpr (C == 2) __builtin_amdgcn_raw_buffer_store_b32(f32x2_to_bf16(v[0], v[1]), w.r, off, w.at(i), kStreamed);
+  else if constexpr (sizeof(IO) == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v[0]), w.r, off, w.at(i), kStreamed);
+  else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), w.r, off, w.at(i), kStreamed);
 }
 template <typename IO>
 __device__ __forceinline__ void put1(const Rows& w, int i, uint32_t off, float v) {
@@ -71,31 +72,35 @@ __device__ __forceinline__ void fix(V& v) { asm volatile("" : "+v"(v)); }
 
 // ---------------------------------------------------------------- the split over the sequence
 //
-// A workgroup takes work items of 64 channels and some tokens per wave (wave after wave).
+// A workgroup has W waves that compute (fewer for a short sequence) and one that keeps the
+// order.  It takes
+// work items of 64 * C channels and some tokens per computing wave (wave after wave).
 // Each wave scans its tokens from zero and leaves their affine map h -> A h + H in LDS.
-// The workgroup publishes the map of all its tokens, composes the maps of its
-// predecessors back to one that depends on nothing older, publishes its own end state as
-// such a map (A = 0) in the place of the first, and only then runs its recurrence from the
-// state that enters, from decays and inputs still in registers: every input is read once.
-// The loads of the next item are in flight during the look back and the recurrence of the
-// present one.
+// The other wave publishes the map of all of them, looks back at its predecessors' to one
+// that depends on nothing older, takes the state through them, publishes the end state as
+// such a map (A = 0) in the place of the first, and hands the state that enters to the
+// others, which run their recurrence from decays and inputs still in registers: every
+// input is read once.  Meanwhile the computing waves have the next item's loads in flight;
+// a wave's loads return in order, which is why one that looks back must not load.
 //
-// Which of the two a reader meets depends on timing, so maps are never composed with each
-// other: the state is taken through them one by one, oldest first, which gives the bits
-// that the chain of end states has wherever it starts.
+// Which of a level's two maps a reader meets depends on timing, so maps of levels are
+// never composed with each other: the state is taken through them one by one, oldest
+// first, which gives the bits that the chain of end states has wherever it starts.
 //
 // A published {A, H} is one 64-bit word and its own flag: the workspace starts as all
 // ones, and an A of all ones is a NaN that no publisher writes (its NaNs are replaced by
-// the standard one), so a reader needs no separate flag and no cache write-back.  Items are handed out by a
-// counter, level after level.  A workgroup holds one item that it works on and the next
-// one that it only loads; the unfinished item that was handed out first is one that its
-// holder works on (the holder's present item came before), and it waits for nothing
-// unfinished: every wait ends.
+// the standard one), so a reader needs no separate flag and no cache write-back.  Items
+// are handed out by a counter, level after level.  A workgroup holds one item that it
+// works on and the next one that it only loads; the unfinished item that was handed out
+// first is one that its holder works on (the holder's present item came before), and it
+// waits for nothing unfinished: every wait ends.
 // A decay of exactly 0 (a reset) drops the older state, whatever it is.
 
-constexpr int kMaxWaves = 8;
-constexpr int kRounds = 3;  // rounds of the look back in which every wave reads one predecessor
-constexpr int kDepth = 1 + kRounds * kMaxWaves;
+constexpr int kRead = 4;      // predecessors read at once
+// Predecessors looked back at; the last of them is waited for to its end.  Two channels a
+// lane is a plan of many blocks, so that few levels of one are in flight.
+template <int C>
+constexpr int kDepth = C == 2 ? 32 : 128;
 constexpr uint32_t kEmpty = 0xffffffffu;
 
 // x / d for x < 2^31 by a multiplication: m = floor(2^(31 + s) / d) + 1, 2^s >= d.
@@ -114,17 +119,47 @@ struct Link {
   Divisor by_blocks, by_row;
 };
 
-// Arrays that consecutive items write without a barrier between them are doubled.
-template <int C>
+template <int C, int W>
 struct ScanShared {
-  float A[2][kMaxWaves][64 * C], H[2][kMaxWaves][64 * C];  // the waves' maps
-  float backA[kDepth][64 * C], backH[kDepth][64 * C];      // the predecessors' maps, nearest first
-  uint32_t item[2];
+  float S[W][64 * C], A[W][64 * C], H[W][64 * C];  // the waves' log decays and maps
+  float in[64 * C];                                    // the state that enters the item
+  float backA[kDepth<C>][64 * C], backH[kDepth<C>][64 * C];  // the predecessors' maps, nearest first
+  uint32_t first, item;                                // the workgroup's first item, and its next one
 };
 
 __device__ __forceinline__ uint32_t published(float v) { return v != v ? 0x7fc00000u : __float_as_uint(v); }
-
 __device__ __forceinline__ float apply(float A, float H, float h) { return A == 0.0f ? H : __builtin_fmaf(A, h, H); }
+
+// (A, H) of the waves before `wave`, in order.
+template <int C, int W>
+__device__ __forceinline__ void maps_before(int wave, uint32_t lane, float (&A)[C], float (&H)[C],
+                                            const ScanShared<C, W>& sm) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) A[c] = 0.0f, H[c] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    if (w < wave) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        H[c] = apply(sm.A[w][lane * C + c], sm.H[w][lane * C + c], H[c]);
+        A[c] += sm.S[w][lane * C + c];
+      }
+    }
+#pragma unroll
+  for (int c = 0; c < C; ++c) A[c] = run_decay(A[c]);
+}
+
+// Leaves a wave's map in sm.
+template <int C, int W>
+__device__ __forceinline__ void leave_map(int wave, uint32_t lane, const float (&S)[C], const float (&H)[C],
+                                          ScanShared<C, W>& sm) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    sm.S[wave][lane * C + c] = S[c];
+    sm.A[wave][lane * C + c] = run_decay(S[c]);
+    sm.H[wave][lane * C + c] = H[c];
+  }
+}
 
 template <int C>
 __device__ __forceinline__ void read_map(const Link& k, int level, int blk, uint32_t lane, unsigned long long (&m)[C]) {
@@ -142,65 +177,60 @@ __device__ __forceinline__ void write_map(const Link& k, int level, int blk, uin
                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Brings the map of level e (-1: the initial state) into slot `to` of sm.  final: only a map
-// that depends on nothing older will do.
-template <int C>
-__device__ __forceinline__ void look_at(const Link& k, int e, int blk, uint32_t lane, const float (&init)[C],
-                                        bool final, int to, ScanShared<C>& sm) {
-  float A[C], H[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) A[c] = 0.0f, H[c] = init[c];
-  for (uint32_t polls = 0; e >= 0; ++polls) {
-    unsigned long long m[C];
-    read_map<C>(k, e, blk, lane, m);
-    bool there = true;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      A[c] = __uint_as_float((uint32_t)m[c]), H[c] = __uint_as_float((uint32_t)(m[c] >> 32));
-      there &= final ? A[c] == 0.0f : (uint32_t)m[c] != kEmpty;
-    }
-    if (__all(there)) break;
-    if (polls >= k.spin_limit) {  // never expected: report, and go on from NaN
-      if (lane == 0) __hip_atomic_store(k.err, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-      for (int c = 0; c < C; ++c) A[c] = 0.0f, H[c] = __uint_as_float(0x7fc00000u);
-      break;
-    }
-    __builtin_amdgcn_s_sleep(1);
-  }
-#pragma unroll
-  for (int c = 0; c < C; ++c) sm.backA[to][lane * C + c] = A[c], sm.backH[to][lane * C + c] = H[c];
-}
-
-// State entering `level` (> 0) of a block (init: the one entering level 0).  All waves
-// call.  The first wave looks at the nearest predecessor alone, which is all there is to
-// do unless many levels are in flight; then all waves look at one each, kRounds times, and
-// the last of these waits for an end state.
-template <int C>
-__device__ __forceinline__ void look_back(const Link& k, int level, int blk, int wave, uint32_t lane,
-                                          const float (&init)[C], float (&state)[C], ScanShared<C>& sm) {
+// State entering `level` of a block (state: the one entering level 0, on entry).
+template <int C, int W>
+__device__ __forceinline__ void look_back(const Link& k, int level, int blk, uint32_t lane, float (&state)[C],
+                                          ScanShared<C, W>& sm) {
   int slot = 0;
-  for (int lookers = 1;; lookers = blockDim.x >> 6) {
-    const bool last = slot + lookers + kMaxWaves > kDepth;
-    const int e = level - 1 - slot - wave;
-    if (wave < lookers && e >= -1) look_at<C>(k, e, blk, lane, init, last && wave == lookers - 1, slot + wave, sm);
-    __syncthreads();
-    const int end = slot + lookers < level + 1 ? slot + lookers : level + 1;
-    for (bool closed = false; slot < end && !closed; ++slot) {
-      closed = true;
+  bool closed = level == 0;
+  while (!closed) {
+    unsigned long long m[kRead][C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) closed &= sm.backA[slot][lane * C + c] == 0.0f;
-      closed = __all(closed);
+    for (int j = 0; j < kRead; ++j) {
+      const int e = level - 1 - slot - j;
+      read_map<C>(k, e > 0 ? e : 0, blk, lane, m[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kRead; ++j) {
+      const int e = level - 1 - slot;
+      if (closed) continue;
+      if (e < 0) {  // before level 0: the initial state
+        closed = true;
+        continue;
+      }
+      for (uint32_t polls = 0;; ++polls) {
+        bool there = true, end = true;
+#pragma unroll
+        for (int c = 0; c < C; ++c) there &= (uint32_t)m[j][c] != kEmpty, end &= __uint_as_float((uint32_t)m[j][c]) == 0.0f;
+        closed = __all(end);
+        if (closed || (__all(there) && slot + 1 < kDepth<C>)) break;
+        if (polls >= k.spin_limit) {  // never expected: report, and go on from NaN
+          if (lane == 0) __hip_atomic_store(k.err, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+          for (int c = 0; c < C; ++c) m[j][c] = 0x7fc0000000000000ull;
+          closed = true;
+          break;
+        }
+        __builtin_amdgcn_s_sleep(1);
+        read_map<C>(k, e, blk, lane, m[j]);
+      }
       if (closed) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) state[c] = sm.backH[slot][lane * C + c];
-        for (int j = slot - 1; j >= 0; --j) {
+        for (int c = 0; c < C; ++c) state[c] = __uint_as_float((uint32_t)(m[j][c] >> 32));
+      } else {
 #pragma unroll
-          for (int c = 0; c < C; ++c) state[c] = apply(sm.backA[j][lane * C + c], sm.backH[j][lane * C + c], state[c]);
+        for (int c = 0; c < C; ++c) {
+          sm.backA[slot][lane * C + c] = __uint_as_float((uint32_t)m[j][c]);
+          sm.backH[slot][lane * C + c] = __uint_as_float((uint32_t)(m[j][c] >> 32));
         }
-        return;
+        ++slot;
       }
     }
+  }
+#pragma unroll 8
+  for (int j = slot - 1; j >= 0; --j) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) state[c] = apply(sm.backA[j][lane * C + c], sm.backH[j][lane * C + c], state[c]);
   }
 }
 
@@ -214,7 +244,7 @@ struct Place {
   template <int T, int C, bool REVERSE>
   __device__ __forceinline__ void set(const Link& k, uint32_t item, bool real, int wave, uint32_t lane, int64_t L,
                                       int64_t D) {
-    const int waves = blockDim.x >> 6;
+    const int waves = (int)(blockDim.x >> 6) - 1;
     level = (int)k.by_blocks.of(item);
     blk = (int)(item - (uint32_t)level * (uint32_t)k.blocks);
     const uint32_t b = k.by_row.of((uint32_t)blk);
@@ -235,63 +265,62 @@ struct Place {
 template <typename IO>
 __device__ __forceinline__ uint32_t bytes(uint32_t off) { return off == kNowhere ? kNowhere : off * (uint32_t)sizeof(IO); }
 
-// The workgroup's first item, and its request for the next (thread 0's answer is stored
-// into sm.item before the barrier of the waves' maps).
-__device__ __forceinline__ uint32_t first_item(const Link& k, uint32_t* shared_item) {
-  if (k.levels == 1) return blockIdx.x;
-  if (threadIdx.x == 0) *shared_item = atomicAdd(k.ticket, 1u);
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane(*shared_item);
-}
-__device__ __forceinline__ uint32_t request_item(const Link& k, uint32_t item) {
-  if (k.levels == 1) return item + gridDim.x;
-  return threadIdx.x == 0 ? atomicAdd(k.ticket, 1u) : 0u;
+// The items of a workgroup, one after the other (one level: from the grid, no order).
+__device__ __forceinline__ uint32_t take_item(const Link& k, uint32_t item) {
+  if (k.levels == 1) return item == kEmpty ? blockIdx.x : item + gridDim.x;
+  const uint32_t t = (threadIdx.x & 63) == 0 ? atomicAdd(k.ticket, 1u) : 0u;
+  return __builtin_amdgcn_readfirstlane(t);
 }
 
-// The map (Ap, Hp) of the waves before this one, in slot s of sm, and of this one with them
-// (Aw, Hw): in the last wave the level's map, which it publishes.
-template <int C>
-__device__ __forceinline__ void publish_map(const Link& k, const Place& p, int s, int wave, uint32_t lane,
-                                            const float (&A)[C], const float (&H)[C], float (&Ap)[C], float (&Hp)[C],
-                                            float (&Aw)[C], float (&Hw)[C], const ScanShared<C>& sm) {
-#pragma unroll
-  for (int c = 0; c < C; ++c) Ap[c] = 1.0f, Hp[c] = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kMaxWaves - 1; ++w)
-    if (w < wave) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float a = sm.A[s][w][lane * C + c];
-        Hp[c] = apply(a, sm.H[s][w][lane * C + c], Hp[c]);
-        Ap[c] = a == 0.0f ? 0.0f : Ap[c] * a;
-      }
+// The order-keeping wave's part, item after item.  init: (batch, D) states entering level 0,
+// or null (zero); end_state: (batch, D) states leaving the last level, or null.  SUMS: after
+// each item, the sum over the waves of each lane's value in sums goes to pl.
+template <typename IO, int T, int C, int W, bool REVERSE, bool SUMS>
+__device__ __forceinline__ void keep_order(const Link& k, uint32_t item, uint32_t lane, int64_t L, int64_t D,
+                                           const float* init, float* end_state, float* pl, const float (*sums)[64],
+                                           ScanShared<C, W>& sm) {
+  const int waves = (int)(blockDim.x >> 6) - 1;
+  const uint32_t items = (uint32_t)k.levels * (uint32_t)k.blocks, sstride = (uint32_t)D * 4;
+  uint32_t last_off = kNowhere;
+  size_t last_row = 0;
+  bool more = true, first = true;
+  while (true) {
+    const uint32_t next = more ? take_item(k, item) : kEmpty;
+    Place p;
+    if (more) {
+      p.set<T, C, REVERSE>(k, item, true, 0, lane, L, D);
+      if (lane == 0) sm.item = next;
     }
+    float state[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) Aw[c] = A[c] == 0.0f ? 0.0f : Ap[c] * A[c], Hw[c] = apply(A[c], H[c], Hp[c]);
-  if (wave == (int)(blockDim.x >> 6) - 1 && p.level > 0 && p.level + 1 < k.levels)
-    write_map<C>(k, p.level, p.blk, lane, Aw, Hw);
-}
-
-// State entering the wave's tokens (from init at level 0); the last wave publishes the
-// level's end state and has it in `end`.
-template <int C>
-__device__ __forceinline__ void enter(const Link& k, const Place& p, int wave, uint32_t lane, const float (&Ap)[C],
-                                      const float (&Hp)[C], const float (&Aw)[C], const float (&Hw)[C],
-                                      const float (&init)[C], float (&carry)[C], float (&end)[C], ScanShared<C>& sm) {
-  float in[C];
+    for (int c = 0; c < C; ++c) state[c] = more && init && p.level == 0 ? init[p.bt * D + p.d + c] : 0.0f;
+    __syncthreads();  // the waves' maps, and the sums of the item before
+    if (SUMS && !first) {
+      float v = 0.0f;
+      for (int w = 0; w < waves; ++w) v += sums[w][lane];
+      const float vs[1] = {v};
+      put_state<1>(Rows(pl, last_row * sstride, sstride, 1), 0, last_off, vs);
+    }
+    if (!more) return;
+    float A[C], H[C];
+    maps_before<C, W>(waves, lane, A, H, sm);
+    if (p.level > 0 && p.level + 1 < k.levels) write_map<C>(k, p.level, p.blk, lane, A, H);
+    look_back<C, W>(k, p.level, p.blk, lane, state, sm);
+    float end[C], none[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) in[c] = init[c];
-  if (p.level > 0) look_back<C>(k, p.level, p.blk, wave, lane, init, in, sm);
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    carry[c] = apply(Ap[c], Hp[c], in[c]);
-    end[c] = apply(Aw[c], Hw[c], in[c]);  // the bits that a reader of the level's map gets
-  }
-  if (wave == (int)(blockDim.x >> 6) - 1 && p.level + 1 < k.levels) {
-    float none[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) none[c] = 0.0f;
-    write_map<C>(k, p.level, p.blk, lane, none, end);
+    for (int c = 0; c < C; ++c) {
+      sm.in[lane * C + c] = state[c];
+      end[c] = apply(A[c], H[c], state[c]);  // the bits that a reader of the level's map gets
+      none[c] = 0.0f;
+    }
+    if (p.level + 1 < k.levels) write_map<C>(k, p.level, p.blk, lane, none, end);
+    else if (end_state) put_state<C>(Rows(end_state, (size_t)p.bt * sstride, sstride, 1), 0, bytes<float>(p.off), end);
+    __syncthreads();  // the state that enters
+    first = false;
+    if (SUMS) last_row = (size_t)(p.bt * k.levels + p.level), last_off = bytes<float>(p.off);
+    more = next < items;
+    if (!more && !SUMS) return;
+    item = next;
   }
 }
 
@@ -307,12 +336,13 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(uint32_t* ticket, uint
 // raw values beside them) is what 128 registers hold.
 template <int C>
 constexpr int kTokF = 16 / C;
+constexpr int kWavesF = 15;  // computing waves
 
 // A run as loaded (z, which is needed last, is loaded when the run's turn comes).
 template <typename IO, int C, bool HASR, int T>
 struct FwdRaw {
   uint32_t ra[T], rx[T], u[T], reset;
-  float lam[C], init[C];
+  float lam[C];
   __device__ __forceinline__ void load(const GatedArgs& g, const Place& p, uint32_t lane) {
     const uint32_t stride = (uint32_t)g.D * sizeof(IO), off = bytes<IO>(p.off);
     const size_t skip = (size_t)p.row * stride;
@@ -325,30 +355,35 @@ struct FwdRaw {
     }
     if (HASR) reset = (int)lane < p.n ? g.reset[p.row + lane] : 0;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      lam[c] = g.lam[p.d + c];
-      init[c] = g.h0 && p.level == 0 ? g.h0[p.bt * g.D + p.d + c] : 0.0f;
-    }
+    for (int c = 0; c < C; ++c) lam[c] = g.lam[p.d + c];
   }
 };
 
 template <typename IO, int C, bool HASZ, bool HASR>
-__global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_fwd_kernel(GatedArgs g, Link k) {
-  constexpr int T = kTokF<C>;
-  __shared__ ScanShared<C> sm;
+__global__ __launch_bounds__(64 * (kWavesF + 1), 4) void gated_fwd_kernel(GatedArgs g, Link k) {
+  constexpr int T = kTokF<C>, W = kWavesF;
+  __shared__ ScanShared<C, W> sm;
   const uint32_t lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = (int)(blockDim.x >> 6) - 1;
   const uint32_t items = (uint32_t)k.levels * (uint32_t)k.blocks;
+  if (wave == waves) {
+    const uint32_t first = take_item(k, kEmpty);
+    if (lane == 0) sm.first = first;
+  }
+  __syncthreads();
+  uint32_t item = __builtin_amdgcn_readfirstlane(sm.first);
+  if (item >= items) return;
+  if (wave == waves) {
+    keep_order<IO, T, C, W, false, false>(k, item, lane, g.L, g.D, g.h0, nullptr, nullptr, nullptr, sm);
+    return;
+  }
   const int64_t nst = (g.L + kGatedStateChunk - 1) / kGatedStateChunk;
   const uint32_t stride = (uint32_t)g.D * sizeof(IO), sstride = (uint32_t)g.D * 4;
-  uint32_t item = first_item(k, &sm.item[1]);
-  if (item >= items) return;
   Place p;
   p.set<T, C, false>(k, item, true, wave, lane, g.L, g.D);
   FwdRaw<IO, C, HASR, T> raw;
   raw.load(g, p, lane);
-  for (int s = 0;; s ^= 1) {
-    uint32_t next = request_item(k, item);
+  while (true) {
     const uint32_t off = bytes<IO>(p.off), soff = bytes<float>(p.off);
     uint32_t z[T];
     if (HASZ) {
@@ -356,15 +391,16 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_fwd_kernel(GatedArgs 
 #pragma unroll
       for (int i = 0; i < T; ++i) z[i] = fetch<IO, C>(r_z, i, off);
     }
-    float kappa[C], init[C], A[C], H[C], a[T][C], b[T][C];
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      kappa[c] = g.c * softplus(raw.lam[c]), init[c] = raw.init[c], A[c] = 1.0f, H[c] = 0.0f;
-    const uint32_t reset = HASR ? (uint32_t)__ballot(raw.reset != 0) : 0;
+    float kappa[C], S[C], H[C], a[T][C], b[T][C];
     bool slow = true;
 #pragma unroll
-    for (int c = 0; c < C; ++c) slow &= kappa[c] < kNearExp;
+    for (int c = 0; c < C; ++c) {
+      kappa[c] = g.c * softplus(raw.lam[c]);
+      slow &= kappa[c] < kNearExp;
+      S[c] = 0.0f, H[c] = 0.0f;
+    }
     slow = __all(slow);
+    const uint32_t reset = HASR ? (uint32_t)__ballot(raw.reset != 0) : 0;
     // Decays and inputs, and the run's map from zero.  A token past the end has loaded
     // zeros: it adds nothing, and no token after it is kept.
 #pragma unroll
@@ -373,26 +409,27 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_fwd_kernel(GatedArgs 
       fix(raw.ra[i]), fix(raw.rx[i]), fix(raw.u[i]);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
+        float l;
         gated_token(value<C>(raw.ra[i], c), value<C>(raw.rx[i], c), value<C>(raw.u[i], c), kappa[c], slow, cut,
-                    a[i][c], b[i][c]);
+                    a[i][c], b[i][c], l);
         fix(a[i][c]), fix(b[i][c]);
         H[c] = cut ? b[i][c] : __builtin_fmaf(a[i][c], H[c], b[i][c]);
-        A[c] = cut ? 0.0f : A[c] * a[i][c];
+        S[c] = cut ? -__builtin_inff() : S[c] + l;
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c) sm.A[s][wave][lane * C + c] = A[c], sm.H[s][wave][lane * C + c] = H[c];
-    if (threadIdx.x == 0) sm.item[s] = next;
+    leave_map<C, W>(wave, lane, S, H, sm);
     __syncthreads();
-    next = __builtin_amdgcn_readfirstlane(sm.item[s]);
-    float Ap[C], Hp[C], Aw[C], Hw[C], h[C], end[C];
-    publish_map<C>(k, p, s, wave, lane, A, H, Ap, Hp, Aw, Hw, sm);
+    const uint32_t next = __builtin_amdgcn_readfirstlane(sm.item);
     const bool more = next < items;  // (else the loads below are of no tokens)
     Place q;
     q.set<T, C, false>(k, more ? next : item, more, wave, lane, g.L, g.D);
     raw.load(g, q, lane);
-    enter<C>(k, p, wave, lane, Ap, Hp, Aw, Hw, init, h, end, sm);
+    float Ap[C], Hp[C], h[C];
+    maps_before<C, W>(wave, lane, Ap, Hp, sm);
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < C; ++c) h[c] = apply(Ap[c], Hp[c], sm.in[lane * C + c]);
 
     // the recurrence from the state that enters
     const Rows r_out(g.out, (size_t)p.row * stride, stride, p.n);
@@ -415,7 +452,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_fwd_kernel(GatedArgs 
       if (i == last_token) put_state<C>(r_last, 0, soff, h);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (!more) break;
+    if (!more) return;
     p = q;
     item = next;
   }
@@ -439,6 +476,12 @@ __global__ __launch_bounds__(256) void gated_copy_state_kernel(const float* h0, 
 //   dgate_a = e (1 - sa),  dlam = dlam_factor * sum e.
 
 constexpr int kTokB = kGatedStateChunk;  // tokens per wave
+// Computing waves: two workgroups of 7 share a compute unit, which overlaps them better
+// where there are blocks enough ((8, 2048, 1536) bf16, 192 blocks: 128 us against 137 with
+// one of 15).  With few blocks more levels of one are in flight, and longer levels mean
+// less looking back ((3, 1537, 1101) fp32, 54 blocks: 48 us with 15 and 56 with 7).
+constexpr int kWavesB = 7, kWavesBFew = 15;
+constexpr int64_t kFewBlocks = 128;
 
 template <typename IO, bool HASZ, bool HASR, int T>
 struct BwdRaw {
@@ -471,32 +514,40 @@ struct BwdRaw {
   }
 };
 
-template <typename IO, bool HASZ, bool HASR>
-__global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdArgs g, Link k, float* pl) {
+template <typename IO, int W, bool HASZ, bool HASR>
+__global__ __launch_bounds__(64 * (W + 1), 4) void gated_bwd_kernel(GatedBwdArgs g, Link k, float* pl) {
   constexpr int T = kTokB;
   const GatedArgs& f = g.f;
-  __shared__ ScanShared<1> sm;
-  __shared__ float sums[2][kMaxWaves][64];
+  __shared__ ScanShared<1, W> sm;
+  __shared__ float sums[W][64];
   const uint32_t lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = (int)(blockDim.x >> 6) - 1;
   const uint32_t items = (uint32_t)k.levels * (uint32_t)k.blocks;
-  const uint32_t stride = (uint32_t)f.D * sizeof(IO), sstride = (uint32_t)f.D * 4;
-  uint32_t item = first_item(k, &sm.item[1]);
+  if (wave == waves) {
+    const uint32_t first = take_item(k, kEmpty);
+    if (lane == 0) sm.first = first;
+  }
+  __syncthreads();
+  uint32_t item = __builtin_amdgcn_readfirstlane(sm.first);
   if (item >= items) return;
+  if (wave == waves) {
+    keep_order<IO, T, 1, W, true, true>(k, item, lane, f.L, f.D, nullptr, g.dh0, pl, sums, sm);
+    return;
+  }
+  const uint32_t stride = (uint32_t)f.D * sizeof(IO);
   Place p;
   p.set<T, 1, true>(k, item, true, wave, lane, f.L, f.D);
   BwdRaw<IO, HASZ, HASR, T> raw;
   raw.load(g, p, lane);
-  for (int s = 0;; s ^= 1) {
-    uint32_t next = request_item(k, item);
+  while (true) {
     const float kappa = f.c * softplus(raw.lam);
     const bool slow = __all(kappa < kNearExp);
     const uint32_t reset = HASR ? (uint32_t)__ballot(raw.reset != 0) : 0;
     const Rows r_dz(g.dz, (size_t)p.row * stride, stride, p.n);
-    const uint32_t off = bytes<IO>(p.off), soff = bytes<float>(p.off);
+    const uint32_t off = bytes<IO>(p.off);
     // The way forward.  A token past the end has loaded zeros: its gradient is 0 and
     // stays 0 up to the last token, where dlast enters.
-    float a[T], dy[T], p1[T], p2[T], e0[T], oa[T], h = raw.h;
+    float a[T], dy[T], p1[T], p2[T], e0[T], oa[T], h = raw.h, S[1] = {0.0f}, H[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < T; ++i) {
       const bool cut = HASR && ((reset >> i) & 1);
@@ -511,6 +562,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdAr
       p2[i] = b * q.ox;
       e0[i] = __builtin_fmaf(ah, q.l, -q.q * x);
       oa[i] = q.oa;
+      S[0] = cut ? -__builtin_inff() : S[0] + q.l;
       dy[i] = value<1>(raw.dout[i], 0);
       if (HASZ) {
         float sz, dsz;
@@ -518,33 +570,29 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdAr
         put1<IO>(r_dz, i, off, dy[i] * h * dsz);
         dy[i] *= sz;
       }
-      dy[i] += i == raw.last_token ? raw.dlast : 0.0f;
       fix(a[i]), fix(p1[i]), fix(p2[i]), fix(e0[i]), fix(oa[i]), fix(dy[i]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    float A[1] = {1.0f}, H[1] = {0.0f};
+    if (raw.last_token >= 0) {
+#pragma unroll
+      for (int i = 0; i < T; ++i) dy[i] += i == raw.last_token ? raw.dlast : 0.0f;
+    }
 #pragma unroll
     for (int i = T - 1; i >= 0; --i) {
       const bool cut = HASR && ((reset >> i) & 1);
       H[0] = cut ? 0.0f : a[i] * (dy[i] + H[0]);
-      A[0] = cut ? 0.0f : A[0] * a[i];
     }
-    sm.A[s][wave][lane] = A[0];
-    sm.H[s][wave][lane] = H[0];
-    if (threadIdx.x == 0) sm.item[s] = next;
+    leave_map<1, W>(wave, lane, S, H, sm);
     __syncthreads();
-    next = __builtin_amdgcn_readfirstlane(sm.item[s]);
-    float Ap[1], Hp[1], Aw[1], Hw[1], enter_at[1], end[1], sum = 0.0f;
-    const float zero[1] = {0.0f};
-    publish_map<1>(k, p, s, wave, lane, A, H, Ap, Hp, Aw, Hw, sm);
+    const uint32_t next = __builtin_amdgcn_readfirstlane(sm.item);
     const bool more = next < items;  // (else the loads below are of no tokens)
     Place q;
     q.set<T, 1, true>(k, more ? next : item, more, wave, lane, f.L, f.D);
     raw.load(g, q, lane);
-    enter<1>(k, p, wave, lane, Ap, Hp, Aw, Hw, zero, enter_at, end, sm);
-    if (g.dh0 && p.level == k.levels - 1 && wave == waves - 1)
-      put_state<1>(Rows(g.dh0, (size_t)p.bt * sstride, sstride, 1), 0, soff, end);
-    float cg = enter_at[0];
+    float Ap[1], Hp[1];
+    maps_before<1, W>(wave, lane, Ap, Hp, sm);
+    __syncthreads();
+    float cg = apply(Ap[0], Hp[0], sm.in[lane]), sum = 0.0f;
 
     // the way back from the gradient that enters
     const Rows r_du(g.du, (size_t)p.row * stride, stride, p.n), r_drx(g.drx, (size_t)p.row * stride, stride, p.n),
@@ -561,18 +609,12 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void gated_bwd_kernel(GatedBwdAr
       put1<IO>(r_dra, i, off, e * oa[i]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    sums[s][wave][lane] = sum;
-    __syncthreads();
-    if (wave == 0) {
-      float v[1] = {0.0f};
-#pragma unroll 1
-      for (int w = 0; w < waves; ++w) v[0] += sums[s][w][lane];
-      put_state<1>(Rows(pl, (size_t)(p.bt * k.levels + p.level) * sstride, sstride, 1), 0, soff, v);
-    }
+    sums[wave][lane] = sum;
     if (!more) break;
     p = q;
     item = next;
   }
+  __syncthreads();  // the order-keeping wave adds the last sums
 }
 
 // Column sums of `rows` consecutive rows of in (n, D) per blockIdx.y, each of four waves
@@ -604,9 +646,9 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepArgs g) {
   if (d >= g.D) return;
   const size_t i = (size_t)bt * g.D + d;
   const bool reset = g.reset && g.reset[bt] != 0;
-  float a, b;
+  float a, b, l;
   gated_token(load_io((const IO*)g.ra, i), load_io((const IO*)g.rx, i), load_io((const IO*)g.u, i),
-              g.c * softplus(g.lam[d]), false, reset, a, b);
+              g.c * softplus(g.lam[d]), false, reset, a, b, l);
   const float h = reset ? b : __builtin_fmaf(a, g.state[i], b);
   g.state[i] = h;
   store_io((IO*)g.out, i, g.z ? h * silu(load_io((const IO*)g.z, i)) : h);
@@ -614,21 +656,21 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepArgs g) {
 
 size_t al256(size_t v) { return (v + 255) / 256 * 256; }
 
-// How a sequence is cut: levels of waves * tok tokens, blocks of 64 * vec channels.
+// How a sequence is cut: levels of waves * tok tokens (`waves` computing ones), blocks of 64 * vec channels.
 struct GatedPlan {
   int vec, waves, row_blocks;
   int64_t levels, blocks;
   size_t words, bytes;  // workspace: the ticket in 256 bytes, then the map's words (none for one level)
 };
 
-GatedPlan plan_gated(int64_t batch, int64_t L, int64_t D, int tok, int vec) {
+GatedPlan plan_gated(int64_t batch, int64_t L, int64_t D, int tok, int vec, int waves) {
   GatedPlan p{};
   if (batch == 0 || L == 0 || D == 0) return p;
   p.vec = vec;
   p.row_blocks = (int)((D + 64 * vec - 1) / (64 * vec));
   p.blocks = batch * p.row_blocks;
   const int64_t runs = (L + tok - 1) / tok;
-  p.waves = (int)std::min<int64_t>(runs, kMaxWaves);
+  p.waves = (int)std::min<int64_t>(runs, waves);
   p.levels = (runs + p.waves - 1) / p.waves;
   if (p.levels > 1) {
     const size_t n = (size_t)p.levels * p.blocks * 64 * vec;
@@ -638,9 +680,16 @@ GatedPlan plan_gated(int64_t batch, int64_t L, int64_t D, int tok, int vec) {
   return p;
 }
 
-// The forward's plan: pairs of bf16 channels where rows stay 4-byte aligned.
+// The forward's plan: pairs of bf16 channels where rows stay 4-byte aligned and there are
+// blocks enough that few levels of one are in flight (the look back is shallower there).
 GatedPlan plan_gated_fwd(int64_t batch, int64_t L, int64_t D, int io) {
-  return io == kIoBF16 && D % 2 == 0 ? plan_gated(batch, L, D, kTokF<2>, 2) : plan_gated(batch, L, D, kTokF<1>, 1);
+  const GatedPlan two = plan_gated(batch, L, D, kTokF<2>, 2, kWavesF);
+  return io == kIoBF16 && D % 2 == 0 && two.blocks >= 64 ? two : plan_gated(batch, L, D, kTokF<1>, 1, kWavesF);
+}
+
+GatedPlan plan_gated_bwd_link(int64_t batch, int64_t L, int64_t D) {
+  const GatedPlan p = plan_gated(batch, L, D, kTokB, 1, kWavesB);
+  return p.blocks < kFewBlocks ? plan_gated(batch, L, D, kTokB, 1, kWavesBFew) : p;
 }
 
 Divisor divisor(int64_t d) {
@@ -650,10 +699,10 @@ Divisor divisor(int64_t d) {
   return r;
 }
 
-// Workgroups of a launch: as many as the chip holds (256 units of two; fewer waves, more
-// workgroups), each going from item to item.
+// Workgroups of a launch: as many as the chip's 256 compute units hold (more where they
+// have fewer waves), each going from item to item.
 unsigned grid_of(const GatedPlan& p) {
-  return (unsigned)std::min<int64_t>(p.levels * p.blocks, 512 * kMaxWaves / p.waves);
+  return (unsigned)std::min<int64_t>(p.levels * p.blocks, 256 * 16 / (p.waves + 1));
 }
 
 // The link of a launch: clears the workspace's words (one level: nothing).
@@ -685,17 +734,17 @@ auto* pick_fwd(const GatedArgs& a) {
   return a.z ? (a.reset ? gated_fwd_kernel<IO, C, true, true> : gated_fwd_kernel<IO, C, true, false>)
              : (a.reset ? gated_fwd_kernel<IO, C, false, true> : gated_fwd_kernel<IO, C, false, false>);
 }
-template <typename IO>
+template <typename IO, int W>
 auto* pick_bwd(const GatedArgs& a) {
-  return a.z ? (a.reset ? gated_bwd_kernel<IO, true, true> : gated_bwd_kernel<IO, true, false>)
-             : (a.reset ? gated_bwd_kernel<IO, false, true> : gated_bwd_kernel<IO, false, false>);
+  return a.z ? (a.reset ? gated_bwd_kernel<IO, W, true, true> : gated_bwd_kernel<IO, W, true, false>)
+             : (a.reset ? gated_bwd_kernel<IO, W, false, true> : gated_bwd_kernel<IO, W, false, false>);
 }
 
 }  // namespace
 
 // Work items are counted in 32 bits.
 bool gated_fits(int64_t batch, int64_t L, int64_t D) {
-  const GatedPlan p = plan_gated(batch, L, D, kTokB, 1);
+  const GatedPlan p = plan_gated(batch, L, D, kTokB, 1, kWavesB);
   return p.levels < (int64_t(1) << 31) && p.blocks < (int64_t(1) << 31) &&
          (double)p.levels * (double)p.blocks < 2147483648.0;
 }
@@ -715,7 +764,7 @@ hipError_t launch_gated_fwd(const GatedArgs& a, int io, void* ws, hipStream_t st
   Link k;
   const hipError_t e = prepare_link(p, ws, k, st);
   if (e != hipSuccess) return e;
-  const dim3 grid(grid_of(p)), block(64 * p.waves);
+  const dim3 grid(grid_of(p)), block(64 * (p.waves + 1));
   auto* kernel = p.vec == 2 ? pick_fwd<uint16_t, 2>(a) : io == kIoBF16 ? pick_fwd<uint16_t, 1>(a) : pick_fwd<float, 1>(a);
   hipLaunchKernelGGL(kernel, grid, block, 0, st, a, k);
   return hipGetLastError();
@@ -735,7 +784,7 @@ struct GatedBwdPlan {
 GatedBwdPlan plan_gated_bwd(int64_t batch, int64_t L, int64_t D, int io) {
   GatedBwdPlan p{};
   if (batch == 0 || D == 0 || L == 0) return p;
-  p.link = plan_gated(batch, L, D, kTokB, 1);
+  p.link = plan_gated_bwd_link(batch, L, D);
   const int64_t n = batch * p.link.levels;
   p.rows = std::max<int64_t>(64, (n + 255) / 256);
   p.stages = (n + p.rows - 1) / p.rows;
@@ -784,8 +833,10 @@ hipError_t launch_gated_bwd(const GatedBwdArgs& a, int io, void* ws, hipStream_t
   if ((e = prepare_link(p.link, ws, k, st)) != hipSuccess) return e;
   float* pl = reinterpret_cast<float*>(w + p.off_sum);
   float* pl2 = reinterpret_cast<float*>(w + p.off_sum2);
-  const dim3 grid(grid_of(p.link)), block(64 * p.link.waves);
-  auto* kernel = io == kIoBF16 ? pick_bwd<uint16_t>(f) : pick_bwd<float>(f);
+  const dim3 grid(grid_of(p.link)), block(64 * (p.link.waves + 1));
+  const bool few = p.link.blocks < kFewBlocks;
+  auto* kernel = io == kIoBF16 ? (few ? pick_bwd<uint16_t, kWavesBFew>(f) : pick_bwd<uint16_t, kWavesB>(f))
+                               : (few ? pick_bwd<float, kWavesBFew>(f) : pick_bwd<float, kWavesB>(f));
   hipLaunchKernelGGL(kernel, grid, block, 0, st, g, k, pl);
   const int64_t n = f.batch * p.link.levels;
   const unsigned cols = (unsigned)((f.D + 63) / 64);

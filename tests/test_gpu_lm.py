@@ -60,6 +60,10 @@ def _gated_inputs(batch, L, D, io, seed, z=True, reset=0.1, h0=True, lam=None):
     return p, opt, r(batch, L, D), _f32(rng, batch, D)
 
 
+def shape_of(p):
+    return p["u"].shape
+
+
 def _gated_dev(p, opt, io):
     args = (_dev(p["u"], io), _dev(p["ra"], io), _dev(p["rx"], io), _dev(p["lam"]))
     return args, dict(z=_dev(opt["z"], io), h0=_dev(opt["h0"]), reset=_dev(opt["reset"]))
@@ -82,6 +86,7 @@ def _check_gated(p, opt, dout, dlast, io, c=8.0, label="", states_too=True):
                                      check=True)
         assert set(g) == set(wg)
         e = {k: parity_error(_host(g[k]), wg[k]) for k in g}
+        print(label, shape_of(p), io, {**errs, **e})
         for k, v in e.items():
             assert v <= (5e-4 if k == "dlam" else 1e-4 if k == "dh0" else tol), (label, k, e)
     return out, last, g
