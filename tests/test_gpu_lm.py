@@ -254,7 +254,7 @@ def test_gated_scan_reports_a_wait_that_gives_up():
 
 # ------------------------------------------------------------------------------------------ embedding
 
-EMBED = [(1, 7, 8), (5, 3, 1), (64, 1, 16), (777, 300, 96), (1000, 70000, 33), (2500, 11, 520), (4097, 1023, 8),
+EMBED = [(20000, 300, 24), (17000, 40000, 8), (40000, 1000000, 3), (1, 7, 8), (5, 3, 1), (64, 1, 16), (777, 300, 96), (1000, 70000, 33), (2500, 11, 520), (4097, 1023, 8),
          (9000, 5000, 64), (3, 1024, 2560)]
 
 
@@ -279,7 +279,7 @@ def test_embedding_and_its_gradient(shape, io):
     assert torch.equal(g, lib.mamba_embed_bwd(_dev(ids), _dev(dout, io), V, scale=1.7))
 
 
-@pytest.mark.parametrize("n", [1, 31, 32, 33, 64, 65, 1000, 5000])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 31, 32, 33, 64, 65, 1000, 5000, 30000])
 def test_embedding_gradient_of_one_repeated_id(n):
     lib = _lib()
     rng = np.random.default_rng(n)
