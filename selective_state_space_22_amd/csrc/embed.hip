@@ -101,19 +101,28 @@ constexpr size_t kStreamZeros = size_t(128) << 20;
 constexpr size_t kZeroChunk = 65536;
 
 // Part of `blocks` workgroups of the launch, a chunk at a time.
-__device__ __forceinline__ void write_zeros(const Zeros& z, int64_t block, int64_t blocks) {
+template <bool STREAM>
+__device__ __forceinline__ void zero_chunks(const Zeros& z, int64_t block, int64_t blocks) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 zero = {0, 0, 0, 0};
   for (size_t c = z.from + block * kZeroChunk; c < z.to; c += blocks * kZeroChunk) {
     const size_t end = c + kZeroChunk < z.to ? c + kZeroChunk : z.to;
     for (size_t i = c + threadIdx.x * 16; i < end; i += blockDim.x * 16) {
-      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
       u32x4* q = reinterpret_cast<u32x4*>(z.p + i);
-      const u32x4 zero = {0, 0, 0, 0};
-      if (i + 16 <= end && z.stream) __builtin_nontemporal_store(zero, q);
-      else if (i + 16 <= end) *q = zero;
-      else
+      if (i + 16 > end) {
         for (size_t k = i; k < end; ++k) z.p[k] = 0;
+      } else if (STREAM) {
+        __builtin_nontemporal_store(zero, q);
+      } else {
+        *q = zero;
+      }
     }
   }
+}
+
+__device__ __forceinline__ void write_zeros(const Zeros& z, int64_t block, int64_t blocks) {
+  if (z.stream) zero_chunks<true>(z, block, blocks);
+  else zero_chunks<false>(z, block, blocks);
 }
 
 __global__ __launch_bounds__(1024) void zeros_kernel(Zeros z) { write_zeros(z, blockIdx.x, gridDim.x); }
