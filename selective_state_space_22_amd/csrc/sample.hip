@@ -1,11 +1,15 @@
 // sample.hip -- drawing a token per row of logits (include/mamba_mi355x_lm.h).
 //
-// One workgroup per row.  The three filters keep a prefix of the row in falling
-// order (equal logits: lower index first), so what stays is everything above a
-// cut key, the first few logits equal to it, and of those what min_p leaves.  The
-// cut is found by radix selection over an order-preserving 32-bit key, by counts
-// (top_k) or by masses (top_p).  Masses are summed as integers (w 2^s, s = 62 -
-// log2 of the row length), so that their sums do not depend on an order.
+// One workgroup per row.  The filters keep a prefix of the row in falling order (equal
+// logits: lower index first), so nothing has to be sorted: it is enough to find where the
+// prefix ends.  A histogram over (m - x) / T, 64 bins to a unit, brackets the end; what
+// lies above the bracket stays, and the few elements inside are listed in LDS and searched
+// for the exact end by radix selection over (key, index), by counts (top_k) or by masses
+// (top_p).  Rows that do not fit this (lists longer than LDS, logits spread over more than
+// 32 units) take a radix selection over the whole row.
+//
+// Masses that are added by atomics are integers (w 2^s, s = 62 - log2 of the row length,
+// 44 at most), so that no sum depends on an order.
 #include <hip/hip_runtime.h>
 
 #include "lm_internal.h"
@@ -17,6 +21,11 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr uint32_t kMasked = 0x007fffffu;  // key of -inf; NaN takes it too
+constexpr int kBins = 2048;
+constexpr float kBinsPerUnit = 64.0f;
+constexpr int kList = 2048;        // elements that the exact search holds
+constexpr int kCacheVecs = 7168;   // 16-byte pieces of the row kept in LDS
+constexpr int kMaximaTopK = 512;   // top_k up to which the threads' maxima bracket the end
 
 // Order-preserving key: larger logit, larger key; -0 and +0 are equal.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -38,34 +47,80 @@ __device__ __forceinline__ float exp_accurate(float t) {
   return t < -87.0f ? 0.0f : __builtin_fmaf(r, lo * kLn2, r);
 }
 
-// One row's logits as keys, and the weights relative to its largest logit.
-template <typename IO>
-struct Row {
-  const IO* x;
-  int V;
-  uint32_t mkey;  // key of the largest logit
-  float m, temperature;
-  float unit;     // masses are round(w * unit)
-  __device__ __forceinline__ uint32_t key(int i) const { return key_of(load_io(x, i)); }
-  // (x - m) / T, 0 where x equals the maximum (also an infinite one)
-  __device__ __forceinline__ float scaled(uint32_t k) const {
-    return k == mkey ? 0.0f : (logit_of(k) - m) / temperature;
-  }
-  __device__ __forceinline__ float weight(uint32_t k) const { return k == mkey ? 1.0f : exp_accurate(scaled(k)); }
-  __device__ __forceinline__ uint64_t mass(uint32_t k) const {
-    return (uint64_t)__builtin_rintf(weight(k) * unit);
-  }
-};
-
 struct Shared {
-  unsigned long long hist[256];
+  uint4 cache[kCacheVecs];
+  uint32_t hist[kBins];
+  unsigned long long list[kList];
+  unsigned long long mass[256];
+  uint32_t count[256];
+  double dsum[kWaves];
   unsigned long long sum[kWaves];
   uint32_t word[kWaves];
   float score[kWaves];
-  uint32_t digit;
-  unsigned long long before;
-  int cut_index;
+  unsigned long long before, found;
+  uint32_t digit, listed;
+  int bin, cut_index;
 };
+
+// One row's logits, the first of them in LDS, and the weights relative to the largest.
+template <typename IO>
+struct Row {
+  static constexpr int VEC = 16 / sizeof(IO);
+  const IO* x;
+  const uint4* vecs;  // the row's 16-byte aligned pieces
+  const uint4* cache;
+  int V, head, nvec, cached;
+  uint32_t mkey;  // key of the largest logit
+  float m, temperature, to_bin;
+  float unit;     // masses are round(w * unit)
+
+  __device__ __forceinline__ void set(const IO* row, int v) {
+    x = row;
+    V = v;
+    const int off = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(IO));
+    head = off ? (VEC - off < v ? VEC - off : v) : 0;
+    nvec = (v - head) / VEC;
+    vecs = reinterpret_cast<const uint4*>(row + head);
+  }
+  __device__ __forceinline__ float at(int i) const { return load_io(x, i); }
+  __device__ __forceinline__ uint32_t key(int i) const { return key_of(at(i)); }
+  static __device__ __forceinline__ float element(const uint4& v, int e) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (VEC == 8) return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+    else return __uint_as_float(w[e]);
+  }
+  // f(logit, index) for the thread's elements: pieces in steps of the workgroup, then the
+  // elements before the first and after the last piece, one to a thread.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll 2
+    for (int j = threadIdx.x; j < nvec; j += kThreads) {
+      const uint4 v = j < cached ? cache[j] : vecs[j];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f(element(v, e), head + j * VEC + e);
+    }
+    edges(f);
+  }
+  template <typename F>
+  __device__ __forceinline__ void edges(F f) const {
+    const int rest = V - nvec * VEC;
+    if ((int)threadIdx.x < rest) {
+      const int i = (int)threadIdx.x < head ? (int)threadIdx.x : nvec * VEC + (int)threadIdx.x;
+      f(at(i), i);
+    }
+  }
+  // (x - m) / T, 0 where x equals the maximum (also an infinite one)
+  __device__ __forceinline__ float scaled(float v) const { return v == m ? 0.0f : (v - m) / temperature; }
+  __device__ __forceinline__ float weight(float v) const { return exp_accurate(scaled(v)); }
+  __device__ __forceinline__ uint64_t mass(float w) const { return (uint64_t)__builtin_rintf(w * unit); }
+  // Bin of a logit, monotone in it; masked ones: none.
+  __device__ __forceinline__ int bin(float v, float& d) const {
+    d = v == m ? 0.0f : (m - v) * to_bin;
+    return d < (float)(kBins - 1) ? (int)d : kBins - 1;
+  }
+};
+
+__device__ __forceinline__ bool masked(float v) { return !(v > -__builtin_inff()); }
 
 __device__ __forceinline__ uint32_t block_max(uint32_t v, Shared& sm) {
 #pragma unroll
@@ -73,6 +128,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, Shared& sm) {
   if ((threadIdx.x & 63) == 0) sm.word[threadIdx.x >> 6] = v;
   __syncthreads();
   uint32_t r = 0;
+#pragma unroll
   for (int w = 0; w < kWaves; ++w) r = max(r, sm.word[w]);
   __syncthreads();
   return r;
@@ -84,10 +140,186 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, Shared& sm) {
   if ((threadIdx.x & 63) == 0) sm.sum[threadIdx.x >> 6] = v;
   __syncthreads();
   uint64_t r = 0;
+#pragma unroll
   for (int w = 0; w < kWaves; ++w) r += sm.sum[w];
   __syncthreads();
   return r;
 }
+
+__device__ __forceinline__ double block_sum(double v, Shared& sm) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if ((threadIdx.x & 63) == 0) sm.dsum[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double r = 0.0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) r += sm.dsum[w];
+  __syncthreads();
+  return r;
+}
+
+// The best (score, lowest index) so far; a NaN score counts as -inf.
+struct Best {
+  float score = -__builtin_inff();
+  uint32_t at = 0xffffffffu;  // none
+  __device__ __forceinline__ void take(float s, uint32_t i) {
+    if (i != 0xffffffffu && (at == 0xffffffffu || s > score || (s == score && i < at))) score = s, at = i;
+  }
+  __device__ __forceinline__ void offer(float w, float noise, uint32_t i) {
+    const float s = w / noise;
+    take(s != s ? -__builtin_inff() : s, i);
+  }
+  __device__ __forceinline__ void block(Shared& sm) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const float s = __shfl_xor(score, o, 64);
+      const uint32_t i = __shfl_xor(at, o, 64);
+      take(s, i);
+    }
+    if ((threadIdx.x & 63) == 0) sm.score[threadIdx.x >> 6] = score, sm.word[threadIdx.x >> 6] = at;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) take(sm.score[w], sm.word[w]);
+  }
+};
+
+// ---------------------------------------------------------------- bracketing by a histogram
+
+__device__ __forceinline__ void clear_bins(Shared& sm) {
+  __syncthreads();  // sm.bin has been read
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sm.hist[i] = 0;
+  if (threadIdx.x == 0) sm.bin = kBins, sm.listed = 0;
+  __syncthreads();
+}
+
+// The first bin up to which the bins' measure reaches `target` (kBins: none does).  MASS: a
+// bin holds the sum of e^{(bin - 64 d) / 64} 2^14 of its elements, its mass but for a common
+// factor of the bin; else their count.
+template <bool MASS>
+__device__ __forceinline__ int find_bin(float share, float target, Shared& sm) {
+  __syncthreads();
+  const int b = 2 * threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const float scale = MASS ? ex2(-(float)b * (kLog2e / kBinsPerUnit)) : 1.0f;
+  const float v0 = (float)sm.hist[b] * scale;
+  const float v1 = (float)sm.hist[b + 1] * scale * (MASS ? 0.98449644f : 1.0f);  // e^{-1/64}
+  float incl = v0 + v1;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const float y = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 63) sm.score[wave] = incl;
+  __syncthreads();
+  float below = 0.0f, total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    below += w < wave ? sm.score[w] : 0.0f;
+    total += sm.score[w];
+  }
+  const float want = MASS ? share * total : target;
+  const float end = below + incl, start = end - v0 - v1;
+  if (end >= want) atomicMin(&sm.bin, start + v0 >= want ? b : b + 1);
+  __syncthreads();
+  return sm.bin;
+}
+
+// Appends (key, ~index) of the lanes that have one to the list.
+__device__ __forceinline__ void append(bool have, float v, int i, Shared& sm) {
+  const uint64_t m = __ballot(have);
+  if (m == 0) return;
+  const int lane = threadIdx.x & 63, first = __ffsll((unsigned long long)m) - 1;
+  uint32_t base = 0;
+  if (lane == first) base = atomicAdd(&sm.listed, (uint32_t)__popcll(m));
+  base = __shfl(base, first, 64);
+  const uint32_t at = base + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+  if (have && at < kList) sm.list[at] = (unsigned long long)key_of(v) << 32 | (uint32_t)~i;
+}
+
+__device__ __forceinline__ float listed_logit(unsigned long long e) { return logit_of((uint32_t)(e >> 32)); }
+__device__ __forceinline__ uint32_t listed_index(unsigned long long e) { return ~(uint32_t)e; }
+
+// The element of the first n of the list at which the measure of the elements >= it first
+// reaches target (1 <= target <= their total).  The measure is the count, or the mass of
+// the elements >= from.  Eight bits a step, from the first bit in which the elements differ.
+template <bool MASS, typename IO>
+__device__ __forceinline__ unsigned long long select_listed(const Row<IO>& row, int n, unsigned long long from,
+                                                            uint64_t target, Shared& sm) {
+  unsigned long long lo = ~0ull, hi = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const unsigned long long e = sm.list[i];
+    if (e >= from) lo = min(lo, e), hi = max(hi, e);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    lo = min(lo, (unsigned long long)__shfl_xor(lo, o, 64));
+    hi = max(hi, (unsigned long long)__shfl_xor(hi, o, 64));
+  }
+  if ((threadIdx.x & 63) == 0) sm.sum[threadIdx.x >> 6] = lo, sm.mass[threadIdx.x >> 6] = hi;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) lo = min(lo, sm.sum[w]), hi = max(hi, sm.mass[w]);
+  __syncthreads();
+  if (lo == hi) return lo;
+  int top = 64 - __clzll(lo ^ hi);  // bits below `top` are undecided
+  unsigned long long prefix = top < 64 ? lo >> top : 0;
+  uint64_t above = 0;
+  while (true) {
+    const int s = top > 8 ? top - 8 : 0, width = top - s;
+    if (threadIdx.x < 256) sm.mass[threadIdx.x] = 0, sm.count[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const unsigned long long e = sm.list[i];
+      if (e >= from && (top == 64 || e >> top == prefix)) {
+        const uint32_t d = (uint32_t)(e >> s) & ((1u << width) - 1);
+        atomicAdd(&sm.count[d], 1u);
+        if (MASS) atomicAdd(&sm.mass[d], (unsigned long long)row.mass(row.weight(listed_logit(e))));
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {  // lane l: digits 255 - 4l downwards
+      const int lane = threadIdx.x;
+      unsigned long long h[4], incl = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = 255 - 4 * lane - j;
+        incl += h[j] = MASS ? sm.mass[d] : (unsigned long long)sm.count[d];
+      }
+      const unsigned long long mine = incl;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const unsigned long long y = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += y;
+      }
+      const uint64_t reach = __ballot(above + incl >= target);
+      if (reach != 0 && lane == __ffsll((unsigned long long)reach) - 1) {
+        unsigned long long b = above + incl - mine;
+        int j = 0;
+        while (j < 3 && b + h[j] < target) b += h[j++];
+        sm.digit = 255 - 4 * lane - j;
+        sm.before = b;
+      }
+      if (reach == 0 && lane == 0) sm.digit = 0, sm.before = above;  // (not where target <= total)
+    }
+    __syncthreads();
+    const uint32_t d = sm.digit;
+    above = sm.before;
+    prefix = prefix << width | d;
+    top = s;
+    const bool last = top == 0 || sm.count[d] == 1;
+    if (last) {
+      if (top == 0) return prefix;
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const unsigned long long e = sm.list[i];
+        if (e >= from && e >> top == prefix) sm.found = e;
+      }
+      __syncthreads();
+      return sm.found;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- selection over the whole row
 
 // The largest key K such that the measure of the keys >= K (those >= low and not
 // masked) reaches target (1 <= target <= their total measure); before: the measure
@@ -98,19 +330,19 @@ __device__ __forceinline__ uint32_t select_key(const Row<IO>& row, uint32_t low,
   uint32_t prefix = 0;
   uint64_t above = 0;
   for (int s = 24; s >= 0; s -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kThreads) sm.hist[i] = 0;
+    if (threadIdx.x < 256) sm.mass[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < row.V; i += kThreads) {
-      const uint32_t k = row.key(i);
+    row.each([&](float v, int) {
+      const uint32_t k = key_of(v);
       if (k >= low && k > kMasked && (s == 24 || k >> (s + 8) == prefix))
-        atomicAdd(&sm.hist[(k >> s) & 255], MASS ? (unsigned long long)row.mass(k) : 1ull);
-    }
+        atomicAdd(&sm.mass[(k >> s) & 255], MASS ? (unsigned long long)row.mass(row.weight(v)) : 1ull);
+    });
     __syncthreads();
     if (threadIdx.x < 64) {  // lane l: digits 255 - 4l downwards
       const int lane = threadIdx.x;
       unsigned long long h[4], incl = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) incl += h[j] = sm.hist[255 - 4 * lane - j];
+      for (int j = 0; j < 4; ++j) incl += h[j] = sm.mass[255 - 4 * lane - j];
       const unsigned long long mine = incl;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -135,60 +367,39 @@ __device__ __forceinline__ uint32_t select_key(const Row<IO>& row, uint32_t low,
   return prefix;
 }
 
+// What stays of a row, found without the histogram: the keys above `cut` and, of those equal
+// to it, the ones up to index `last_tie`.
+struct Cut {
+  uint32_t key;
+  int last_tie;
+};
+
 template <typename IO>
-__global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, float unit) {
-  __shared__ Shared sm;
-  const int64_t r = blockIdx.x;
-  Row<IO> row;
-  row.x = (const IO*)a.logits + r * a.V;
-  row.V = (int)a.V;
-  row.unit = unit;
-  const float* noise = a.noise + r * a.V;
-  int64_t k = a.top_k ? a.top_k[r] : 0;
-  const float t = a.temperature ? a.temperature[r] : 1.0f;
-  const float p = a.top_p ? a.top_p[r] : 1.0f;
-  const float minp = a.min_p && a.min_p[r] > 0.0f ? fminf(a.min_p[r], 1.0f) : 0.0f;  // NaN: off
-  const bool greedy = !(t > 0.0f) || p <= 0.0f;
-  row.temperature = t > 0.0f ? t : 1.0f;
-  if (greedy) k = 1;
-
-  uint32_t mk = 0;
-  for (int i = threadIdx.x; i < row.V; i += kThreads) mk = max(mk, row.key(i));
-  row.mkey = block_max(mk, sm);
-  row.m = logit_of(row.mkey);
-  if (row.mkey <= kMasked) {
-    if (threadIdx.x == 0) {
-      a.tokens[r] = -1;
-      if (a.logprob) a.logprob[r] = -__builtin_inff();
-    }
-    return;
-  }
-
-  // What stays: keys above cut, and the first `ties` of those equal to it.
+__device__ Cut cut_row(const Row<IO>& row, int64_t k, float p, Shared& sm) {
   uint32_t cut = kMasked + 1;
   uint64_t ties = ~0ull;
   if (k > 0 && k < row.V) {
     uint64_t n = 0, before;
-    for (int i = threadIdx.x; i < row.V; i += kThreads) n += row.key(i) > kMasked;
+    row.each([&](float v, int) { n += !masked(v); });
     n = block_sum(n, sm);
     if ((uint64_t)k < n) {
       cut = select_key<false>(row, cut, (uint64_t)k, before, sm);
       ties = (uint64_t)k - before;
     }
   }
-  if (p < 1.0f && k != 1) {
+  if (p < 1.0f) {
     uint64_t total = 0;
-    for (int i = threadIdx.x; i < row.V; i += kThreads) {
-      const uint32_t key = row.key(i);
-      if (key > cut || (key == cut && ties == ~0ull)) total += row.mass(key);
-    }
+    row.each([&](float v, int) {
+      const uint32_t key = key_of(v);
+      if (key > cut || (key == cut && ties == ~0ull)) total += row.mass(row.weight(v));
+    });
     total = block_sum(total, sm);
-    if (ties != ~0ull) total += ties * row.mass(cut);
+    if (ties != ~0ull) total += ties * row.mass(row.weight(logit_of(cut)));
     // before < p total for the integer `before` is before < ceil(p total)
     uint64_t target = (uint64_t)__builtin_ceil((double)p * (double)total), before;
     target = target < 1 ? 1 : (target > total ? total : target);
     const uint32_t at = select_key<true>(row, cut, target, before, sm);
-    const uint64_t one = row.mass(at);
+    const uint64_t one = row.mass(row.weight(logit_of(at)));
     const uint64_t need = one > 0 ? (target - before + one - 1) / one : ~0ull;
     if (at != cut || need < ties) ties = need;
     cut = at;
@@ -220,38 +431,171 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
     }
   }
   __syncthreads();
-  const int last_tie = sm.cut_index;
+  return Cut{cut, sm.cut_index};
+}
 
-  uint64_t total = 0;
-  float best = -__builtin_inff();
-  uint32_t at = 0xffffffffu;
-  for (int i = threadIdx.x; i < row.V; i += kThreads) {
-    const uint32_t key = row.key(i);
-    if (!(key > cut || (key == cut && i <= last_tie))) continue;
-    const float w = row.weight(key);
-    if (!(w > 0.0f && w >= minp)) continue;
-    total += (uint64_t)__builtin_rintf(w * row.unit);
-    float sc = w / noise[i];
-    if (sc != sc) sc = -__builtin_inff();
-    if (at == 0xffffffffu || sc > best) best = sc, at = i;
-  }
-  total = block_sum(total, sm);
+// ---------------------------------------------------------------- the row
+
+template <typename IO>
+__global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, float unit) {
+  __shared__ Shared sm;
+  const int64_t r = blockIdx.x;
+  Row<IO> row;
+  row.set((const IO*)a.logits + r * a.V, (int)a.V);
+  row.unit = unit;
+  row.cache = sm.cache;
+  row.cached = row.nvec < kCacheVecs ? row.nvec : kCacheVecs;
+  const float* noise = a.noise + r * a.V;
+  int64_t k = a.top_k ? a.top_k[r] : 0;
+  const float t = a.temperature ? a.temperature[r] : 1.0f;
+  const float p = a.top_p ? a.top_p[r] : 1.0f;
+  const float minp = a.min_p && a.min_p[r] > 0.0f ? fminf(a.min_p[r], 1.0f) : 0.0f;  // NaN: off
+  const bool greedy = !(t > 0.0f) || p <= 0.0f || k == 1;
+  row.temperature = t > 0.0f ? t : 1.0f;
+  row.to_bin = kBinsPerUnit / row.temperature;
+
+  // the largest logit (a NaN is never the larger), the thread's and the row's
+  float mine = -__builtin_inff();
+#pragma unroll 4
+  for (int j = threadIdx.x; j < row.nvec; j += kThreads) {
+    const uint4 v = row.vecs[j];
+    if (j < kCacheVecs) sm.cache[j] = v;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float sc = __shfl_xor(best, o, 64);
-    const uint32_t i = __shfl_xor(at, o, 64);
-    if (i != 0xffffffffu && (at == 0xffffffffu || sc > best || (sc == best && i < at))) best = sc, at = i;
+    for (int e = 0; e < Row<IO>::VEC; ++e) mine = fmaxf(mine, Row<IO>::element(v, e));
   }
-  if ((threadIdx.x & 63) == 0) sm.score[threadIdx.x >> 6] = best, sm.word[threadIdx.x >> 6] = at;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kWaves; ++w) {
-      const float sc = sm.score[w];
-      const uint32_t i = sm.word[w];
-      if (i != 0xffffffffu && (at == 0xffffffffu || sc > best || (sc == best && i < at))) best = sc, at = i;
+  row.edges([&](float v, int) { mine = fmaxf(mine, v); });
+  row.mkey = block_max(key_of(mine), sm);
+  row.m = logit_of(row.mkey);
+  if (row.mkey <= kMasked) {
+    if (threadIdx.x == 0) {
+      a.tokens[r] = -1;
+      if (a.logprob) a.logprob[r] = -__builtin_inff();
     }
-    a.tokens[r] = at;
-    if (a.logprob) a.logprob[r] = row.scaled(row.key(at)) - logf((float)((double)total / (double)row.unit));
+    return;
+  }
+
+  Best best;
+  double total = 0.0;  // mass of what stays
+  if (greedy) {
+    uint32_t first = 0;
+    row.each([&](float v, int i) {
+      if (v == row.m) first = max(first, (uint32_t)~i);
+    });
+    best.at = ~block_max(first, sm);
+    total = 1.0;
+  } else {
+    const bool want_k = k > 0 && k < row.V, want_p = p < 1.0f;
+    int lo = 0, hi = -1;  // bins below lo stay, bins lo ... hi are listed
+    bool row_wide = false;
+    if (want_k) {
+      clear_bins(sm);
+      float d;
+      if (k <= kMaximaTopK) {  // k threads' maxima, so k elements, lie up to the bin
+        if (!masked(mine)) atomicAdd(&sm.hist[row.bin(mine, d)], 1u);
+        hi = find_bin<false>(0.0f, (float)k, sm);
+      }
+      if (hi < 0 || hi == kBins) {
+        clear_bins(sm);
+        row.each([&](float v, int) {
+          if (!masked(v)) atomicAdd(&sm.hist[row.bin(v, d)], 1u);
+        });
+        hi = find_bin<false>(0.0f, (float)k, sm);
+      }
+    } else if (want_p) {
+      clear_bins(sm);
+      row.each([&](float v, int) {
+        float d;
+        const int b = row.bin(v, d);
+        const float f = (d - (float)b) * (1.0f / kBinsPerUnit);
+        // e^-f 2^14 for f <= 1/64
+        if (b < kBins - 1) atomicAdd(&sm.hist[b], (uint32_t)__builtin_fmaf(f, __builtin_fmaf(f, 8192.0f, -16384.0f), 16384.5f));
+      });
+      const int b = find_bin<true>(p, 0.0f, sm);
+      lo = b - 1, hi = b + 1;  // (a bin to either side for the rounding of the sums)
+      row_wide = b >= kBins - 2;
+    }
+    if (want_k || want_p) {
+      float all = 0.0f, above = 0.0f, kept = 0.0f;
+      row.each([&](float v, int i) {
+        float d;
+        const int b = masked(v) ? kBins + 1 : row.bin(v, d);
+        append(b >= lo && b <= hi, v, i, sm);
+        if (!want_k) {
+          const float w = masked(v) ? 0.0f : row.weight(v);
+          all += w;
+          if (b < lo) {
+            above += w;
+            if (w >= minp) {
+              kept += w;
+              best.offer(w, noise[i], i);
+            }
+          }
+        }
+      });
+      __syncthreads();
+      const int n = (int)sm.listed;
+      row_wide |= n > kList;
+      unsigned long long from = 0;  // listed elements >= from stay
+      if (!row_wide && want_k) {
+        if (n > k) from = select_listed<false>(row, n, 0ull, (uint64_t)k, sm);
+        if (want_p) {
+          uint64_t sum = 0;
+          for (int i = threadIdx.x; i < n; i += kThreads)
+            if (sm.list[i] >= from) sum += row.mass(row.weight(listed_logit(sm.list[i])));
+          sum = block_sum(sum, sm);
+          uint64_t target = (uint64_t)__builtin_ceil((double)p * (double)sum);
+          target = target < 1 ? 1 : (target > sum ? sum : target);
+          from = select_listed<true>(row, n, from, target, sm);
+        }
+      } else if (!row_wide) {
+        const double whole = block_sum((double)all, sm), over = block_sum((double)above, sm);
+        uint64_t sum = 0;
+        for (int i = threadIdx.x; i < n; i += kThreads) sum += row.mass(row.weight(listed_logit(sm.list[i])));
+        sum = block_sum(sum, sm);
+        const double target = __builtin_ceil(((double)p * whole - over) * (double)unit);
+        if (target < 1.0 || target > (double)sum) row_wide = true;  // the end is not in the list
+        else from = select_listed<true>(row, n, 0ull, (uint64_t)target, sm);
+      }
+      if (row_wide) {
+        best = Best();
+        kept = 0.0f;
+        const Cut cut = cut_row(row, k, p, sm);
+        row.each([&](float v, int i) {
+          const uint32_t key = key_of(v);
+          if (!(key > cut.key || (key == cut.key && i <= cut.last_tie))) return;
+          const float w = row.weight(v);
+          if (!(w > 0.0f && w >= minp)) return;
+          kept += w;
+          best.offer(w, noise[i], i);
+        });
+      } else {
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+          const unsigned long long e = sm.list[i];
+          if (e < from) continue;
+          const float w = row.weight(listed_logit(e));
+          if (!(w > 0.0f && w >= minp)) continue;
+          kept += w;
+          best.offer(w, noise[listed_index(e)], listed_index(e));
+        }
+      }
+      total = (double)kept;
+    } else {
+      float kept = 0.0f;
+      row.each([&](float v, int i) {
+        if (masked(v)) return;
+        const float w = row.weight(v);
+        if (!(w > 0.0f && w >= minp)) return;
+        kept += w;
+        best.offer(w, noise[i], i);
+      });
+      total = (double)kept;
+    }
+    total = block_sum(total, sm);
+    best.block(sm);
+  }
+  if (threadIdx.x == 0) {
+    a.tokens[r] = best.at;
+    if (a.logprob) a.logprob[r] = row.scaled(row.at(best.at)) - logf((float)total);
   }
 }
 
