@@ -53,7 +53,7 @@ struct Shared {
   unsigned long long list[kList];
   unsigned long long mass[256];
   uint32_t count[256];
-  double dsum[kWaves];
+  double dsum[2][kWaves];
   unsigned long long sum[kWaves];
   uint32_t word[kWaves];
   float score[kWaves];
@@ -93,13 +93,36 @@ struct Row {
   // elements before the first and after the last piece, one to a thread.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-#pragma unroll 2
-    for (int j = threadIdx.x; j < nvec; j += kThreads) {
-      const uint4 v = j < cached ? cache[j] : vecs[j];
+    for (int j = threadIdx.x; j < cached; j += kThreads) {
+      const uint4 v = cache[j];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) f(element(v, e), head + j * VEC + e);
     }
+    // cached is a multiple of the workgroup or the whole row: the thread's pieces go on
+    ahead<4>(cached, [&](const uint4& v, int j) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f(element(v, e), head + j * VEC + e);
+    });
     edges(f);
+  }
+  // f(piece, its number) for the thread's pieces from number `from` on, the next N in flight.
+  template <int N, typename F>
+  __device__ __forceinline__ void ahead(int from, F f) const {
+    uint4 v[N];
+    int j = from + (int)threadIdx.x;
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      if (j + q * kThreads < nvec) v[q] = vecs[j + q * kThreads];
+    while (j < nvec) {
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        if (j + q * kThreads >= nvec) break;
+        const uint4 now = v[q];
+        if (j + (q + N) * kThreads < nvec) v[q] = vecs[j + (q + N) * kThreads];
+        f(now, j + q * kThreads);
+      }
+      j += N * kThreads;
+    }
   }
   template <typename F>
   __device__ __forceinline__ void edges(F f) const {
@@ -113,11 +136,11 @@ struct Row {
   __device__ __forceinline__ float scaled(float v) const { return v == m ? 0.0f : (v - m) / temperature; }
   __device__ __forceinline__ float weight(float v) const { return exp_accurate(scaled(v)); }
   __device__ __forceinline__ uint64_t mass(float w) const { return (uint64_t)__builtin_rintf(w * unit); }
-  // Bin of a logit, monotone in it; masked ones: none.
-  __device__ __forceinline__ int bin(float v, float& d) const {
-    d = v == m ? 0.0f : (m - v) * to_bin;
-    return d < (float)(kBins - 1) ? (int)d : kBins - 1;
-  }
+  // Distance below the (finite) maximum in bins, monotone in the logit: infinite for -inf, a
+  // NaN for a NaN; and the weight from it, to some 1e-6: for sums, and to tell whether an
+  // element can matter.
+  __device__ __forceinline__ float distance(float v) const { return (m - v) * to_bin; }
+  static __device__ __forceinline__ float rough_weight(float d) { return ex2(d * (-kLog2e / kBinsPerUnit)); }
 };
 
 __device__ __forceinline__ bool masked(float v) { return !(v > -__builtin_inff()); }
@@ -146,16 +169,22 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, Shared& sm) {
   return r;
 }
 
-__device__ __forceinline__ double block_sum(double v, Shared& sm) {
+// Sums of two numbers and of an integer at once.
+__device__ __forceinline__ void block_sums(double& a, double& b, uint64_t& c, Shared& sm) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  if ((threadIdx.x & 63) == 0) sm.dsum[threadIdx.x >> 6] = v;
+  for (int o = 32; o > 0; o >>= 1) {
+    a += __shfl_xor(a, o, 64);
+    b += __shfl_xor(b, o, 64);
+    c += (uint64_t)__shfl_xor((unsigned long long)c, o, 64);
+  }
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) sm.dsum[0][wave] = a, sm.dsum[1][wave] = b, sm.sum[wave] = c;
   __syncthreads();
-  double r = 0.0;
+  a = b = 0.0;
+  c = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) r += sm.dsum[w];
+  for (int w = 0; w < kWaves; ++w) a += sm.dsum[0][w], b += sm.dsum[1][w], c += sm.sum[w];
   __syncthreads();
-  return r;
 }
 
 // The best (score, lowest index) so far; a NaN score counts as -inf.
@@ -168,6 +197,10 @@ struct Best {
   __device__ __forceinline__ void offer(float w, float noise, uint32_t i) {
     const float s = w / noise;
     take(s != s ? -__builtin_inff() : s, i);
+  }
+  // Whether an element of about that weight may be better: false only where it is not.
+  __device__ __forceinline__ bool may(float rough, float noise) const {
+    return !(rough * rcp(noise) < __builtin_fmaf(-1.0e-4f, fabsf(score), score));
   }
   __device__ __forceinline__ void block(Shared& sm) {
 #pragma unroll
@@ -434,6 +467,83 @@ __device__ Cut cut_row(const Row<IO>& row, int64_t k, float p, Shared& sm) {
   return Cut{cut, sm.cut_index};
 }
 
+// ---------------------------------------------------------------- scoring
+
+// One pass over the row: elements at distances below lo are scored (those of at least minp)
+// and summed, those from lo up to below hi are listed, the rest is summed too.  Sums take
+// the rough weights, a score that may be the best the exact one.  kBatch pieces of the row
+// at a time: their noise is in flight together, and so are the next pieces.
+struct Sums {
+  float above = 0.0f, kept = 0.0f, rest = 0.0f;  // of distances below lo, of the scored ones, from hi on
+};
+
+template <typename IO>
+__device__ __forceinline__ void score_row(const Row<IO>& row, float lo, float hi, float minp, const float* noise,
+                                          Sums& sums, Best& best, Shared& sm) {
+  constexpr int VEC = Row<IO>::VEC, kBatch = 16 / VEC;
+  typedef float Noise4 __attribute__((ext_vector_type(4), aligned(4)));
+  // the rough weight of an element that is scored, else -1
+  auto first = [&](float v, int i) {
+    const float d = row.distance(v);
+    const float w = Row<IO>::rough_weight(d);
+    append(d >= lo && d < hi, v, i, sm);
+    const bool in = d < lo;
+    sums.above += in ? w : 0.0f;
+    sums.rest += d >= hi ? w : 0.0f;  // (a NaN is in none, an infinite distance weighs 0)
+    bool take = in && w >= minp;
+    if (fabsf(w - minp) < 1.0e-5f * minp) take = in && row.weight(v) >= minp;
+    sums.kept += take ? w : 0.0f;
+    return take ? w : -1.0f;
+  };
+  auto second = [&](float rough, float v, float e, int i) {
+    if (rough < 0.0f || !best.may(rough, e)) return;
+    const float w = row.weight(v);
+    if (w > 0.0f) best.offer(w, e, i);
+  };
+  auto fetch = [&](uint4 (&v)[kBatch], int j0) {
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int j = j0 + q * kThreads;
+      if (j < row.nvec) v[q] = j < row.cached ? row.cache[j] : row.vecs[j];
+    }
+  };
+  uint4 next[kBatch];
+  fetch(next, threadIdx.x);
+  for (int j0 = threadIdx.x; j0 < row.nvec; j0 += kBatch * kThreads) {
+    uint4 v[kBatch];
+    float w[kBatch][VEC];
+    Noise4 e[kBatch][VEC / 4];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      v[q] = next[q];
+      const int j = j0 + q * kThreads, i = row.head + j * VEC;
+      if (j >= row.nvec) continue;
+      bool any = false;
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        w[q][c] = first(Row<IO>::element(v[q], c), i + c);
+        any |= w[q][c] >= 0.0f;
+      }
+      if (any) {
+#pragma unroll
+        for (int c = 0; c < VEC / 4; ++c) e[q][c] = *reinterpret_cast<const Noise4*>(noise + i + 4 * c);
+      }
+    }
+    fetch(next, j0 + kBatch * kThreads);
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int j = j0 + q * kThreads, i = row.head + j * VEC;
+      if (j >= row.nvec) continue;
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) second(w[q][c], Row<IO>::element(v[q], c), e[q][c / 4][c % 4], i + c);
+    }
+  }
+  row.edges([&](float v, int i) {
+    const float w = first(v, i);
+    if (w >= 0.0f) second(w, v, noise[i], i);
+  });
+}
+
 // ---------------------------------------------------------------- the row
 
 template <typename IO>
@@ -456,13 +566,11 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
 
   // the largest logit (a NaN is never the larger), the thread's and the row's
   float mine = -__builtin_inff();
-#pragma unroll 4
-  for (int j = threadIdx.x; j < row.nvec; j += kThreads) {
-    const uint4 v = row.vecs[j];
+  row.template ahead<8>(0, [&](const uint4& v, int j) {
     if (j < kCacheVecs) sm.cache[j] = v;
 #pragma unroll
     for (int e = 0; e < Row<IO>::VEC; ++e) mine = fmaxf(mine, Row<IO>::element(v, e));
-  }
+  });
   row.edges([&](float v, int) { mine = fmaxf(mine, v); });
   row.mkey = block_max(key_of(mine), sm);
   row.m = logit_of(row.mkey);
@@ -485,53 +593,52 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
     total = 1.0;
   } else {
     const bool want_k = k > 0 && k < row.V, want_p = p < 1.0f;
-    int lo = 0, hi = -1;  // bins below lo stay, bins lo ... hi are listed
-    bool row_wide = false;
-    if (want_k) {
+    float lo = 0.0f, hi = -1.0f;  // distances below lo stay, those from lo up to below hi are listed
+    // (an infinite maximum has no distances; its equals are all that has a weight)
+    bool row_wide = row.m > 3.4028235e38f;
+    if (row_wide) {
       clear_bins(sm);
-      float d;
+    } else if (want_k) {
+      clear_bins(sm);
+      int b = kBins;
       if (k <= kMaximaTopK) {  // k threads' maxima, so k elements, lie up to the bin
-        if (!masked(mine)) atomicAdd(&sm.hist[row.bin(mine, d)], 1u);
-        hi = find_bin<false>(0.0f, (float)k, sm);
+        const float d = row.distance(mine);
+        if (d < (float)kBins) atomicAdd(&sm.hist[(int)d], 1u);
+        b = find_bin<false>(0.0f, (float)k, sm);
       }
-      if (hi < 0 || hi == kBins) {
+      if (b == kBins) {
         clear_bins(sm);
         row.each([&](float v, int) {
-          if (!masked(v)) atomicAdd(&sm.hist[row.bin(v, d)], 1u);
+          const float d = row.distance(v);
+          if (d < (float)kBins) atomicAdd(&sm.hist[(int)d], 1u);
         });
-        hi = find_bin<false>(0.0f, (float)k, sm);
+        b = find_bin<false>(0.0f, (float)k, sm);
       }
+      // fewer than k within the histogram's range: all that is not masked
+      hi = b == kBins ? __builtin_inff() : (float)(b + 1);
     } else if (want_p) {
       clear_bins(sm);
       row.each([&](float v, int) {
-        float d;
-        const int b = row.bin(v, d);
-        const float f = (d - (float)b) * (1.0f / kBinsPerUnit);
-        // e^-f 2^14 for f <= 1/64
-        if (b < kBins - 1) atomicAdd(&sm.hist[b], (uint32_t)__builtin_fmaf(f, __builtin_fmaf(f, 8192.0f, -16384.0f), 16384.5f));
-      });
-      const int b = find_bin<true>(p, 0.0f, sm);
-      lo = b - 1, hi = b + 1;  // (a bin to either side for the rounding of the sums)
-      row_wide = b >= kBins - 2;
-    }
-    if (want_k || want_p) {
-      float all = 0.0f, above = 0.0f, kept = 0.0f;
-      row.each([&](float v, int i) {
-        float d;
-        const int b = masked(v) ? kBins + 1 : row.bin(v, d);
-        append(b >= lo && b <= hi, v, i, sm);
-        if (!want_k) {
-          const float w = masked(v) ? 0.0f : row.weight(v);
-          all += w;
-          if (b < lo) {
-            above += w;
-            if (w >= minp) {
-              kept += w;
-              best.offer(w, noise[i], i);
-            }
-          }
+        const float d = row.distance(v);
+        if (d < (float)kBins) {
+          const int b = (int)d;
+          const float f = (d - (float)b) * (1.0f / kBinsPerUnit);
+          // e^-f 2^14 for f <= 1/64
+          atomicAdd(&sm.hist[b], (uint32_t)__builtin_fmaf(f, __builtin_fmaf(f, 8192.0f, -16384.0f), 16384.5f));
         }
       });
+      const int b = find_bin<true>(p, 0.0f, sm);
+      lo = (float)(b - 1), hi = (float)(b + 2);  // (a bin to either side for the rounding of the sums)
+      row_wide = b == kBins;
+    }
+    if (!want_k && !want_p && !row_wide) lo = hi = __builtin_inff();
+    Sums sums;
+    uint64_t listed = 0;  // mass of the listed elements that stay
+    if (!row_wide) {
+      if (want_k) row.each([&](float v, int i) { append(row.distance(v) < hi, v, i, sm); });
+      else score_row(row, lo, hi, minp, noise, sums, best, sm);
+    }
+    if (want_k || want_p || row_wide) {
       __syncthreads();
       const int n = (int)sm.listed;
       row_wide |= n > kList;
@@ -548,24 +655,25 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
           from = select_listed<true>(row, n, from, target, sm);
         }
       } else if (!row_wide) {
-        const double whole = block_sum((double)all, sm), over = block_sum((double)above, sm);
         uint64_t sum = 0;
         for (int i = threadIdx.x; i < n; i += kThreads) sum += row.mass(row.weight(listed_logit(sm.list[i])));
-        sum = block_sum(sum, sm);
+        double over = (double)sums.above, below = (double)sums.rest;
+        block_sums(over, below, sum, sm);
+        const double whole = over + (double)sum / (double)unit + below;
         const double target = __builtin_ceil(((double)p * whole - over) * (double)unit);
         if (target < 1.0 || target > (double)sum) row_wide = true;  // the end is not in the list
         else from = select_listed<true>(row, n, 0ull, (uint64_t)target, sm);
       }
       if (row_wide) {
         best = Best();
-        kept = 0.0f;
+        sums.kept = 0.0f;
         const Cut cut = cut_row(row, k, p, sm);
         row.each([&](float v, int i) {
           const uint32_t key = key_of(v);
           if (!(key > cut.key || (key == cut.key && i <= cut.last_tie))) return;
           const float w = row.weight(v);
           if (!(w > 0.0f && w >= minp)) return;
-          kept += w;
+          sums.kept += w;
           best.offer(w, noise[i], i);
         });
       } else {
@@ -574,23 +682,14 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
           if (e < from) continue;
           const float w = row.weight(listed_logit(e));
           if (!(w > 0.0f && w >= minp)) continue;
-          kept += w;
+          listed += row.mass(w);  // an integer: the list's order is no fixed one
           best.offer(w, noise[listed_index(e)], listed_index(e));
         }
       }
-      total = (double)kept;
-    } else {
-      float kept = 0.0f;
-      row.each([&](float v, int i) {
-        if (masked(v)) return;
-        const float w = row.weight(v);
-        if (!(w > 0.0f && w >= minp)) return;
-        kept += w;
-        best.offer(w, noise[i], i);
-      });
-      total = (double)kept;
     }
-    total = block_sum(total, sm);
+    double kept = (double)sums.kept, none = 0.0;
+    block_sums(kept, none, listed, sm);
+    total = kept + (double)listed / (double)unit;
     best.block(sm);
   }
   if (threadIdx.x == 0) {

@@ -401,11 +401,16 @@ def test_sampling_of_spread_logits_beyond_the_exponent_range():
                   top_p=[0.9, 0.9, 0.9, 0.999], top_k=[0, 10, 0, 0])
 
 
-def test_sampling_repeats_bit_for_bit():
+@pytest.mark.parametrize("name", ["top_p", "top_k", "both", "none"])
+def test_sampling_repeats_bit_for_bit(name):
     x, noise, _ = _logits(16, 12345, "bf16", 21)
-    kw = dict(top_p=np.linspace(0.5, 0.99, 16), temperature=np.linspace(0.5, 1.5, 16))
+    kw = dict(temperature=np.linspace(0.5, 1.5, 16))
+    if name in ("top_p", "both"):
+        kw["top_p"] = np.linspace(0.5, 0.99, 16)
+    if name in ("top_k", "both"):
+        kw["top_k"] = np.arange(5, 800, 50)
     first = _sample(x, noise, "bf16", **kw)
-    for _ in range(3):
+    for _ in range(10):
         again = _sample(x, noise, "bf16", **kw)
         assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
 
