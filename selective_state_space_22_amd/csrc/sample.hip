@@ -24,6 +24,7 @@ constexpr uint32_t kMasked = 0x007fffffu;  // key of -inf; NaN takes it too
 constexpr int kBins = 2048;
 constexpr float kBinsPerUnit = 64.0f;
 constexpr int kList = 2048;        // elements that the exact search holds
+constexpr int kFew = 256;          // elements that it ranks in one go
 constexpr int kCacheVecs = 7168;   // 16-byte pieces of the row kept in LDS
 constexpr int kMaximaTopK = 512;   // top_k up to which the threads' maxima bracket the end
 
@@ -58,7 +59,7 @@ struct Shared {
   uint32_t word[kWaves];
   float score[kWaves];
   unsigned long long before, found;
-  uint32_t digit, listed;
+  uint32_t digit, listed, bound;
   int bin, cut_index;
 };
 
@@ -73,6 +74,7 @@ struct Row {
   uint32_t mkey;  // key of the largest logit
   float m, temperature, to_bin;
   float unit;     // masses are round(w * unit)
+  int ibits;      // bits of an index
 
   __device__ __forceinline__ void set(const IO* row, int v) {
     x = row;
@@ -140,6 +142,20 @@ struct Row {
   // NaN for a NaN; and the weight from it, to some 1e-6: for sums, and to tell whether an
   // element can matter.
   __device__ __forceinline__ float distance(float v) const { return (m - v) * to_bin; }
+  // An element in the list: its key above the falling index, no bit more than they need, so
+  // that the exact search takes few steps.
+  static constexpr int kKeyShift = sizeof(IO) == 2 ? 16 : 0;  // a bf16's key has 16 bits
+  __device__ __forceinline__ unsigned long long entry(float v, int i) const {
+    return (unsigned long long)(key_of(v) >> kKeyShift) << ibits | (uint32_t)((1 << ibits) - 1 - i);
+  }
+  __device__ __forceinline__ float entry_logit(unsigned long long e) const {
+    const float v = logit_of((uint32_t)(e >> ibits) << kKeyShift);
+    return kKeyShift == 0 ? v : __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+  }
+  __device__ __forceinline__ int entry_index(unsigned long long e) const {
+    return (1 << ibits) - 1 - (int)((uint32_t)e & (uint32_t)((1 << ibits) - 1));
+  }
+  __device__ __forceinline__ uint64_t entry_mass(unsigned long long e) const { return mass(weight(entry_logit(e))); }
   static __device__ __forceinline__ float rough_weight(float d) { return ex2(d * (-kLog2e / kBinsPerUnit)); }
 };
 
@@ -198,10 +214,6 @@ struct Best {
     const float s = w / noise;
     take(s != s ? -__builtin_inff() : s, i);
   }
-  // Whether an element of about that weight may be better: false only where it is not.
-  __device__ __forceinline__ bool may(float rough, float noise) const {
-    return !(rough * rcp(noise) < __builtin_fmaf(-1.0e-4f, fabsf(score), score));
-  }
   __device__ __forceinline__ void block(Shared& sm) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
@@ -256,8 +268,8 @@ __device__ __forceinline__ int find_bin(float share, float target, Shared& sm) {
   return sm.bin;
 }
 
-// Appends (key, ~index) of the lanes that have one to the list.
-__device__ __forceinline__ void append(bool have, float v, int i, Shared& sm) {
+// Appends an entry of each lane that has one to the list.
+__device__ __forceinline__ void append(bool have, unsigned long long entry, Shared& sm) {
   const uint64_t m = __ballot(have);
   if (m == 0) return;
   const int lane = threadIdx.x & 63, first = __ffsll((unsigned long long)m) - 1;
@@ -265,11 +277,8 @@ __device__ __forceinline__ void append(bool have, float v, int i, Shared& sm) {
   if (lane == first) base = atomicAdd(&sm.listed, (uint32_t)__popcll(m));
   base = __shfl(base, first, 64);
   const uint32_t at = base + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-  if (have && at < kList) sm.list[at] = (unsigned long long)key_of(v) << 32 | (uint32_t)~i;
+  if (have && at < kList) sm.list[at] = entry;
 }
-
-__device__ __forceinline__ float listed_logit(unsigned long long e) { return logit_of((uint32_t)(e >> 32)); }
-__device__ __forceinline__ uint32_t listed_index(unsigned long long e) { return ~(uint32_t)e; }
 
 // The element of the first n of the list at which the measure of the elements >= it first
 // reaches target (1 <= target <= their total).  The measure is the count, or the mass of
@@ -305,7 +314,7 @@ __device__ __forceinline__ unsigned long long select_listed(const Row<IO>& row, 
       if (e >= from && (top == 64 || e >> top == prefix)) {
         const uint32_t d = (uint32_t)(e >> s) & ((1u << width) - 1);
         atomicAdd(&sm.count[d], 1u);
-        if (MASS) atomicAdd(&sm.mass[d], (unsigned long long)row.mass(row.weight(listed_logit(e))));
+        if (MASS) atomicAdd(&sm.mass[d], (unsigned long long)row.entry_mass(e));
       }
     }
     __syncthreads();
@@ -350,6 +359,55 @@ __device__ __forceinline__ unsigned long long select_listed(const Row<IO>& row, 
     }
     __syncthreads();
   }
+}
+
+// The same for a list of n <= kFew, without steps: each entry's rank is counted, and the
+// masses are summed in the ranks' order (by each wave for itself).  The element with which
+// the first `most` entries end or, if that is asked for, at which their mass reaches target
+// (0: the share p of it).
+template <typename IO>
+__device__ __forceinline__ unsigned long long end_of_few(const Row<IO>& row, int n, uint32_t most, bool by_mass,
+                                                         uint64_t target, float p, Shared& sm) {
+  constexpr int kParts = kThreads / kFew, kPart = kFew / kParts;
+  unsigned long long* sorted = sm.list + kFew;
+  const int i = threadIdx.x % kFew, part = threadIdx.x / kFew, lane = threadIdx.x & 63;
+  if (threadIdx.x < kFew) sm.count[threadIdx.x] = 0, sm.mass[threadIdx.x] = 0;
+  __syncthreads();
+  const unsigned long long e = i < n ? sm.list[i] : 0;
+  uint32_t rank = 0;
+  const int end = min(n, (part + 1) * kPart);
+  for (int j = part * kPart; j < end; ++j) rank += sm.list[j] > e;
+  if (i < n && rank) atomicAdd(&sm.count[i], rank);
+  __syncthreads();
+  if (part == 0 && i < n) {
+    rank = sm.count[i];
+    sorted[rank] = e;
+    if (by_mass && rank < most) sm.mass[rank] = row.entry_mass(e);
+  }
+  __syncthreads();
+  const uint32_t last = min((uint32_t)n, most) - 1;
+  if (!by_mass) return sorted[last];
+  unsigned long long h[kFew / 64], incl = 0;
+#pragma unroll
+  for (int j = 0; j < kFew / 64; ++j) incl += h[j] = sm.mass[kFew / 64 * lane + j];
+  const unsigned long long mine = incl;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const unsigned long long y = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += y;
+  }
+  if (target == 0) {
+    const unsigned long long sum = __shfl(incl, 63, 64);
+    target = (uint64_t)__builtin_ceil((double)p * (double)sum);
+    target = target < 1 ? 1 : (target > sum ? sum : target);
+  }
+  const uint64_t reach = __ballot(incl >= target);
+  const int at = reach == 0 ? 63 : __ffsll((unsigned long long)reach) - 1;
+  unsigned long long b = incl - mine;
+  int j = 0;
+#pragma unroll
+  for (int q = 0; q < kFew / 64 - 1; ++q) b += h[q], j += b < target;
+  return sorted[min((uint32_t)__shfl(kFew / 64 * lane + j, at, 64), last)];
 }
 
 // ---------------------------------------------------------------- selection over the whole row
@@ -469,90 +527,168 @@ __device__ Cut cut_row(const Row<IO>& row, int64_t k, float p, Shared& sm) {
 
 // ---------------------------------------------------------------- scoring
 
-// One pass over the row: elements at distances below lo are scored (those of at least minp)
-// and summed, those from lo up to below hi are listed, the rest is summed too.  Sums take
-// the rough weights, a score that may be the best the exact one.  kBatch pieces of the row
-// at a time: their noise is in flight together, and so are the next pieces.
+// Limits of m - x for one pass over the row.  Below `sure` an element is scored, from there
+// up to below `near` if its exact weight is large enough, from `lo` up to below `hi` it is
+// listed (sure <= near <= lo <= hi).
+struct Limits {
+  float sure, near, lo, hi;
+  bool lists;
+};
+// Sums of rough weights: of what lies below lo, of the scored elements, of all.
 struct Sums {
-  float above = 0.0f, kept = 0.0f, rest = 0.0f;  // of distances below lo, of the scored ones, from hi on
+  float above = 0.0f, kept = 0.0f, all = 0.0f;
 };
 
+// Sixteen elements to a thread at a time: rough weights, then the noise of the pieces that
+// have an element to be scored, the next pieces underway meanwhile, then the question whether
+// a weight w exceeds its noise times a bound a little below the best rough score that any
+// wave has published, one multiply-add to an element.  Where one does, rough scores are worked out,
+// and the exact form (an exponential and a division) for the elements that pass the raised bound.
 template <typename IO>
-__device__ __forceinline__ void score_row(const Row<IO>& row, float lo, float hi, float minp, const float* noise,
+__device__ __forceinline__ void score_row(const Row<IO>& row, const Limits& at, float minp, const float* noise,
                                           Sums& sums, Best& best, Shared& sm) {
   constexpr int VEC = Row<IO>::VEC, kBatch = 16 / VEC;
+  constexpr uint32_t kNone = sizeof(IO) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
   typedef float Noise4 __attribute__((ext_vector_type(4), aligned(4)));
-  // the rough weight of an element that is scored, else -1
-  auto first = [&](float v, int i) {
-    const float d = row.distance(v);
-    const float w = Row<IO>::rough_weight(d);
-    append(d >= lo && d < hi, v, i, sm);
-    const bool in = d < lo;
-    sums.above += in ? w : 0.0f;
-    sums.rest += d >= hi ? w : 0.0f;  // (a NaN is in none, an infinite distance weighs 0)
-    bool take = in && w >= minp;
-    if (fabsf(w - minp) < 1.0e-5f * minp) take = in && row.weight(v) >= minp;
-    sums.kept += take ? w : 0.0f;
-    return take ? w : -1.0f;
-  };
-  auto second = [&](float rough, float v, float e, int i) {
-    if (rough < 0.0f || !best.may(rough, e)) return;
+  const int tid = threadIdx.x;
+  const float to_exponent = row.to_bin * (-kLog2e / kBinsPerUnit);
+  const uint32_t lo_bits = __float_as_uint(at.lo), span = __float_as_uint(at.hi) - lo_bits;
+  float bound = 0.0f, zone = 0.0f;
+  Noise4 e[4];  // (that of pieces without an element to be scored: whatever was there)
+#pragma unroll
+  for (int c = 0; c < 4; ++c) e[c] = Noise4{1.0f, 1.0f, 1.0f, 1.0f};
+  auto exact = [&](float v, float n, int i, bool counted) {
     const float w = row.weight(v);
-    if (w > 0.0f) best.offer(w, e, i);
+    if (!(w > 0.0f && w >= minp)) return;
+    if (!counted) zone += w;
+    best.offer(w, n, i);
   };
-  auto fetch = [&](uint4 (&v)[kBatch], int j0) {
+  auto fetch = [&](uint4 (&v)[kBatch], int base) {
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
-      const int j = j0 + q * kThreads;
-      if (j < row.nvec) v[q] = j < row.cached ? row.cache[j] : row.vecs[j];
+      const int first = base + q * kThreads, j = first + tid;
+      v[q] = make_uint4(kNone, kNone, kNone, kNone);
+      if (first < row.cached) {  // (a multiple of the workgroup, or the whole row)
+        if (j < row.nvec) v[q] = row.cache[j];
+      } else if (j < row.nvec) v[q] = row.vecs[j];
     }
   };
+  auto index = [&](int base, int c) { return row.head + (base + tid + c / VEC * kThreads) * VEC + c % VEC; };
   uint4 next[kBatch];
-  fetch(next, threadIdx.x);
-  for (int j0 = threadIdx.x; j0 < row.nvec; j0 += kBatch * kThreads) {
+  fetch(next, 0);
+  for (int base = 0; base < row.nvec; base += kBatch * kThreads) {
     uint4 v[kBatch];
-    float w[kBatch][VEC];
-    Noise4 e[kBatch][VEC / 4];
+    float w[16];
+    uint32_t listed = 0;  // bit 15 - c: element c
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       v[q] = next[q];
-      const int j = j0 + q * kThreads, i = row.head + j * VEC;
-      if (j >= row.nvec) continue;
-      bool any = false;
+      float least = 3.0e38f;
 #pragma unroll
       for (int c = 0; c < VEC; ++c) {
-        w[q][c] = first(Row<IO>::element(v[q], c), i + c);
-        any |= w[q][c] >= 0.0f;
+        const float d = fminf(row.m - Row<IO>::element(v[q], c), 3.0e38f);  // (NaN: no weight)
+        const float rough = ex2(d * to_exponent);
+        least = fminf(least, d);
+        sums.all += rough;
+        w[q * VEC + c] = d < at.sure ? rough : 0.0f;
+        sums.kept += w[q * VEC + c];
+        listed = listed + listed + (__float_as_uint(d) - lo_bits < span ? 1u : 0u);
+      }
+      if (least < at.sure) {
+        const int i = index(base, q * VEC);
+#pragma unroll
+        for (int c = 0; c < VEC / 4; ++c)
+          e[q * (VEC / 4) + c] = *reinterpret_cast<const Noise4*>(noise + i + 4 * c);
+      }
+    }
+    if (at.lists) {
+      while (__any(listed != 0)) {
+        const int c = 15 - (31 - __clz((int)(listed | 1u)));
+        uint32_t word = 0;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) word = c * (int)sizeof(IO) / 4 == q * 4 + k ? u[k] : word;
+        }
+        float x = __uint_as_float(word);
+        if constexpr (VEC == 8) x = c & 1 ? bf16_hi(word) : bf16_lo(word);
+        append(listed != 0, row.entry(x, index(base, c)), sm);
+        listed &= ~(1u << (15 - c));
+      }
+      if (at.sure < at.lo) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float d = row.m - Row<IO>::element(v[c / VEC], c % VEC);
+          sums.above += d >= at.sure && d < at.lo ? ex2(d * to_exponent) : 0.0f;
+        }
+      }
+    }
+    fetch(next, base + kBatch * kThreads);
+    bound = fmaxf(bound, __uint_as_float(*(volatile uint32_t*)&sm.bound));
+    float over = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) over = fmaxf(over, __builtin_fmaf(-bound, e[c / 4][c % 4], w[c]));
+    if (__any(over > 0.0f)) {
+      float score[16], top = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        score[c] = w[c] > 0.0f ? w[c] * rcp(e[c / 4][c % 4]) : -__builtin_inff();
+        top = fmaxf(top, score[c]);
+      }
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+      // (an infinite score leaves the bound as it is)
+      bound = fmaxf(bound, __builtin_fmaf(-1.0e-4f, top, top));
+      if ((tid & 63) == 0) atomicMax(&sm.bound, __float_as_uint(bound));
+      uint32_t which = 0;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) which |= w[c] > 0.0f && !(score[c] < bound) ? 1u << c : 0u;
+      while (which != 0) {
+        const int i = index(base, __ffs((int)which) - 1);
+        exact(row.at(i), noise[i], i, true);
+        which &= which - 1;
+      }
+    }
+    if (at.sure < at.near) {
+      bool any = false;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float d = row.m - Row<IO>::element(v[c / VEC], c % VEC);
+        any |= d >= at.sure && d < at.near;
       }
       if (any) {
-#pragma unroll
-        for (int c = 0; c < VEC / 4; ++c) e[q][c] = *reinterpret_cast<const Noise4*>(noise + i + 4 * c);
+#pragma unroll 1
+        for (int c = 0; c < 16; ++c) {
+          const int i = index(base, c);
+          if (i >= row.head + row.nvec * VEC) break;
+          const float x = row.at(i), d = row.m - x;
+          if (d >= at.sure && d < at.near) exact(x, noise[i], i, false);
+        }
       }
     }
-    fetch(next, j0 + kBatch * kThreads);
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const int j = j0 + q * kThreads, i = row.head + j * VEC;
-      if (j >= row.nvec) continue;
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) second(w[q][c], Row<IO>::element(v[q], c), e[q][c / 4][c % 4], i + c);
-    }
   }
-  row.edges([&](float v, int i) {
-    const float w = first(v, i);
-    if (w >= 0.0f) second(w, v, noise[i], i);
+  sums.above += sums.kept;
+  row.edges([&](float x, int i) {
+    const float d = fminf(row.m - x, 3.0e38f), rough = ex2(d * to_exponent);
+    sums.all += rough;
+    sums.above += d < at.lo ? rough : 0.0f;
+    append(__float_as_uint(d) - lo_bits < span, row.entry(x, i), sm);
+    if (d < at.near) exact(x, noise[i], i, false);
   });
+  sums.kept += zone;
 }
 
 // ---------------------------------------------------------------- the row
 
 template <typename IO>
-__global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, float unit) {
+__global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, float unit, int ibits) {
   __shared__ Shared sm;
   const int64_t r = blockIdx.x;
   Row<IO> row;
   row.set((const IO*)a.logits + r * a.V, (int)a.V);
   row.unit = unit;
+  row.ibits = ibits;
   row.cache = sm.cache;
   row.cached = row.nvec < kCacheVecs ? row.nvec : kCacheVecs;
   const float* noise = a.noise + r * a.V;
@@ -564,6 +700,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
   row.temperature = t > 0.0f ? t : 1.0f;
   row.to_bin = kBinsPerUnit / row.temperature;
 
+  if (threadIdx.x == 0) sm.bound = 0;
   // the largest logit (a NaN is never the larger), the thread's and the row's
   float mine = -__builtin_inff();
   row.template ahead<8>(0, [&](const uint4& v, int j) {
@@ -595,7 +732,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
     const bool want_k = k > 0 && k < row.V, want_p = p < 1.0f;
     float lo = 0.0f, hi = -1.0f;  // distances below lo stay, those from lo up to below hi are listed
     // (an infinite maximum has no distances; its equals are all that has a weight)
-    bool row_wide = row.m > 3.4028235e38f;
+    bool row_wide = row.m > 3.4028235e38f || row.to_bin > 3.4028235e38f;
     if (row_wide) {
       clear_bins(sm);
     } else if (want_k) {
@@ -628,27 +765,37 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
         }
       });
       const int b = find_bin<true>(p, 0.0f, sm);
-      lo = (float)(b - 1), hi = (float)(b + 2);  // (a bin to either side for the rounding of the sums)
+      lo = (float)(b > 0 ? b - 1 : 0), hi = (float)(b + 2);  // (a bin to either side for the rounding of the sums)
       row_wide = b == kBins;
     }
     if (!want_k && !want_p && !row_wide) lo = hi = __builtin_inff();
     Sums sums;
     uint64_t listed = 0;  // mass of the listed elements that stay
     if (!row_wide) {
-      if (want_k) row.each([&](float v, int i) { append(row.distance(v) < hi, v, i, sm); });
-      else score_row(row, lo, hi, minp, noise, sums, best, sm);
+      if (want_k) row.each([&](float v, int i) { append(row.distance(v) < hi, row.entry(v, i), sm); });
+      else {
+        // the exact test of min_p for what lies a hundredth of a bin about its limit; weights
+        // below e^-80 are worked out exactly too, and those below e^-87 are 0
+        const float limit = fminf(-logf(minp) * kBinsPerUnit, 83.5f * kBinsPerUnit);
+        const float margin = minp > 0.0f && limit < 83.5f * kBinsPerUnit ? 0.01f : 4.0f * kBinsPerUnit;
+        const float one = 1.0f / row.to_bin, end = lo * one;
+        score_row(row, {fminf((limit - margin) * one, end), fminf((limit + margin) * one, end), end, hi * one, want_p},
+                  minp, noise, sums, best, sm);
+      }
     }
     if (want_k || want_p || row_wide) {
       __syncthreads();
       const int n = (int)sm.listed;
       row_wide |= n > kList;
       unsigned long long from = 0;  // listed elements >= from stay
-      if (!row_wide && want_k) {
+      if (!row_wide && want_k && n <= kFew) {
+        from = end_of_few(row, n, (uint32_t)min((int64_t)k, (int64_t)kFew), want_p, 0, p, sm);
+      } else if (!row_wide && want_k) {
         if (n > k) from = select_listed<false>(row, n, 0ull, (uint64_t)k, sm);
         if (want_p) {
           uint64_t sum = 0;
           for (int i = threadIdx.x; i < n; i += kThreads)
-            if (sm.list[i] >= from) sum += row.mass(row.weight(listed_logit(sm.list[i])));
+            if (sm.list[i] >= from) sum += row.entry_mass(sm.list[i]);
           sum = block_sum(sum, sm);
           uint64_t target = (uint64_t)__builtin_ceil((double)p * (double)sum);
           target = target < 1 ? 1 : (target > sum ? sum : target);
@@ -656,17 +803,30 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
         }
       } else if (!row_wide) {
         uint64_t sum = 0;
-        for (int i = threadIdx.x; i < n; i += kThreads) sum += row.mass(row.weight(listed_logit(sm.list[i])));
-        double over = (double)sums.above, below = (double)sums.rest;
-        block_sums(over, below, sum, sm);
-        const double whole = over + (double)sum / (double)unit + below;
+        for (int i = threadIdx.x; i < n; i += kThreads) sum += row.entry_mass(sm.list[i]);
+        double over = (double)sums.above, whole = (double)sums.all;
+        block_sums(over, whole, sum, sm);
         const double target = __builtin_ceil(((double)p * whole - over) * (double)unit);
         if (target < 1.0 || target > (double)sum) row_wide = true;  // the end is not in the list
+        else if (n <= kFew) from = end_of_few(row, n, kFew, true, (uint64_t)target, p, sm);
         else from = select_listed<true>(row, n, 0ull, (uint64_t)target, sm);
       }
+      if (!row_wide) {
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+          const unsigned long long e = sm.list[i];
+          if (e < from) continue;
+          const float w = row.weight(row.entry_logit(e));
+          if (!(w > 0.0f && w >= minp)) continue;
+          listed += row.mass(w);  // an integer: the list's order is no fixed one
+          best.offer(w, noise[row.entry_index(e)], row.entry_index(e));
+        }
+      }
+    }
+    while (true) {
       if (row_wide) {
         best = Best();
         sums.kept = 0.0f;
+        listed = 0;
         const Cut cut = cut_row(row, k, p, sm);
         row.each([&](float v, int i) {
           const uint32_t key = key_of(v);
@@ -676,21 +836,16 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
           sums.kept += w;
           best.offer(w, noise[i], i);
         });
-      } else {
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-          const unsigned long long e = sm.list[i];
-          if (e < from) continue;
-          const float w = row.weight(listed_logit(e));
-          if (!(w > 0.0f && w >= minp)) continue;
-          listed += row.mass(w);  // an integer: the list's order is no fixed one
-          best.offer(w, noise[listed_index(e)], listed_index(e));
-        }
       }
+      double kept = (double)sums.kept, none = 0.0;
+      uint64_t mass = listed;
+      block_sums(kept, none, mass, sm);
+      total = kept + (double)mass / (double)unit;
+      best.block(sm);
+      if (best.at != 0xffffffffu || row_wide) break;
+      row_wide = true;  // no score above -inf was among the sure ones: all of them count
+      __syncthreads();
     }
-    double kept = (double)sums.kept, none = 0.0;
-    block_sums(kept, none, listed, sm);
-    total = kept + (double)listed / (double)unit;
-    best.block(sm);
   }
   if (threadIdx.x == 0) {
     a.tokens[r] = best.at;
@@ -706,8 +861,8 @@ hipError_t launch_sample(const SampleArgs& a, int io, void*, hipStream_t st) {
   int bits = 0;
   while ((int64_t(1) << bits) < a.V) ++bits;
   const float unit = __builtin_ldexpf(1.0f, 62 - bits < 44 ? 62 - bits : 44);
-  if (io == kIoBF16) hipLaunchKernelGGL(sample_row_kernel<uint16_t>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, a, unit);
-  else hipLaunchKernelGGL(sample_row_kernel<float>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, a, unit);
+  if (io == kIoBF16) hipLaunchKernelGGL(sample_row_kernel<uint16_t>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, a, unit, bits);
+  else hipLaunchKernelGGL(sample_row_kernel<float>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, a, unit, bits);
   return hipGetLastError();
 }
 
