@@ -233,15 +233,17 @@ struct Best {
 __device__ __forceinline__ void clear_bins(Shared& sm) {
   __syncthreads();  // sm.bin has been read
   for (int i = threadIdx.x; i < kBins; i += kThreads) sm.hist[i] = 0;
-  if (threadIdx.x == 0) sm.bin = kBins, sm.listed = 0;
+  if (threadIdx.x == 0) sm.bin = 4 * kBins, sm.listed = 0;
   __syncthreads();
 }
 
 // The first bin up to which the bins' measure reaches `target` (kBins: none does).  MASS: a
 // bin holds the sum of e^{(bin - 64 d) / 64} 2^14 of its elements, its mass but for a common
-// factor of the bin; else their count.
+// factor of the bin; else their count.  before and after: whether the masses, whose rounding
+// is some 4e-5 of the total, leave it open that it is the bin before or after.
 template <bool MASS>
-__device__ __forceinline__ int find_bin(float share, float target, Shared& sm) {
+__device__ __forceinline__ int find_bin(float share, float target, int& before, int& after, Shared& sm) {
+  constexpr float kSlack = 1.0e-4f;
   __syncthreads();
   const int b = 2 * threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float scale = MASS ? ex2(-(float)b * (kLog2e / kBinsPerUnit)) : 1.0f;
@@ -263,9 +265,19 @@ __device__ __forceinline__ int find_bin(float share, float target, Shared& sm) {
   }
   const float want = MASS ? share * total : target;
   const float end = below + incl, start = end - v0 - v1;
-  if (end >= want) atomicMin(&sm.bin, start + v0 >= want ? b : b + 1);
+  if (end >= want) {
+    const bool second = start + v0 < want;
+    int bits = (second ? b + 1 : b) * 4;
+    if (MASS) {
+      const float from = second ? start + v0 : start, to = second ? end : start + v0;
+      bits |= (want - from < kSlack * total ? 2 : 0) | (to - want < kSlack * total ? 1 : 0);
+    }
+    atomicMin(&sm.bin, bits);
+  }
   __syncthreads();
-  return sm.bin;
+  const int bits = sm.bin;
+  before = bits >> 1 & 1, after = bits & 1;
+  return bits >> 2;
 }
 
 // Appends an entry of each lane that has one to the list.
@@ -730,6 +742,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
     total = 1.0;
   } else {
     const bool want_k = k > 0 && k < row.V, want_p = p < 1.0f;
+    int before, after;
     float lo = 0.0f, hi = -1.0f;  // distances below lo stay, those from lo up to below hi are listed
     // (an infinite maximum has no distances; its equals are all that has a weight)
     bool row_wide = row.m > 3.4028235e38f || row.to_bin > 3.4028235e38f;
@@ -741,7 +754,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
       if (k <= kMaximaTopK) {  // k threads' maxima, so k elements, lie up to the bin
         const float d = row.distance(mine);
         if (d < (float)kBins) atomicAdd(&sm.hist[(int)d], 1u);
-        b = find_bin<false>(0.0f, (float)k, sm);
+        b = find_bin<false>(0.0f, (float)k, before, after, sm);
       }
       if (b == kBins) {
         clear_bins(sm);
@@ -749,7 +762,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
           const float d = row.distance(v);
           if (d < (float)kBins) atomicAdd(&sm.hist[(int)d], 1u);
         });
-        b = find_bin<false>(0.0f, (float)k, sm);
+        b = find_bin<false>(0.0f, (float)k, before, after, sm);
       }
       // fewer than k within the histogram's range: all that is not masked
       hi = b == kBins ? __builtin_inff() : (float)(b + 1);
@@ -764,8 +777,8 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
           atomicAdd(&sm.hist[b], (uint32_t)__builtin_fmaf(f, __builtin_fmaf(f, 8192.0f, -16384.0f), 16384.5f));
         }
       });
-      const int b = find_bin<true>(p, 0.0f, sm);
-      lo = (float)(b > 0 ? b - 1 : 0), hi = (float)(b + 2);  // (a bin to either side for the rounding of the sums)
+      const int b = find_bin<true>(p, 0.0f, before, after, sm);
+      lo = (float)(b > 0 ? b - before : 0), hi = (float)(b + 1 + after);
       row_wide = b == kBins;
     }
     if (!want_k && !want_p && !row_wide) lo = hi = __builtin_inff();
