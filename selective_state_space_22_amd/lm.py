@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import MambaError, _check_status, _io_dtype, _ptr, _stream, load_library
+from .binding import MambaError, _check_status, _io_dtype, _ptr, load_library
 
 MAMBA_GATED_STATE_CHUNK = 8
 
@@ -39,6 +39,23 @@ def _lib():
         getattr(lib, name).restype = I
     _typed = lib
     return lib
+
+
+# A call on one token is as long as its checks: a tensor that is as expected costs one condition here,
+# _ptr names what is wrong with any other (decode of 1 x 2560: 10.1 us a call with _ptr alone, 7.5 so).
+def _arg(t, name, dtype, shape, device):
+    """Device pointer of a contiguous tensor of that type, shape and device (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous() and t.numel():
+        return t.data_ptr()
+    return _ptr(t, name, dtype, shape, device)
+
+
+def _stream(device):
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _workspace(workspace, need, device):
@@ -90,10 +107,10 @@ def mamba_gated_scan_fwd(u, gate_a, gate_x, lam, z=None, h0=None, reset=None, c=
         states = torch.empty((batch, chunks, D), dtype=f32, device=dev)
     workspace, ws, ws_bytes = _workspace(workspace, lib.mamba_gated_scan_fwd_workspace_size(batch, L, D, io), dev)
     st = lib.mamba_gated_scan_fwd(
-        batch, L, D, io, _ptr(u, "u", t, shape), _ptr(gate_a, "gate_a", t, shape, dev),
-        _ptr(gate_x, "gate_x", t, shape, dev), _ptr(lam, "lam", f32, (D,), dev), c, _ptr(z, "z", t, shape, dev),
-        _reset_bytes(reset, (batch, L), dev), _ptr(h0, "h0", f32, (batch, D), dev), _ptr(out, "out", t, shape, dev),
-        _ptr(last_state, "last_state", f32, (batch, D), dev), _ptr(states, "states", f32, (batch, chunks, D), dev),
+        batch, L, D, io, _arg(u, "u", t, shape, dev), _arg(gate_a, "gate_a", t, shape, dev),
+        _arg(gate_x, "gate_x", t, shape, dev), _arg(lam, "lam", f32, (D,), dev), c, _arg(z, "z", t, shape, dev),
+        _reset_bytes(reset, (batch, L), dev), _arg(h0, "h0", f32, (batch, D), dev), _arg(out, "out", t, shape, dev),
+        _arg(last_state, "last_state", f32, (batch, D), dev), _arg(states, "states", f32, (batch, chunks, D), dev),
         ws, ws_bytes, _stream(dev))
     if st != 0:
         raise MambaError("mamba_gated_scan_fwd", st)
@@ -130,14 +147,14 @@ def mamba_gated_scan_bwd(u, gate_a, gate_x, lam, dout, z=None, h0=None, reset=No
     workspace, ws, ws_bytes = _workspace(workspace, lib.mamba_gated_scan_bwd_workspace_size(batch, L, D, io), dev)
 
     def gp(k):
-        return _ptr(g[k], k, like[k][1], like[k][0], dev) if k in g else None
+        return _arg(g[k], k, like[k][1], like[k][0], dev) if k in g else None
 
     st = lib.mamba_gated_scan_bwd(
-        batch, L, D, io, _ptr(u, "u", t, shape), _ptr(gate_a, "gate_a", t, shape, dev),
-        _ptr(gate_x, "gate_x", t, shape, dev), _ptr(lam, "lam", f32, (D,), dev), c, _ptr(z, "z", t, shape, dev),
-        _reset_bytes(reset, (batch, L), dev), _ptr(h0, "h0", f32, (batch, D), dev),
-        _ptr(states, "states", f32, (batch, chunks, D), dev), _ptr(dout, "dout", t, shape, dev),
-        _ptr(dlast_state, "dlast_state", f32, (batch, D), dev), gp("du"), gp("dgate_a"), gp("dgate_x"), gp("dlam"),
+        batch, L, D, io, _arg(u, "u", t, shape, dev), _arg(gate_a, "gate_a", t, shape, dev),
+        _arg(gate_x, "gate_x", t, shape, dev), _arg(lam, "lam", f32, (D,), dev), c, _arg(z, "z", t, shape, dev),
+        _reset_bytes(reset, (batch, L), dev), _arg(h0, "h0", f32, (batch, D), dev),
+        _arg(states, "states", f32, (batch, chunks, D), dev), _arg(dout, "dout", t, shape, dev),
+        _arg(dlast_state, "dlast_state", f32, (batch, D), dev), gp("du"), gp("dgate_a"), gp("dgate_x"), gp("dlam"),
         gp("dz"), gp("dh0"), ws, ws_bytes, _stream(dev))
     if st != 0:
         raise MambaError("mamba_gated_scan_bwd", st)
@@ -157,9 +174,10 @@ def mamba_gated_state_update(state, u, gate_a, gate_x, lam, z=None, reset=None, 
     shape = (batch, D)
     out = torch.empty_like(u) if out is None else out
     st = lib.mamba_gated_state_update(
-        batch, D, io, _ptr(state, "state", f32, shape, dev), _ptr(u, "u", t, shape), _ptr(gate_a, "gate_a", t, shape, dev),
-        _ptr(gate_x, "gate_x", t, shape, dev), _ptr(lam, "lam", f32, (D,), dev), c, _ptr(z, "z", t, shape, dev),
-        _reset_bytes(reset, (batch,), dev), _ptr(out, "out", t, shape, dev), _stream(dev))
+        batch, D, io, _arg(state, "state", f32, shape, dev), _arg(u, "u", t, shape, dev),
+        _arg(gate_a, "gate_a", t, shape, dev), _arg(gate_x, "gate_x", t, shape, dev),
+        _arg(lam, "lam", f32, (D,), dev), c, _arg(z, "z", t, shape, dev),
+        _reset_bytes(reset, (batch,), dev), _arg(out, "out", t, shape, dev), _stream(dev))
     if st != 0:
         raise MambaError("mamba_gated_state_update", st)
     return out
@@ -175,8 +193,9 @@ def mamba_embed_fwd(ids, weight, scale=1.0, out=None):
     io, dev, t = _io_dtype(weight), weight.device, weight.dtype
     shape = (*ids.shape, D)
     out = torch.empty(shape, dtype=t, device=dev) if out is None else out
-    st = lib.mamba_embed_fwd(ids.numel(), V, D, io, _ptr(ids, "ids", torch.int64, None, dev), _ptr(weight, "weight"),
-                             scale, _ptr(out, "out", t, shape, dev), _stream(dev))
+    st = lib.mamba_embed_fwd(ids.numel(), V, D, io, _arg(ids, "ids", torch.int64, ids.shape, dev),
+                             _arg(weight, "weight", t, (V, D), dev), scale,
+                             _arg(out, "out", t, shape, dev), _stream(dev))
     if st != 0:
         raise MambaError("mamba_embed_fwd", st)
     return out
@@ -196,9 +215,9 @@ def mamba_embed_bwd(ids, dout, vocab, scale=1.0, dweight=None, workspace=None):
     n, V = ids.numel(), int(vocab)
     dweight = torch.empty((V, D), dtype=t, device=dev) if dweight is None else dweight
     workspace, ws, ws_bytes = _workspace(workspace, lib.mamba_embed_bwd_workspace_size(n, V, D, io), dev)
-    st = lib.mamba_embed_bwd(n, V, D, io, _ptr(ids, "ids", torch.int64, None, dev),
-                             _ptr(dout, "dout", t, (*ids.shape, D), dev), scale,
-                             _ptr(dweight, "dweight", t, (V, D), dev), ws, ws_bytes, _stream(dev))
+    st = lib.mamba_embed_bwd(n, V, D, io, _arg(ids, "ids", torch.int64, ids.shape, dev),
+                             _arg(dout, "dout", t, (*ids.shape, D), dev), scale,
+                             _arg(dweight, "dweight", t, (V, D), dev), ws, ws_bytes, _stream(dev))
     if st != 0:
         raise MambaError("mamba_embed_bwd", st)
     return dweight
@@ -223,11 +242,12 @@ def mamba_sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=
     if logprob is None and return_logprob:
         logprob = torch.empty((rows,), dtype=f32, device=dev)
     workspace, ws, ws_bytes = _workspace(workspace, lib.mamba_sample_workspace_size(rows, V, io), dev)
-    st = lib.mamba_sample(rows, V, io, _ptr(logits, "logits"), _ptr(noise, "noise", f32, (rows, V), dev),
-                          _ptr(temperature, "temperature", f32, (rows,), dev),
-                          _ptr(top_k, "top_k", torch.int32, (rows,), dev), _ptr(top_p, "top_p", f32, (rows,), dev),
-                          _ptr(min_p, "min_p", f32, (rows,), dev), _ptr(tokens, "tokens", torch.int64, (rows,), dev),
-                          _ptr(logprob, "logprob", f32, (rows,), dev), ws, ws_bytes, _stream(dev))
+    st = lib.mamba_sample(rows, V, io, _arg(logits, "logits", logits.dtype, (rows, V), dev),
+                          _arg(noise, "noise", f32, (rows, V), dev),
+                          _arg(temperature, "temperature", f32, (rows,), dev),
+                          _arg(top_k, "top_k", torch.int32, (rows,), dev), _arg(top_p, "top_p", f32, (rows,), dev),
+                          _arg(min_p, "min_p", f32, (rows,), dev), _arg(tokens, "tokens", torch.int64, (rows,), dev),
+                          _arg(logprob, "logprob", f32, (rows,), dev), ws, ws_bytes, _stream(dev))
     if st != 0:
         raise MambaError("mamba_sample", st)
     return tokens, logprob
