@@ -48,13 +48,18 @@ __device__ __forceinline__ float exp_accurate(float t) {
   return t < -87.0f ? 0.0f : __builtin_fmaf(r, lo * kLn2, r);
 }
 
+struct Three {
+  double a, b;
+  unsigned long long c;
+};
+
 struct Shared {
   uint4 cache[kCacheVecs];
   uint32_t hist[kBins];
   unsigned long long list[kList];
   unsigned long long mass[256];
   uint32_t count[256];
-  double dsum[2][kWaves];
+  Three three[kWaves];
   unsigned long long sum[kWaves];
   uint32_t word[kWaves];
   float score[kWaves];
@@ -91,27 +96,58 @@ struct Row {
     if constexpr (VEC == 8) return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
     else return __uint_as_float(w[e]);
   }
-  // f(logit, index) for the thread's elements: pieces in steps of the workgroup, then the
-  // elements before the first and after the last piece, one to a thread.
+  // The thread's pieces of a batch of N times the workgroup's, from piece `base` on; -inf past
+  // the last.
+  template <int N>
+  __device__ __forceinline__ void fetch(uint4 (&v)[N], int base) const {
+    constexpr uint32_t kNone = VEC == 8 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const int first = base + q * kThreads, j = first + (int)threadIdx.x;
+      v[q] = make_uint4(kNone, kNone, kNone, kNone);
+      if (first < cached) {  // (a multiple of the workgroup, or the whole row)
+        if (j < nvec) v[q] = cache[j];
+      } else if (j < nvec) v[q] = vecs[j];
+    }
+  }
+  // f(pieces, base, prefetch) for batch after batch of kElems elements to a thread; f calls
+  // prefetch() behind its own loads.  The loops are rolled: a short row takes a few batches in
+  // each pass, and fetching long code costs more than running it.  Eight elements: 256 rows of
+  // 128000 f32, top_p, take 83 us, with four 90, with sixteen 115 (registers spill); 64 rows of
+  // 50001 bf16 19.5 us, with sixteen 22.9.
+  static constexpr int kElems = 8, kBatch = kElems / VEC;
+  template <typename F>
+  __device__ __forceinline__ void batches(F f) const {
+    uint4 next[kBatch];
+    fetch(next, 0);
+#pragma unroll 1
+    for (int base = 0; base < nvec; base += kBatch * kThreads) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) v[q] = next[q];
+      f(v, base, [&] { fetch(next, base + kBatch * kThreads); });
+    }
+  }
+  // Index of element c of a batch.
+  __device__ __forceinline__ int index(int base, int c) const {
+    return head + (base + (int)threadIdx.x + c / VEC * kThreads) * VEC + c % VEC;
+  }
+  // f(logit, index) for the thread's elements: the batches', where some past the row's end come
+  // with -inf, then those before the first and after the last piece, one to a thread.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    for (int j = threadIdx.x; j < cached; j += kThreads) {
-      const uint4 v = cache[j];
+    batches([&](const uint4 (&v)[kBatch], int base, auto prefetch) {
+      prefetch();
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) f(element(v, e), head + j * VEC + e);
-    }
-    // cached is a multiple of the workgroup or the whole row: the thread's pieces go on
-    ahead<4>(cached, [&](const uint4& v, int j) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) f(element(v, e), head + j * VEC + e);
+      for (int c = 0; c < kElems; ++c) f(element(v[c / VEC], c % VEC), index(base, c));
     });
     edges(f);
   }
-  // f(piece, its number) for the thread's pieces from number `from` on, the next N in flight.
+  // f(piece, its number) for the thread's pieces, the next N in flight.
   template <int N, typename F>
-  __device__ __forceinline__ void ahead(int from, F f) const {
+  __device__ __forceinline__ void ahead(F f) const {
     uint4 v[N];
-    int j = from + (int)threadIdx.x;
+    int j = (int)threadIdx.x;
 #pragma unroll
     for (int q = 0; q < N; ++q)
       if (j + q * kThreads < nvec) v[q] = vecs[j + q * kThreads];
@@ -161,46 +197,43 @@ struct Row {
 
 __device__ __forceinline__ bool masked(float v) { return !(v > -__builtin_inff()); }
 
+// Reductions over the workgroup; slots: one to a wave, read again before it is written anew.
+template <typename T, typename F>
+__device__ __forceinline__ T block_all(T v, T* slots, F f) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = f(v, (T)__shfl_xor(v, o, 64));
+  if (lane == 0) slots[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = slots[lane & (kWaves - 1)];
+#pragma unroll
+  for (int o = kWaves / 2; o > 0; o >>= 1) v = f(v, (T)__shfl_xor(v, o, 64));
+  __syncthreads();
+  return v;
+}
 __device__ __forceinline__ uint32_t block_max(uint32_t v, Shared& sm) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor(v, o, 64));
-  if ((threadIdx.x & 63) == 0) sm.word[threadIdx.x >> 6] = v;
-  __syncthreads();
-  uint32_t r = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) r = max(r, sm.word[w]);
-  __syncthreads();
-  return r;
+  return block_all(v, sm.word, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
-
 __device__ __forceinline__ uint64_t block_sum(uint64_t v, Shared& sm) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += (uint64_t)__shfl_xor((unsigned long long)v, o, 64);
-  if ((threadIdx.x & 63) == 0) sm.sum[threadIdx.x >> 6] = v;
-  __syncthreads();
-  uint64_t r = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) r += sm.sum[w];
-  __syncthreads();
-  return r;
+  return block_all((unsigned long long)v, sm.sum, [](unsigned long long a, unsigned long long b) { return a + b; });
 }
-
 // Sums of two numbers and of an integer at once.
-__device__ __forceinline__ void block_sums(double& a, double& b, uint64_t& c, Shared& sm) {
+__device__ __forceinline__ Three block_sums(Three v, Shared& sm) {
+  const int lane = threadIdx.x & 63;
+  auto add = [&](int o) {
+    v.a += __shfl_xor(v.a, o, 64);
+    v.b += __shfl_xor(v.b, o, 64);
+    v.c += __shfl_xor(v.c, o, 64);
+  };
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    a += __shfl_xor(a, o, 64);
-    b += __shfl_xor(b, o, 64);
-    c += (uint64_t)__shfl_xor((unsigned long long)c, o, 64);
-  }
-  const int wave = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 0) sm.dsum[0][wave] = a, sm.dsum[1][wave] = b, sm.sum[wave] = c;
+  for (int o = 32; o > 0; o >>= 1) add(o);
+  if (lane == 0) sm.three[threadIdx.x >> 6] = v;
   __syncthreads();
-  a = b = 0.0;
-  c = 0;
+  v = sm.three[lane & (kWaves - 1)];
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) a += sm.dsum[0][w], b += sm.dsum[1][w], c += sm.sum[w];
+  for (int o = kWaves / 2; o > 0; o >>= 1) add(o);
   __syncthreads();
+  return v;
 }
 
 // The best (score, lowest index) so far; a NaN score counts as -inf.
@@ -215,16 +248,21 @@ struct Best {
     take(s != s ? -__builtin_inff() : s, i);
   }
   __device__ __forceinline__ void block(Shared& sm) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
       const float s = __shfl_xor(score, o, 64);
-      const uint32_t i = __shfl_xor(at, o, 64);
-      take(s, i);
+      take(s, __shfl_xor(at, o, 64));
     }
-    if ((threadIdx.x & 63) == 0) sm.score[threadIdx.x >> 6] = score, sm.word[threadIdx.x >> 6] = at;
+    if (lane == 0) sm.score[threadIdx.x >> 6] = score, sm.word[threadIdx.x >> 6] = at;
     __syncthreads();
+    score = sm.score[lane & (kWaves - 1)], at = sm.word[lane & (kWaves - 1)];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) take(sm.score[w], sm.word[w]);
+    for (int o = kWaves / 2; o > 0; o >>= 1) {
+      const float s = __shfl_xor(score, o, 64);
+      take(s, __shfl_xor(at, o, 64));
+    }
+    __syncthreads();
   }
 };
 
@@ -292,12 +330,45 @@ __device__ __forceinline__ void append(bool have, unsigned long long entry, Shar
   if (have && at < kList) sm.list[at] = entry;
 }
 
+// Lists the elements of a batch that have their bit in `marks` (bit kElems - 1 - c: element c).
+template <typename IO>
+__device__ __forceinline__ void append_marked(const Row<IO>& row, const uint4 (&v)[Row<IO>::kBatch], int base,
+                                              uint32_t marks, Shared& sm) {
+  while (__any(marks != 0)) {
+    const int c = __clz((int)(marks | 1u)) - (32 - Row<IO>::kElems);
+    uint32_t word = 0;
+#pragma unroll
+    for (int k = 0; k < 4 * Row<IO>::kBatch; ++k) {
+      const uint32_t u[4] = {v[k / 4].x, v[k / 4].y, v[k / 4].z, v[k / 4].w};
+      word = c * (int)sizeof(IO) / 4 == k ? u[k % 4] : word;
+    }
+    float x = __uint_as_float(word);
+    if constexpr (sizeof(IO) == 2) x = c & 1 ? bf16_hi(word) : bf16_lo(word);
+    append(marks != 0, row.entry(x, row.index(base, c)), sm);
+    marks &= ~((1u << (Row<IO>::kElems - 1)) >> c);
+  }
+}
+
+// Lists the elements with m - x < end.
+template <typename IO>
+__device__ __forceinline__ void list_row(const Row<IO>& row, float end, Shared& sm) {
+  row.batches([&](const uint4 (&v)[Row<IO>::kBatch], int base, auto prefetch) {
+    prefetch();
+    uint32_t marks = 0;
+#pragma unroll
+    for (int c = 0; c < Row<IO>::kElems; ++c)
+      marks = marks + marks + (row.m - Row<IO>::element(v[c / Row<IO>::VEC], c % Row<IO>::VEC) < end ? 1u : 0u);
+    append_marked(row, v, base, marks, sm);
+  });
+  row.edges([&](float x, int i) { append(row.m - x < end, row.entry(x, i), sm); });
+}
+
 // The element of the first n of the list at which the measure of the elements >= it first
 // reaches target (1 <= target <= their total).  The measure is the count, or the mass of
 // the elements >= from.  Eight bits a step, from the first bit in which the elements differ.
-template <bool MASS, typename IO>
+template <typename IO>
 __device__ __forceinline__ unsigned long long select_listed(const Row<IO>& row, int n, unsigned long long from,
-                                                            uint64_t target, Shared& sm) {
+                                                            uint64_t target, bool by_mass, Shared& sm) {
   unsigned long long lo = ~0ull, hi = 0;
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const unsigned long long e = sm.list[i];
@@ -326,7 +397,7 @@ __device__ __forceinline__ unsigned long long select_listed(const Row<IO>& row, 
       if (e >= from && (top == 64 || e >> top == prefix)) {
         const uint32_t d = (uint32_t)(e >> s) & ((1u << width) - 1);
         atomicAdd(&sm.count[d], 1u);
-        if (MASS) atomicAdd(&sm.mass[d], (unsigned long long)row.entry_mass(e));
+        if (by_mass) atomicAdd(&sm.mass[d], (unsigned long long)row.entry_mass(e));
       }
     }
     __syncthreads();
@@ -336,7 +407,7 @@ __device__ __forceinline__ unsigned long long select_listed(const Row<IO>& row, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int d = 255 - 4 * lane - j;
-        incl += h[j] = MASS ? sm.mass[d] : (unsigned long long)sm.count[d];
+        incl += h[j] = by_mass ? sm.mass[d] : (unsigned long long)sm.count[d];
       }
       const unsigned long long mine = incl;
 #pragma unroll
@@ -373,28 +444,29 @@ __device__ __forceinline__ unsigned long long select_listed(const Row<IO>& row, 
   }
 }
 
-// The same for a list of n <= kFew, without steps: each entry's rank is counted, and the
+// The same for a list of n <= kFew, without steps (1 x 50000, top_k 50 and top_p: 22 us a call
+// in place of 31): each entry's rank is counted, and the
 // masses are summed in the ranks' order (by each wave for itself).  The element with which
 // the first `most` entries end or, if that is asked for, at which their mass reaches target
-// (0: the share p of it).
+// (0: the share p of it).  mass: that of the thread's first entry.
 template <typename IO>
 __device__ __forceinline__ unsigned long long end_of_few(const Row<IO>& row, int n, uint32_t most, bool by_mass,
-                                                         uint64_t target, float p, Shared& sm) {
-  constexpr int kParts = kThreads / kFew, kPart = kFew / kParts;
+                                                         uint64_t target, float p, uint64_t mass, Shared& sm) {
+  constexpr int kParts = kThreads / kFew;
   unsigned long long* sorted = sm.list + kFew;
   const int i = threadIdx.x % kFew, part = threadIdx.x / kFew, lane = threadIdx.x & 63;
   if (threadIdx.x < kFew) sm.count[threadIdx.x] = 0, sm.mass[threadIdx.x] = 0;
   __syncthreads();
   const unsigned long long e = i < n ? sm.list[i] : 0;
   uint32_t rank = 0;
-  const int end = min(n, (part + 1) * kPart);
-  for (int j = part * kPart; j < end; ++j) rank += sm.list[j] > e;
+#pragma unroll 4
+  for (int j = part; j < n; j += kParts) rank += sm.list[j] > e;
   if (i < n && rank) atomicAdd(&sm.count[i], rank);
   __syncthreads();
   if (part == 0 && i < n) {
     rank = sm.count[i];
     sorted[rank] = e;
-    if (by_mass && rank < most) sm.mass[rank] = row.entry_mass(e);
+    if (by_mass && rank < most) sm.mass[rank] = mass;
   }
   __syncthreads();
   const uint32_t last = min((uint32_t)n, most) - 1;
@@ -551,7 +623,7 @@ struct Sums {
   float above = 0.0f, kept = 0.0f, all = 0.0f;
 };
 
-// Sixteen elements to a thread at a time: rough weights, then the noise of the pieces that
+// kElems elements to a thread at a time: rough weights, then the noise of the pieces that
 // have an element to be scored, the next pieces underway meanwhile, then the question whether
 // a weight w exceeds its noise times a bound a little below the best rough score that any
 // wave has published, one multiply-add to an element.  Where one does, rough scores are worked out,
@@ -559,42 +631,26 @@ struct Sums {
 template <typename IO>
 __device__ __forceinline__ void score_row(const Row<IO>& row, const Limits& at, float minp, const float* noise,
                                           Sums& sums, Best& best, Shared& sm) {
-  constexpr int VEC = Row<IO>::VEC, kBatch = 16 / VEC;
-  constexpr uint32_t kNone = sizeof(IO) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+  constexpr int VEC = Row<IO>::VEC, kBatch = Row<IO>::kBatch;
   typedef float Noise4 __attribute__((ext_vector_type(4), aligned(4)));
   const int tid = threadIdx.x;
   const float to_exponent = row.to_bin * (-kLog2e / kBinsPerUnit);
   const uint32_t lo_bits = __float_as_uint(at.lo), span = __float_as_uint(at.hi) - lo_bits;
   float bound = 0.0f, zone = 0.0f;
-  Noise4 e[4];  // (that of pieces without an element to be scored: whatever was there)
+  Noise4 e[Row<IO>::kElems / 4];  // (that of pieces without an element to be scored: whatever was there)
 #pragma unroll
-  for (int c = 0; c < 4; ++c) e[c] = Noise4{1.0f, 1.0f, 1.0f, 1.0f};
-  auto exact = [&](float v, float n, int i, bool counted) {
+  for (int c = 0; c < Row<IO>::kElems / 4; ++c) e[c] = Noise4{1.0f, 1.0f, 1.0f, 1.0f};
+  auto exact = [&](float v, float n, int i, bool count) {
     const float w = row.weight(v);
     if (!(w > 0.0f && w >= minp)) return;
-    if (!counted) zone += w;
+    zone += count ? w : 0.0f;
     best.offer(w, n, i);
   };
-  auto fetch = [&](uint4 (&v)[kBatch], int base) {
+  row.batches([&](const uint4 (&v)[kBatch], int base, auto prefetch) {
+    float w[Row<IO>::kElems];
+    uint32_t listed = 0;  // marks of those to be listed
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
-      const int first = base + q * kThreads, j = first + tid;
-      v[q] = make_uint4(kNone, kNone, kNone, kNone);
-      if (first < row.cached) {  // (a multiple of the workgroup, or the whole row)
-        if (j < row.nvec) v[q] = row.cache[j];
-      } else if (j < row.nvec) v[q] = row.vecs[j];
-    }
-  };
-  auto index = [&](int base, int c) { return row.head + (base + tid + c / VEC * kThreads) * VEC + c % VEC; };
-  uint4 next[kBatch];
-  fetch(next, 0);
-  for (int base = 0; base < row.nvec; base += kBatch * kThreads) {
-    uint4 v[kBatch];
-    float w[16];
-    uint32_t listed = 0;  // bit 15 - c: element c
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      v[q] = next[q];
       float least = 3.0e38f;
 #pragma unroll
       for (int c = 0; c < VEC; ++c) {
@@ -607,86 +663,62 @@ __device__ __forceinline__ void score_row(const Row<IO>& row, const Limits& at, 
         listed = listed + listed + (__float_as_uint(d) - lo_bits < span ? 1u : 0u);
       }
       if (least < at.sure) {
-        const int i = index(base, q * VEC);
+        const int i = row.index(base, q * VEC);
 #pragma unroll
         for (int c = 0; c < VEC / 4; ++c)
           e[q * (VEC / 4) + c] = *reinterpret_cast<const Noise4*>(noise + i + 4 * c);
       }
     }
     if (at.lists) {
-      while (__any(listed != 0)) {
-        const int c = 15 - (31 - __clz((int)(listed | 1u)));
-        uint32_t word = 0;
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) word = c * (int)sizeof(IO) / 4 == q * 4 + k ? u[k] : word;
-        }
-        float x = __uint_as_float(word);
-        if constexpr (VEC == 8) x = c & 1 ? bf16_hi(word) : bf16_lo(word);
-        append(listed != 0, row.entry(x, index(base, c)), sm);
-        listed &= ~(1u << (15 - c));
-      }
+      append_marked(row, v, base, listed, sm);
       if (at.sure < at.lo) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < Row<IO>::kElems; ++c) {
           const float d = row.m - Row<IO>::element(v[c / VEC], c % VEC);
           sums.above += d >= at.sure && d < at.lo ? ex2(d * to_exponent) : 0.0f;
         }
       }
     }
-    fetch(next, base + kBatch * kThreads);
+    prefetch();
     bound = fmaxf(bound, __uint_as_float(*(volatile uint32_t*)&sm.bound));
     float over = 0.0f;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) over = fmaxf(over, __builtin_fmaf(-bound, e[c / 4][c % 4], w[c]));
+    for (int c = 0; c < Row<IO>::kElems; ++c) over = fmaxf(over, __builtin_fmaf(-bound, e[c / 4][c % 4], w[c]));
+    uint32_t which = 0, unsure = 0;
     if (__any(over > 0.0f)) {
-      float score[16], top = 0.0f;
+      float score[Row<IO>::kElems], top = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < Row<IO>::kElems; ++c) {
         score[c] = w[c] > 0.0f ? w[c] * rcp(e[c / 4][c % 4]) : -__builtin_inff();
         top = fmaxf(top, score[c]);
       }
-#pragma unroll
+#pragma unroll 1
       for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
       // (an infinite score leaves the bound as it is)
       bound = fmaxf(bound, __builtin_fmaf(-1.0e-4f, top, top));
       if ((tid & 63) == 0) atomicMax(&sm.bound, __float_as_uint(bound));
-      uint32_t which = 0;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) which |= w[c] > 0.0f && !(score[c] < bound) ? 1u << c : 0u;
-      while (which != 0) {
-        const int i = index(base, __ffs((int)which) - 1);
-        exact(row.at(i), noise[i], i, true);
-        which &= which - 1;
-      }
+      for (int c = 0; c < Row<IO>::kElems; ++c) which |= w[c] > 0.0f && !(score[c] < bound) ? 1u << c : 0u;
     }
     if (at.sure < at.near) {
-      bool any = false;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < Row<IO>::kElems; ++c) {
         const float d = row.m - Row<IO>::element(v[c / VEC], c % VEC);
-        any |= d >= at.sure && d < at.near;
-      }
-      if (any) {
-#pragma unroll 1
-        for (int c = 0; c < 16; ++c) {
-          const int i = index(base, c);
-          if (i >= row.head + row.nvec * VEC) break;
-          const float x = row.at(i), d = row.m - x;
-          if (d >= at.sure && d < at.near) exact(x, noise[i], i, false);
-        }
+        unsure |= d >= at.sure && d < at.near ? 1u << c : 0u;
       }
     }
-  }
+    for (uint32_t todo = which | unsure; todo != 0; todo &= todo - 1) {
+      const int c = __ffs((int)todo) - 1, i = row.index(base, c);
+      exact(row.at(i), noise[i], i, unsure >> c & 1);
+    }
+  });
   sums.above += sums.kept;
   row.edges([&](float x, int i) {
     const float d = fminf(row.m - x, 3.0e38f), rough = ex2(d * to_exponent);
     sums.all += rough;
     sums.above += d < at.lo ? rough : 0.0f;
     append(__float_as_uint(d) - lo_bits < span, row.entry(x, i), sm);
-    if (d < at.near) exact(x, noise[i], i, false);
+    if (d < at.near) exact(x, noise[i], i, true);
   });
   sums.kept += zone;
 }
@@ -715,7 +747,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
   if (threadIdx.x == 0) sm.bound = 0;
   // the largest logit (a NaN is never the larger), the thread's and the row's
   float mine = -__builtin_inff();
-  row.template ahead<8>(0, [&](const uint4& v, int j) {
+  row.template ahead<4>([&](const uint4& v, int j) {
     if (j < kCacheVecs) sm.cache[j] = v;
 #pragma unroll
     for (int e = 0; e < Row<IO>::VEC; ++e) mine = fmaxf(mine, Row<IO>::element(v, e));
@@ -732,14 +764,14 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
   }
 
   Best best;
-  double total = 0.0;  // mass of what stays
+  double total = 1.0;  // mass of what stays
+  float chosen = row.m;
   if (greedy) {
     uint32_t first = 0;
     row.each([&](float v, int i) {
       if (v == row.m) first = max(first, (uint32_t)~i);
     });
     best.at = ~block_max(first, sm);
-    total = 1.0;
   } else {
     const bool want_k = k > 0 && k < row.V, want_p = p < 1.0f;
     int before, after;
@@ -785,7 +817,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
     Sums sums;
     uint64_t listed = 0;  // mass of the listed elements that stay
     if (!row_wide) {
-      if (want_k) row.each([&](float v, int i) { append(row.distance(v) < hi, row.entry(v, i), sm); });
+      if (want_k) list_row(row, hi / row.to_bin, sm);
       else {
         // the exact test of min_p for what lies a hundredth of a bin about its limit; weights
         // below e^-80 are worked out exactly too, and those below e^-87 are 0
@@ -801,37 +833,43 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
       const int n = (int)sm.listed;
       row_wide |= n > kList;
       unsigned long long from = 0;  // listed elements >= from stay
-      if (!row_wide && want_k && n <= kFew) {
-        from = end_of_few(row, n, (uint32_t)min((int64_t)k, (int64_t)kFew), want_p, 0, p, sm);
-      } else if (!row_wide && want_k) {
-        if (n > k) from = select_listed<false>(row, n, 0ull, (uint64_t)k, sm);
-        if (want_p) {
-          uint64_t sum = 0;
+      const bool few = n <= kFew;
+      // the thread's first entry, its noise underway during the search
+      const int i0 = threadIdx.x;
+      const unsigned long long e0 = i0 < n && !row_wide ? sm.list[i0] : 0;
+      const float n0 = i0 < n && !row_wide ? noise[row.entry_index(e0)] : 1.0f;
+      const float w0 = row.weight(row.entry_logit(e0));
+      uint64_t target = (uint64_t)k;
+      // by counts, then (or only) by masses
+      for (bool by_mass = !want_k; !row_wide; by_mass = true) {
+        if (by_mass && !(few && want_k)) {
+          Three sum = {(double)sums.above, (double)sums.all, 0};
           for (int i = threadIdx.x; i < n; i += kThreads)
-            if (sm.list[i] >= from) sum += row.entry_mass(sm.list[i]);
-          sum = block_sum(sum, sm);
-          uint64_t target = (uint64_t)__builtin_ceil((double)p * (double)sum);
-          target = target < 1 ? 1 : (target > sum ? sum : target);
-          from = select_listed<true>(row, n, from, target, sm);
+            if (sm.list[i] >= from) sum.c += row.entry_mass(sm.list[i]);
+          sum = block_sums(sum, sm);
+          const double mass = (double)sum.c;
+          double need = __builtin_ceil(want_k ? (double)p * mass : ((double)p * sum.b - sum.a) * (double)unit);
+          if (want_k) need = fmin(fmax(need, 1.0), mass);
+          if (!(need >= 1.0 && need <= mass)) row_wide = true;  // the end is not in the list
+          target = (uint64_t)need;
         }
-      } else if (!row_wide) {
-        uint64_t sum = 0;
-        for (int i = threadIdx.x; i < n; i += kThreads) sum += row.entry_mass(sm.list[i]);
-        double over = (double)sums.above, whole = (double)sums.all;
-        block_sums(over, whole, sum, sm);
-        const double target = __builtin_ceil(((double)p * whole - over) * (double)unit);
-        if (target < 1.0 || target > (double)sum) row_wide = true;  // the end is not in the list
-        else if (n <= kFew) from = end_of_few(row, n, kFew, true, (uint64_t)target, p, sm);
-        else from = select_listed<true>(row, n, 0ull, (uint64_t)target, sm);
+        if (row_wide) break;
+        if (few) {
+          from = end_of_few(row, n, want_k ? (uint32_t)min(k, (int64_t)kFew) : kFew, want_p, want_k ? 0 : target, p,
+                            row.mass(w0), sm);
+          break;
+        }
+        if (by_mass || n > k) from = select_listed(row, n, from, target, by_mass, sm);
+        if (by_mass || !want_p) break;
       }
       if (!row_wide) {
         for (int i = threadIdx.x; i < n; i += kThreads) {
-          const unsigned long long e = sm.list[i];
+          const unsigned long long e = i == i0 ? e0 : sm.list[i];
           if (e < from) continue;
-          const float w = row.weight(row.entry_logit(e));
+          const float w = i == i0 ? w0 : row.weight(row.entry_logit(e));
           if (!(w > 0.0f && w >= minp)) continue;
           listed += row.mass(w);  // an integer: the list's order is no fixed one
-          best.offer(w, noise[row.entry_index(e)], row.entry_index(e));
+          best.offer(w, i == i0 ? n0 : noise[row.entry_index(e)], row.entry_index(e));
         }
       }
     }
@@ -850,19 +888,17 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
           best.offer(w, noise[i], i);
         });
       }
-      double kept = (double)sums.kept, none = 0.0;
-      uint64_t mass = listed;
-      block_sums(kept, none, mass, sm);
-      total = kept + (double)mass / (double)unit;
       best.block(sm);
+      if (best.at != 0xffffffffu) chosen = row.at(best.at);
+      const Three sum = block_sums(Three{(double)sums.kept, 0.0, listed}, sm);
+      total = sum.a + (double)sum.c / (double)unit;
       if (best.at != 0xffffffffu || row_wide) break;
       row_wide = true;  // no score above -inf was among the sure ones: all of them count
-      __syncthreads();
     }
   }
   if (threadIdx.x == 0) {
     a.tokens[r] = best.at;
-    if (a.logprob) a.logprob[r] = row.scaled(row.at(best.at)) - logf((float)total);
+    if (a.logprob) a.logprob[r] = row.scaled(chosen) - logf((float)total);
   }
 }
 
