@@ -892,8 +892,8 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
       if (best.at != 0xffffffffu) chosen = row.at(best.at);
       const Three sum = block_sums(Three{(double)sums.kept, 0.0, listed}, sm);
       total = sum.a + (double)sum.c / (double)unit;
-      if (best.at != 0xffffffffu || row_wide) break;
-      row_wide = true;  // no score above -inf was among the sure ones: all of them count
+      if (best.score > 0.0f || row_wide) break;
+      row_wide = true;  // scores of 0 and less, and those that are no numbers, are not among the sure ones
     }
   }
   if (threadIdx.x == 0) {

@@ -60,10 +60,6 @@ def _gated_inputs(batch, L, D, io, seed, z=True, reset=0.1, h0=True, lam=None):
     return p, opt, r(batch, L, D), _f32(rng, batch, D)
 
 
-def shape_of(p):
-    return p["u"].shape
-
-
 def _gated_dev(p, opt, io):
     args = (_dev(p["u"], io), _dev(p["ra"], io), _dev(p["rx"], io), _dev(p["lam"]))
     return args, dict(z=_dev(opt["z"], io), h0=_dev(opt["h0"]), reset=_dev(opt["reset"]))
@@ -86,7 +82,6 @@ def _check_gated(p, opt, dout, dlast, io, c=8.0, label="", states_too=True):
                                      check=True)
         assert set(g) == set(wg)
         e = {k: parity_error(_host(g[k]), wg[k]) for k in g}
-        print(label, shape_of(p), io, {**errs, **e})
         for k, v in e.items():
             assert v <= (5e-4 if k == "dlam" else 1e-4 if k == "dh0" else tol), (label, k, e)
     return out, last, g
@@ -391,6 +386,38 @@ def test_sampling_zero_infinite_and_invalid_noise():
     noise[1, :100] = np.nan
     noise[2] = np.inf
     assert _sample(x, noise)[0].tolist() == [50, 100, 0]
+
+
+@pytest.mark.parametrize("kw", [{}, {"top_p": [0.5] * 5}, {"top_k": [40] * 5}, {"min_p": [0.01] * 5}], ids=str)
+def test_sampling_where_no_noise_is_a_number(kw):
+    """Every score counts as -inf: the first element that stays is drawn."""
+    x, noise, _ = _logits(5, 9001, "f32", 31)
+    noise[:, :] = np.nan
+    noise[1, 5000:] = np.inf  # a score of 0 beats the others, wherever it is
+    x[1, 5000:] -= 1.0
+    noise[2] = -1.0           # negative scores: the smallest weight is the best
+    for r in range(5):
+        row = {k: float(np.float32(v[r])) if k != "top_k" else v[r] for k, v in kw.items()}
+        want = R.sample_row(x[r].astype(np.float64), noise[r].astype(np.float32), **row)[0]
+        assert _sample(x, noise, **kw)[0][r] == want, (r, kw)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("k", [256, 257, 300, 600, 2000, 5000])
+def test_sampling_of_long_lists(k, io):
+    """Lists that are ranked, searched by digits, by counts and then by masses, and that do not fit."""
+    x, noise, _ = _logits(3, 20000, io, k)
+    for p in ([1.0, 1.0, 1.0], [0.9, 0.5, 0.999]):
+        _check_sample(x, noise, io, top_k=[k, k + 1, k], top_p=p, temperature=[1.0, 3.0, 8.0])
+
+
+def test_sampling_of_a_flat_long_row():
+    """More elements within one bin of the end than the list holds, and more pieces than LDS holds."""
+    rng = np.random.default_rng(12)
+    x = (rng.standard_normal((3, 130001)) * 0.01).astype(np.float32)
+    _check_sample(x, rng.exponential(size=x.shape), "f32", top_p=[0.3, 0.9, 0.9999], min_p=[0.0, 0.98, 0.0])
+    y = _host(_dev(x + 2, "bf16")).astype(np.float32)
+    _check_sample(y, rng.exponential(size=x.shape), "bf16", top_p=[0.3, 0.9, 0.9999], top_k=[0, 0, 70000])
 
 
 def test_sampling_of_spread_logits_beyond_the_exponent_range():
