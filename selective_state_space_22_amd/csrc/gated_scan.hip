@@ -519,8 +519,8 @@ struct BwdRaw {
   }
 };
 
-// Reads five arrays and writes four, with some 60 vector instructions to an element beside
-// them.  (8, 2048, 1536) bf16 with z and resets, 465 MB: 128 us, 3.6 TB/s (a copy: 81 us).
+// Reads five arrays and writes four, with 96 vector instructions to an element beside them.
+// (8, 2048, 1536) bf16 with z and resets, 465 MB: 128 us, 3.6 TB/s (a copy: 81 us).
 template <typename IO, int W, bool HASZ, bool HASR>
 __global__ __launch_bounds__(64 * (W + 1), 4) void gated_bwd_kernel(GatedBwdArgs g, Link k, float* pl) {
   constexpr int T = kTokB;
