@@ -8,11 +8,12 @@
 // (top_p).  Rows that do not fit this (lists longer than LDS, logits spread over more than
 // 32 units) take a radix selection over the whole row.
 //
-// Three passes: the largest logit, the bracket, the scores; what LDS holds of the row (114 KB)
-// is read from memory once.  256 rows of 128000 fp32 with top_p, a row to a compute unit, 131
-// MB of logits and up to as much noise: 82 us (22 for the first pass, 19 for the second, 30 for
-// the third; a copy of logits and noise would take 46).  One row of 50000 bf16, all filters:
-// 18 us, nearly all of it latency (passes 8, list 4, search and end 6).
+// Two or three passes: the largest logit, the bracket (top_p alone: in the same pass), the
+// scores; what LDS holds of the row (114 KB) is read from memory once.  256 rows of 128000 fp32
+// with top_p, a row to a compute unit, 131 MB of logits and up to as much noise: 70 us (40 up
+// to the bracket, 20 for the scores, 10 for the exact end; a copy of logits and noise would
+// take 46).  One row of 50000 bf16, all filters: 18 us, nearly all of it latency (passes 8,
+// list 4, search and end 6).
 //
 // Masses that are added by atomics are integers (w 2^s, s = 62 - log2 of the row length,
 // 44 at most), so that no sum depends on an order.
@@ -29,6 +30,9 @@ constexpr int kWaves = kThreads / 64;
 constexpr uint32_t kMasked = 0x007fffffu;  // key of -inf; NaN takes it too
 constexpr int kBins = 2048;
 constexpr float kBinsPerUnit = 64.0f;
+// Bins above the reference of a histogram made before the maximum is known.  The reference is a
+// logit of the row itself: no bin ends at it, where rounding would decide its bin.
+constexpr float kAbove = 512.5f;
 constexpr int kList = 2048;        // elements that the exact search holds
 constexpr int kFew = 256;          // elements that it ranks in one go
 constexpr int kCacheVecs = 7168;   // 16-byte pieces of the row kept in LDS
@@ -753,13 +757,47 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
   row.to_bin = kBinsPerUnit / row.temperature;
 
   if (threadIdx.x == 0) sm.bound = 0;
+  const bool want_k = k > 0 && k < row.V, want_p = p < 1.0f;
+  // top_p alone: the histogram is filled in the same pass as the largest logit is found, its
+  // distances taken from the largest of the row's first pieces, kAbove bins of it above that
+  // (256 x 128000: 70 us against 82 with a pass for each).
+  float ref = -__builtin_inff();
+  if (!greedy && want_p && !want_k && row.to_bin <= 3.4028235e38f) {
+    if ((int)threadIdx.x < row.nvec) {
+      const uint4 v = row.vecs[threadIdx.x];
+#pragma unroll
+      for (int e = 0; e < Row<IO>::VEC; ++e) ref = fmaxf(ref, Row<IO>::element(v, e));
+    }
+    ref = logit_of(block_max(key_of(ref), sm));
+  }
+  const bool fused = fabsf(ref) < __builtin_inff();
+  if (fused) clear_bins(sm);
+  auto count = [&](float d) {  // d: a distance in bins
+    if (!(d < (float)kBins)) return;
+    d = fmaxf(d, 0.0f);  // (below 0: the counts are not used)
+    const int b = (int)d;
+    const float f = (d - (float)b) * (1.0f / kBinsPerUnit);
+    // e^-f 2^14 for f <= 1/64
+    atomicAdd(&sm.hist[b], (uint32_t)__builtin_fmaf(f, __builtin_fmaf(f, 8192.0f, -16384.0f), 16384.5f));
+  };
+  auto count_from_ref = [&](float v) { count(__builtin_fmaf(ref - v, row.to_bin, kAbove)); };
   // the largest logit (a NaN is never the larger), the thread's and the row's
   float mine = -__builtin_inff();
-  row.template ahead<4>([&](const uint4& v, int j) {
+  auto piece = [&](const uint4& v, int j) {
     if (j < kCacheVecs) sm.cache[j] = v;
 #pragma unroll
     for (int e = 0; e < Row<IO>::VEC; ++e) mine = fmaxf(mine, Row<IO>::element(v, e));
-  });
+  };
+  if (fused) {
+    row.template ahead<4>([&](const uint4& v, int j) {
+      piece(v, j);
+#pragma unroll
+      for (int e = 0; e < Row<IO>::VEC; ++e) count_from_ref(Row<IO>::element(v, e));
+    });
+    row.edges([&](float v, int) { count_from_ref(v); });
+  } else {
+    row.template ahead<4>(piece);
+  }
   row.edges([&](float v, int) { mine = fmaxf(mine, v); });
   row.mkey = block_max(key_of(mine), sm);
   row.m = logit_of(row.mkey);
@@ -781,7 +819,6 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
     });
     best.at = ~block_max(first, sm);
   } else {
-    const bool want_k = k > 0 && k < row.V, want_p = p < 1.0f;
     int before, after;
     float lo = 0.0f, hi = -1.0f;  // distances below lo stay, those from lo up to below hi are listed
     // (an infinite maximum has no distances; its equals are all that has a weight)
@@ -807,18 +844,15 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
       // fewer than k within the histogram's range: all that is not masked
       hi = b == kBins ? __builtin_inff() : (float)(b + 1);
     } else if (want_p) {
-      clear_bins(sm);
-      row.each([&](float v, int) {
-        const float d = row.distance(v);
-        if (d < (float)kBins) {
-          const int b = (int)d;
-          const float f = (d - (float)b) * (1.0f / kBinsPerUnit);
-          // e^-f 2^14 for f <= 1/64
-          atomicAdd(&sm.hist[b], (uint32_t)__builtin_fmaf(f, __builtin_fmaf(f, 8192.0f, -16384.0f), 16384.5f));
-        }
-      });
+      const float shift = (row.m - ref) * row.to_bin - kAbove;  // from bins of ref to those of m
+      const bool counted = fused && shift <= 0.0f;
+      if (!counted) {
+        clear_bins(sm);
+        row.each([&](float v, int) { count(row.distance(v)); });
+      }
       const int b = find_bin<true>(p, 0.0f, before, after, sm);
-      lo = (float)(b > 0 ? b - before : 0), hi = (float)(b + 1 + after);
+      lo = fmaxf((float)(b - before) + (counted ? shift : 0.0f), 0.0f);
+      hi = (float)(b + 1 + after) + (counted ? shift : 0.0f);
       row_wide = b == kBins;
     }
     if (!want_k && !want_p && !row_wide) lo = hi = __builtin_inff();

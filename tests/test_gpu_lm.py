@@ -411,6 +411,21 @@ def test_sampling_of_long_lists(k, io):
         _check_sample(x, noise, io, top_k=[k, k + 1, k], top_p=p, temperature=[1.0, 3.0, 8.0])
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_sampling_where_the_largest_logits_come_late(io):
+    """The row's first pieces are no guide to its maximum: far below it, masked, or above all the rest."""
+    x, noise, _ = _logits(6, 30011, io, 41)
+    x[0, 20000] = 60.0
+    x[1, :10000] = -np.inf
+    x[2, :10000] -= 7.0
+    x[3, :10000] = np.nan
+    x[4, 5] = 40.0
+    x[5, 25000:] += 9.0
+    x = _host(_dev(x, io)).astype(np.float32)
+    for p in (0.3, 0.9, 0.999):
+        _check_sample(x, noise, io, top_p=[p] * 6, temperature=[1.0, 0.7, 1.0, 1.5, 8.0, 1.0])
+
+
 def test_sampling_of_a_flat_long_row():
     """More elements within one bin of the end than the list holds, and more pieces than LDS holds."""
     rng = np.random.default_rng(12)
