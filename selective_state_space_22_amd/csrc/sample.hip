@@ -659,20 +659,22 @@ __device__ __forceinline__ void score_row(const Row<IO>& row, const Limits& at, 
     best.offer(w, n, i);
   };
   row.batches([&](const uint4 (&v)[kBatch], int base, auto prefetch) {
-    float w[Row<IO>::kElems];
-    uint32_t listed = 0;  // marks of those to be listed
+    float w[Row<IO>::kElems], d[Row<IO>::kElems];
+    float beyond = 3.0e38f;  // the least from `sure` on
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       float least = 3.0e38f;
 #pragma unroll
       for (int c = 0; c < VEC; ++c) {
-        const float d = fminf(row.m - Row<IO>::element(v[q], c), 3.0e38f);  // (NaN: no weight)
-        const float rough = ex2(d * to_exponent);
-        least = fminf(least, d);
+        const int k = q * VEC + c;
+        d[k] = fminf(row.m - Row<IO>::element(v[q], c), 3.0e38f);  // (NaN: no weight)
+        const float rough = ex2(d[k] * to_exponent);
+        const bool in = d[k] < at.sure;
+        least = fminf(least, d[k]);
+        beyond = fminf(beyond, in ? 3.0e38f : d[k]);
         sums.all += rough;
-        w[q * VEC + c] = d < at.sure ? rough : 0.0f;
-        sums.kept += w[q * VEC + c];
-        listed = listed + listed + (__float_as_uint(d) - lo_bits < span ? 1u : 0u);
+        w[k] = in ? rough : 0.0f;
+        sums.kept += w[k];
       }
       if (least < at.sure) {
         const int i = row.index(base, q * VEC);
@@ -682,13 +684,15 @@ __device__ __forceinline__ void score_row(const Row<IO>& row, const Limits& at, 
       }
     }
     if (at.lists) {
+      uint32_t listed = 0;  // marks of those to be listed
+#pragma unroll
+      for (int c = 0; c < Row<IO>::kElems; ++c)
+        listed = listed + listed + (__float_as_uint(d[c]) - lo_bits < span ? 1u : 0u);
       append_marked(row, v, base, listed, sm);
       if (at.sure < at.lo) {
 #pragma unroll
-        for (int c = 0; c < Row<IO>::kElems; ++c) {
-          const float d = row.m - Row<IO>::element(v[c / VEC], c % VEC);
-          sums.above += d >= at.sure && d < at.lo ? ex2(d * to_exponent) : 0.0f;
-        }
+        for (int c = 0; c < Row<IO>::kElems; ++c)
+          sums.above += d[c] >= at.sure && d[c] < at.lo ? ex2(d[c] * to_exponent) : 0.0f;
       }
     }
     prefetch();
@@ -712,12 +716,9 @@ __device__ __forceinline__ void score_row(const Row<IO>& row, const Limits& at, 
 #pragma unroll
       for (int c = 0; c < Row<IO>::kElems; ++c) which |= w[c] > 0.0f && !(score[c] < bound) ? 1u << c : 0u;
     }
-    if (at.sure < at.near) {
+    if (beyond < at.near) {
 #pragma unroll
-      for (int c = 0; c < Row<IO>::kElems; ++c) {
-        const float d = row.m - Row<IO>::element(v[c / VEC], c % VEC);
-        unsure |= d >= at.sure && d < at.near ? 1u << c : 0u;
-      }
+      for (int c = 0; c < Row<IO>::kElems; ++c) unsure |= d[c] >= at.sure && d[c] < at.near ? 1u << c : 0u;
     }
     for (uint32_t todo = which | unsure; todo != 0; todo &= todo - 1) {
       const int c = __ffs((int)todo) - 1, i = row.index(base, c);
