@@ -10,10 +10,11 @@
 //
 // Two or three passes: the largest logit, the bracket (top_p alone: in the same pass), the
 // scores; what LDS holds of the row (114 KB) is read from memory once.  256 rows of 128000 fp32
-// with top_p, a row to a compute unit, 131 MB of logits and up to as much noise: 70 us (40 up
+// with top_p, a row to a compute unit, 131 MB of logits and up to as much noise: 71 us (40 up
 // to the bracket, 20 for the scores, 10 for the exact end; a copy of logits and noise would
 // take 46).  One row of 50000 bf16, all filters: 18 us, nearly all of it latency (passes 8,
-// list 4, search and end 6).
+// list 4, search and end 6); 64 rows of 50001 without filters 17, some 18 vector instructions
+// to an element on 64 of the 256 compute units.
 //
 // Masses that are added by atomics are integers (w 2^s, s = 62 - log2 of the row length,
 // 44 at most), so that no sum depends on an order.
@@ -761,7 +762,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
   const bool want_k = k > 0 && k < row.V, want_p = p < 1.0f;
   // top_p alone: the histogram is filled in the same pass as the largest logit is found, its
   // distances taken from the largest of the row's first pieces, kAbove bins of it above that
-  // (256 x 128000: 70 us against 82 with a pass for each).
+  // (256 x 128000: 70 us in place of 82 with a pass for each).
   float ref = -__builtin_inff();
   if (!greedy && want_p && !want_k && row.to_bin <= 3.4028235e38f) {
     if ((int)threadIdx.x < row.nvec) {
@@ -778,7 +779,8 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
     d = fmaxf(d, 0.0f);  // (below 0: the counts are not used)
     const int b = (int)d;
     const float f = (d - (float)b) * (1.0f / kBinsPerUnit);
-    // e^-f 2^14 for f <= 1/64
+    // e^-f 2^14 for f <= 1/64 (a bin of more than 2^18 elements runs over: no list holds them
+    // either, and a bracket that the end is not in is noticed when the list is searched)
     atomicAdd(&sm.hist[b], (uint32_t)__builtin_fmaf(f, __builtin_fmaf(f, 8192.0f, -16384.0f), 16384.5f));
   };
   auto count_from_ref = [&](float v) { count(__builtin_fmaf(ref - v, row.to_bin, kAbove)); };

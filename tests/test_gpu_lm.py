@@ -431,6 +431,9 @@ def test_sampling_of_a_flat_long_row():
     rng = np.random.default_rng(12)
     x = (rng.standard_normal((3, 130001)) * 0.01).astype(np.float32)
     _check_sample(x, rng.exponential(size=x.shape), "f32", top_p=[0.3, 0.9, 0.9999], min_p=[0.0, 0.98, 0.0])
+    longest = np.full((1, 1 << 20), 3.0, np.float32)  # of one bin
+    longest[0, 77::2] += (rng.standard_normal(longest[0, 77::2].shape) * 1e-3).astype(np.float32)
+    _check_sample(longest, rng.exponential(size=longest.shape), "f32", top_p=[0.4])
     y = _host(_dev(x + 2, "bf16")).astype(np.float32)
     _check_sample(y, rng.exponential(size=x.shape), "bf16", top_p=[0.3, 0.9, 0.9999], top_k=[0, 0, 70000])
 
