@@ -125,7 +125,7 @@ int mamba_embed_bwd(int64_t count, int64_t vocab, int64_t dim, int io_dtype, con
  *   token  = argmax of w_i / noise_i over what stays with w_i > 0, the lowest index of equal ones
  *   logprob = ln(w_token / sum of w over what stays)
  * With independent Exp(1) noise the token has the distribution w / sum(w) over
- * what stays.  Only the noise of what stays is read.  A noise value of 0 always
+ * what stays.  The noise of what does not stay may hold anything.  A noise value of 0 always
  * wins; a negative or NaN one never does, unless none else stays.
  *   logits  : (rows, vocab) I/O type;  noise : (rows, vocab) float
  *   temperature, top_p, min_p : (rows) float, top_k : (rows) int32, all nullable.
@@ -134,13 +134,11 @@ int mamba_embed_bwd(int64_t count, int64_t vocab, int64_t dim, int io_dtype, con
  *     <= 0 or NaN: off; >= 1 keeps what equals the largest.
  *   tokens  : (rows) int64; -1 for a row whose logits are all -inf or NaN
  *   logprob : (rows) float, nullable; -inf for such a row
- *   workspace : mamba_sample_workspace_size() bytes of scratch (may be NULL when 0)
  * Limits: 0 <= rows <= 2^20, 1 <= vocab <= 2^20.
  */
-size_t mamba_sample_workspace_size(int64_t rows, int64_t vocab, int io_dtype);
 int mamba_sample(int64_t rows, int64_t vocab, int io_dtype, const void* logits, const float* noise,
                  const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
-                 int64_t* tokens, float* logprob, void* workspace, size_t workspace_bytes, void* stream);
+                 int64_t* tokens, float* logprob, void* stream);
 
 #ifdef __cplusplus
 }

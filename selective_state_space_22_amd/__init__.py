@@ -17,8 +17,7 @@ from .binding import (MAMBA_IO_BF16, MAMBA_IO_F32, MambaError, load_library, mam
                       status_string)
 from .lm import (MAMBA_GATED_STATE_CHUNK, mamba_embed_bwd, mamba_embed_bwd_workspace_size, mamba_embed_fwd,
                  mamba_gated_scan_bwd, mamba_gated_scan_bwd_workspace_size, mamba_gated_scan_fwd,
-                 mamba_gated_scan_fwd_workspace_size, mamba_gated_state_update, mamba_sample,
-                 mamba_sample_workspace_size)
+                 mamba_gated_scan_fwd_workspace_size, mamba_gated_state_update, mamba_sample)
 
 __all__ = ["mamba_block_fwd", "mamba_block_fwd_workspace_size", "mamba_scan_fwd", "mamba_scan_fwd_complex", "mamba_scan_fwd_complex_workspace_size", "mamba_scan_bwd",
            "mamba_state_update", "mamba_state_update_complex", "mamba_scan_fwd_workspace_size",
@@ -27,5 +26,4 @@ __all__ = ["mamba_block_fwd", "mamba_block_fwd_workspace_size", "mamba_scan_fwd"
            "MAMBA_IO_F32", "MAMBA_IO_BF16", "mamba_set_option", "mamba_get_option", "mamba_stream_status",
            "mamba_scan_fwd_noalloc", "MAMBA_GATED_STATE_CHUNK", "mamba_embed_bwd", "mamba_embed_bwd_workspace_size",
            "mamba_embed_fwd", "mamba_gated_scan_bwd", "mamba_gated_scan_bwd_workspace_size", "mamba_gated_scan_fwd",
-           "mamba_gated_scan_fwd_workspace_size", "mamba_gated_state_update", "mamba_sample",
-           "mamba_sample_workspace_size"]
+           "mamba_gated_scan_fwd_workspace_size", "mamba_gated_state_update", "mamba_sample"]

@@ -237,14 +237,9 @@ int mamba_embed_bwd(int64_t count, int64_t vocab, int64_t dim, int io_dtype, con
   return MAMBA_OK;
 }
 
-size_t mamba_sample_workspace_size(int64_t rows, int64_t vocab, int io_dtype) {
-  if (check_sample("mamba_sample_workspace_size", rows, vocab, io_dtype) != MAMBA_OK) return 0;
-  return s6::sample_ws_bytes(rows, vocab, io_dtype);
-}
-
 int mamba_sample(int64_t rows, int64_t vocab, int io_dtype, const void* logits, const float* noise,
                  const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
-                 int64_t* tokens, float* logprob, void* workspace, size_t workspace_bytes, void* stream) {
+                 int64_t* tokens, float* logprob, void* stream) {
   const char* where = "mamba_sample";
   const int st = check_sample(where, rows, vocab, io_dtype);
   if (st != MAMBA_OK) return st;
@@ -258,13 +253,10 @@ int mamba_sample(int64_t rows, int64_t vocab, int io_dtype, const void* logits, 
   pc.opt(top_p, "top_p");
   pc.opt(min_p, "min_p");
   pc.opt(logprob, "logprob");
-  pc.opt(workspace, "workspace");
   if (pc.status != MAMBA_OK) return pc.status;
   if (!any) return MAMBA_OK;
-  const size_t need = s6::sample_ws_bytes(rows, vocab, io_dtype);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return fail(MAMBA_ERR_WORKSPACE, where, "workspace");
   const s6::SampleArgs a{logits, noise, temperature, top_k, top_p, min_p, tokens, logprob, rows, vocab};
-  const hipError_t e = s6::launch_sample(a, io_dtype, workspace, static_cast<hipStream_t>(stream));
+  const hipError_t e = s6::launch_sample(a, io_dtype, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(MAMBA_ERR_HIP, where, hipGetErrorString(e));
   return MAMBA_OK;
 }

@@ -83,7 +83,6 @@ struct SampleArgs {
   int64_t rows, V;
 };
 
-size_t sample_ws_bytes(int64_t rows, int64_t V, int io);
-hipError_t launch_sample(const SampleArgs& a, int io, void* workspace, hipStream_t stream);
+hipError_t launch_sample(const SampleArgs& a, int io, hipStream_t stream);
 
 }  // namespace s6

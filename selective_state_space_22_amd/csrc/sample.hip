@@ -949,9 +949,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
 
 }  // namespace
 
-size_t sample_ws_bytes(int64_t, int64_t, int) { return 0; }
-
-hipError_t launch_sample(const SampleArgs& a, int io, void*, hipStream_t st) {
+hipError_t launch_sample(const SampleArgs& a, int io, hipStream_t st) {
   int bits = 0;
   while ((int64_t(1) << bits) < a.V) ++bits;
   const float unit = __builtin_ldexpf(1.0f, 62 - bits < 44 ? 62 - bits : 44);

@@ -26,14 +26,12 @@ def _lib():
                  "mamba_embed_bwd_workspace_size"):
         getattr(lib, name).argtypes = [I64, I64, I64, I]
         getattr(lib, name).restype = SZ
-    lib.mamba_sample_workspace_size.argtypes = [I64, I64, I]
-    lib.mamba_sample_workspace_size.restype = SZ
     lib.mamba_gated_scan_fwd.argtypes = [I64, I64, I64, I, P, P, P, P, F, P, P, P, P, P, P, P, SZ, P]
     lib.mamba_gated_scan_bwd.argtypes = [I64, I64, I64, I, P, P, P, P, F] + [P] * 13 + [SZ, P]
     lib.mamba_gated_state_update.argtypes = [I64, I64, I, P, P, P, P, P, F, P, P, P, P]
     lib.mamba_embed_fwd.argtypes = [I64, I64, I64, I, P, P, F, P, P]
     lib.mamba_embed_bwd.argtypes = [I64, I64, I64, I, P, P, F, P, P, SZ, P]
-    lib.mamba_sample.argtypes = [I64, I64, I, P, P, P, P, P, P, P, P, P, SZ, P]
+    lib.mamba_sample.argtypes = [I64, I64, I, P, P, P, P, P, P, P, P, P]
     for name in ("mamba_gated_scan_fwd", "mamba_gated_scan_bwd", "mamba_gated_state_update", "mamba_embed_fwd",
                  "mamba_embed_bwd", "mamba_sample"):
         getattr(lib, name).restype = I
@@ -223,12 +221,8 @@ def mamba_embed_bwd(ids, dout, vocab, scale=1.0, dweight=None, workspace=None):
     return dweight
 
 
-def mamba_sample_workspace_size(rows: int, vocab: int, io_dtype: int) -> int:
-    return int(_lib().mamba_sample_workspace_size(rows, vocab, io_dtype))
-
-
 def mamba_sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprob=None,
-                 workspace=None, return_logprob=True):
+                 return_logprob=True):
     """Draws a token per row of logits (rows, vocab) with Exp(1) noise (rows, vocab) float32, after
     temperature, top_k, top_p and min_p: (rows,) tensors (float32, top_k int32) or None (off).
 
@@ -241,13 +235,12 @@ def mamba_sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=
     tokens = torch.empty((rows,), dtype=torch.int64, device=dev) if tokens is None else tokens
     if logprob is None and return_logprob:
         logprob = torch.empty((rows,), dtype=f32, device=dev)
-    workspace, ws, ws_bytes = _workspace(workspace, lib.mamba_sample_workspace_size(rows, V, io), dev)
     st = lib.mamba_sample(rows, V, io, _arg(logits, "logits", logits.dtype, (rows, V), dev),
                           _arg(noise, "noise", f32, (rows, V), dev),
                           _arg(temperature, "temperature", f32, (rows,), dev),
                           _arg(top_k, "top_k", torch.int32, (rows,), dev), _arg(top_p, "top_p", f32, (rows,), dev),
                           _arg(min_p, "min_p", f32, (rows,), dev), _arg(tokens, "tokens", torch.int64, (rows,), dev),
-                          _arg(logprob, "logprob", f32, (rows,), dev), ws, ws_bytes, _stream(dev))
+                          _arg(logprob, "logprob", f32, (rows,), dev), _stream(dev))
     if st != 0:
         raise MambaError("mamba_sample", st)
     return tokens, logprob

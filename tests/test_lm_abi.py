@@ -28,7 +28,7 @@ def test_every_declared_symbol_is_exported():
     assert names == sorted([
         "mamba_embed_bwd", "mamba_embed_bwd_workspace_size", "mamba_embed_fwd", "mamba_gated_scan_bwd",
         "mamba_gated_scan_bwd_workspace_size", "mamba_gated_scan_fwd", "mamba_gated_scan_fwd_workspace_size",
-        "mamba_gated_state_update", "mamba_sample", "mamba_sample_workspace_size"])
+        "mamba_gated_state_update", "mamba_sample"])
     raw = ctypes.CDLL(binding.LIB_PATH)
     for n in names:
         assert hasattr(raw, n), n
@@ -59,8 +59,7 @@ def _entry(lib, name):
     order = {"fwd": FWD, "bwd": BWD, "step": STEP,
              "embed_fwd": ["ids", "weight", "scale", "out", "stream"],
              "embed_bwd": ["ids", "dout", "scale", "dweight", "ws", "ws_bytes", "stream"],
-             "sample": ["logits", "noise", "temperature", "top_k", "top_p", "min_p", "tokens", "logprob", "ws",
-                        "ws_bytes", "stream"]}[name]
+             "sample": ["logits", "noise", "temperature", "top_k", "top_p", "min_p", "tokens", "logprob", "stream"]}[name]
     fn = {"fwd": lib.mamba_gated_scan_fwd, "bwd": lib.mamba_gated_scan_bwd, "step": lib.mamba_gated_state_update,
           "embed_fwd": lib.mamba_embed_fwd, "embed_bwd": lib.mamba_embed_bwd, "sample": lib.mamba_sample}[name]
     head = {"step": (2, 64, 0), "sample": (2, 64, 0)}.get(name, (2, 8, 64, 0))
@@ -108,8 +107,7 @@ def test_refusal_of_a_vocabulary_of_none(lib):
 @pytest.mark.parametrize("name,size,head", [
     ("fwd", "mamba_gated_scan_fwd_workspace_size", (1, 1 << 20, 256, 0)),
     ("bwd", "mamba_gated_scan_bwd_workspace_size", (2, 4096, 256, 1)),
-    ("embed_bwd", "mamba_embed_bwd_workspace_size", (4096, 1000, 64, 0)),
-    ("sample", "mamba_sample_workspace_size", (4, 50000, 1))])
+    ("embed_bwd", "mamba_embed_bwd_workspace_size", (4096, 1000, 64, 0))])
 def test_workspace_sizes_and_their_refusal(lib, name, size, head):
     fn, order, _ = _entry(lib, name)
     need = getattr(lm, size)(*head)
