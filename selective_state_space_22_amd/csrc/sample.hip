@@ -16,8 +16,8 @@
 // list 4, search and end 6); 64 rows of 50001 without filters 17, some 18 vector instructions
 // to an element on 64 of the 256 compute units.
 //
-// Masses that are added by atomics are integers (w 2^s, s = 62 - log2 of the row length,
-// 44 at most), so that no sum depends on an order.
+// Masses that are added by atomics are integers (w 2^s, s = 62 - log2 of the row length),
+// so that no sum depends on an order.
 #include <hip/hip_runtime.h>
 
 #include "lm_internal.h"
@@ -896,7 +896,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
           double need = __builtin_ceil(want_k ? (double)p * mass : ((double)p * sum.b - sum.a) * (double)unit);
           if (want_k) need = fmin(fmax(need, 1.0), mass);
           if (!(need >= 1.0 && need <= mass)) row_wide = true;  // the end is not in the list
-          target = (uint64_t)need;
+          target = min((uint64_t)need, (uint64_t)sum.c);  // (`mass` may have been rounded up)
         }
         if (row_wide) break;
         if (few) {
@@ -952,7 +952,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
 hipError_t launch_sample(const SampleArgs& a, int io, hipStream_t st) {
   int bits = 0;
   while ((int64_t(1) << bits) < a.V) ++bits;
-  const float unit = __builtin_ldexpf(1.0f, 62 - bits < 44 ? 62 - bits : 44);
+  const float unit = __builtin_ldexpf(1.0f, 62 - bits);  // a row's masses sum to 2^62 at most
   if (io == kIoBF16) hipLaunchKernelGGL(sample_row_kernel<uint16_t>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, a, unit, bits);
   else hipLaunchKernelGGL(sample_row_kernel<float>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, a, unit, bits);
   return hipGetLastError();
