@@ -6,7 +6,7 @@
 // lies above the bracket stays, and the few elements inside are listed in LDS and searched
 // for the exact end by radix selection over (key, index), by counts (top_k) or by masses
 // (top_p).  Rows that do not fit this (lists longer than LDS, logits spread over more than
-// 32 units) take a radix selection over the whole row.
+// 32 units, temperatures near the end of fp32's range) take a radix selection over the whole row.
 //
 // Two or three passes: the largest logit, the bracket (top_p alone: in the same pass), the
 // scores; what LDS holds of the row (114 KB) is read from memory once.  256 rows of 128000 fp32
@@ -34,6 +34,15 @@ constexpr float kBinsPerUnit = 64.0f;
 // Bins above the reference of a histogram made before the maximum is known.  The reference is a
 // logit of the row itself: no bin ends at it, where rounding would decide its bin.
 constexpr float kAbove = 512.5f;
+// Distances m - x end at kFarthest: those of masked logits, NaN and what lies past the row's end,
+// which only a limit below it keeps out.  All limits are at most 90 units of the temperature, or
+// kBins + 2 bins of it; below kLeastToBin bins to a logit (a temperature above 6.4e31) these could
+// reach kFarthest, and the row takes the selection over the whole of it.
+constexpr float kFarthest = 3.0e38f;
+constexpr float kLeastToBin = 1.0e-30f;
+static_assert((90.0f * kBinsPerUnit) / kLeastToBin < 1.0e-3f * kFarthest &&
+                  (kBins + 2) / kLeastToBin < 1.0e-3f * kFarthest,
+              "no limit comes near the farthest distance");
 constexpr int kList = 2048;        // elements that the exact search holds
 constexpr int kFew = 256;          // elements that it ranks in one go
 constexpr int kCacheVecs = 7168;   // 16-byte pieces of the row kept in LDS
@@ -624,7 +633,7 @@ __device__ Cut cut_row(const Row<IO>& row, int64_t k, float p, Shared& sm) {
 
 // Limits of m - x for one pass over the row.  Below `sure` an element is scored, from there
 // up to below `near` if its exact weight is large enough, from `lo` up to below `hi` it is
-// listed (sure <= near <= lo <= hi).
+// listed (sure <= near <= lo <= hi; all but an infinite lo = hi far below kFarthest).
 struct Limits {
   float sure, near, lo, hi;
   bool lists;
@@ -661,18 +670,18 @@ __device__ __forceinline__ void score_row(const Row<IO>& row, const Limits& at, 
   };
   row.batches([&](const uint4 (&v)[kBatch], int base, auto prefetch) {
     float w[Row<IO>::kElems], d[Row<IO>::kElems];
-    float beyond = 3.0e38f;  // the least from `sure` on
+    float beyond = kFarthest;  // the least from `sure` on
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
-      float least = 3.0e38f;
+      float least = kFarthest;
 #pragma unroll
       for (int c = 0; c < VEC; ++c) {
         const int k = q * VEC + c;
-        d[k] = fminf(row.m - Row<IO>::element(v[q], c), 3.0e38f);  // (NaN: no weight)
+        d[k] = fminf(row.m - Row<IO>::element(v[q], c), kFarthest);  // (NaN: no weight)
         const float rough = ex2(d[k] * to_exponent);
         const bool in = d[k] < at.sure;
         least = fminf(least, d[k]);
-        beyond = fminf(beyond, in ? 3.0e38f : d[k]);
+        beyond = fminf(beyond, in ? kFarthest : d[k]);
         sums.all += rough;
         w[k] = in ? rough : 0.0f;
         sums.kept += w[k];
@@ -728,7 +737,7 @@ __device__ __forceinline__ void score_row(const Row<IO>& row, const Limits& at, 
   });
   sums.above += sums.kept;
   row.edges([&](float x, int i) {
-    const float d = fminf(row.m - x, 3.0e38f), rough = ex2(d * to_exponent);
+    const float d = fminf(row.m - x, kFarthest), rough = ex2(d * to_exponent);
     sums.all += rough;
     sums.above += d < at.lo ? rough : 0.0f;
     append(__float_as_uint(d) - lo_bits < span, row.entry(x, i), sm);
@@ -764,7 +773,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
   // distances taken from the largest of the row's first pieces, kAbove bins of it above that
   // (256 x 128000: 70 us in place of 82 with a pass for each).
   float ref = -__builtin_inff();
-  if (!greedy && want_p && !want_k && row.to_bin <= 3.4028235e38f) {
+  if (!greedy && want_p && !want_k && row.to_bin >= kLeastToBin && row.to_bin <= 3.4028235e38f) {
     if ((int)threadIdx.x < row.nvec) {
       const uint4 v = row.vecs[threadIdx.x];
 #pragma unroll
@@ -825,7 +834,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
     int before, after;
     float lo = 0.0f, hi = -1.0f;  // distances below lo stay, those from lo up to below hi are listed
     // (an infinite maximum has no distances; its equals are all that has a weight)
-    bool row_wide = row.m > 3.4028235e38f || row.to_bin > 3.4028235e38f;
+    bool row_wide = row.m > 3.4028235e38f || row.to_bin > 3.4028235e38f || row.to_bin < kLeastToBin;
     if (row_wide) {
       clear_bins(sm);
     } else if (want_k) {
@@ -855,7 +864,8 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
       }
       const int b = find_bin<true>(p, 0.0f, before, after, sm);
       lo = fmaxf((float)(b - before) + (counted ? shift : 0.0f), 0.0f);
-      hi = (float)(b + 1 + after) + (counted ? shift : 0.0f);
+      // (at least lo: counts that run over to nothing leave the first bin, above the maximum's)
+      hi = fmaxf((float)(b + 1 + after) + (counted ? shift : 0.0f), lo);
       row_wide = b == kBins;
     }
     if (!want_k && !want_p && !row_wide) lo = hi = __builtin_inff();

@@ -6,7 +6,7 @@ Tolerances are those of test_gpu_lm.py where no other is derived at a test."""
 import numpy as np
 import pytest
 
-from test_gpu_lm import _check_sample
+from test_gpu_lm import _check_sample, _host, _logits
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -32,3 +32,27 @@ def test_sampling_where_small_weights_decide_the_end(small, io):
         at = rng.permutation(1003)
         x[r, at[:10]], x[r, at[10:10 + small]] = 0.0, -34.0
     _check_sample(x, rng.exponential(size=x.shape), io, top_k=[10 + small] * 3, top_p=[0.5] * 3)
+
+
+HOT = [1e30, 1e31, 1e32, 1e36, 4e36, 1e37, 1e38, 3e38, np.inf]
+HOT_FILTERS = {"none": {}, "top_p": {"top_p": [0.3, 0.9, 0.999] * 3}, "min_p": {"min_p": [0.0, 0.5, 0.9] * 3},
+               "top_k": {"top_k": [2, 40, 700] * 3},
+               "all": {"top_k": [0, 40, 2500] * 3, "top_p": [0.7, 0.9, 0.5] * 3, "min_p": [0.01, 0.5, 0.02] * 3}}
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [5, 1003, 8193, 20001])
+@pytest.mark.parametrize("name", HOT_FILTERS)
+def test_sampling_at_temperatures_that_level_the_row(name, V, io):
+    """Up to an infinite temperature, where every logit that is not masked weighs the same: masked ones and
+    what lies past the row's end have no part in it.  The type's lowest value is a logit like any other."""
+    x, noise, rng = _logits(9, V, io, V)
+    kw = {"temperature": HOT, **HOT_FILTERS[name]}
+    _check_sample(x, noise, io, **kw)
+    x[rng.random(x.shape) < 0.5] = -np.inf
+    x[rng.random(x.shape) < 0.1] = np.nan
+    x[:, 0] = 1.0
+    noise[np.isnan(x) | (x == -np.inf)] = 1e-6  # the best scores by far, if they counted
+    _check_sample(x, noise, io, **kw)
+    x[:, 1::3] = _host(torch.tensor(torch.finfo(torch.bfloat16).min))
+    _check_sample(x, noise, io, **kw)
