@@ -369,7 +369,8 @@ __device__ __forceinline__ void append_marked(const Row<IO>& row, const uint4 (&
   }
 }
 
-// Lists the elements with m - x < end.
+// Lists the elements of the bins before `end`, by the distance that put them into their bins: a
+// limit of m - x, end / to_bin, rounds otherwise and would leave out some of the last bin.
 template <typename IO>
 __device__ __forceinline__ void list_row(const Row<IO>& row, float end, Shared& sm) {
   row.batches([&](const uint4 (&v)[Row<IO>::kBatch], int base, auto prefetch) {
@@ -377,10 +378,10 @@ __device__ __forceinline__ void list_row(const Row<IO>& row, float end, Shared& 
     uint32_t marks = 0;
 #pragma unroll
     for (int c = 0; c < Row<IO>::kElems; ++c)
-      marks = marks + marks + (row.m - Row<IO>::element(v[c / Row<IO>::VEC], c % Row<IO>::VEC) < end ? 1u : 0u);
+      marks = marks + marks + (row.distance(Row<IO>::element(v[c / Row<IO>::VEC], c % Row<IO>::VEC)) < end ? 1u : 0u);
     append_marked(row, v, base, marks, sm);
   });
-  row.edges([&](float x, int i) { append(row.m - x < end, row.entry(x, i), sm); });
+  row.edges([&](float x, int i) { append(row.distance(x) < end, row.entry(x, i), sm); });
 }
 
 // The element of the first n of the list at which the measure of the elements >= it first
@@ -872,7 +873,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a, floa
     Sums sums;
     uint64_t listed = 0;  // mass of the listed elements that stay
     if (!row_wide) {
-      if (want_k) list_row(row, hi / row.to_bin, sm);
+      if (want_k) list_row(row, hi, sm);
       else {
         // the exact test of min_p for what lies a hundredth of a bin about its limit; weights
         // below e^-80 are worked out exactly too, and those below e^-87 are 0

@@ -56,3 +56,35 @@ def test_sampling_at_temperatures_that_level_the_row(name, V, io):
     _check_sample(x, noise, io, **kw)
     x[:, 1::3] = _host(torch.tensor(torch.finfo(torch.bfloat16).min))
     _check_sample(x, noise, io, **kw)
+
+
+# (temperature, difference of two logits): the difference in bins of 1/64 of the temperature rounds to
+# just below a whole number, while that number of bins rounds to the difference itself
+BIN_EDGES = [(0.55, 2.0625), (0.55, 4.125), (0.55, 8.25), (1.1, 1.03125), (1.1, 4.125), (1.35, 1.265625),
+             (1.35, 2.53125), (1.35, 5.0625), (1.35, 10.125), (0.72, 10.125), (2.2, 4.125)]
+
+
+def test_the_differences_lie_at_the_edge_of_a_bin():
+    for t, d in BIN_EDGES:
+        bins = np.float32(64) / np.float32(t)
+        edge = np.floor(np.float32(d) * bins) + np.float32(1)
+        assert np.float32(d) * bins < edge and np.float32(edge / bins) == np.float32(d), (t, d)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("ties", [1, 5, 300])
+@pytest.mark.parametrize("above", [1, 7, 700])
+def test_top_k_that_ends_at_the_edge_of_a_bin(above, ties, io):
+    """`above` logits of the largest value, `ties` at the edge and others far below: the k-th largest is one
+    of those at the edge.  700 above: the histogram of all elements, else that of the threads' maxima."""
+    rng = np.random.default_rng(above + ties)
+    n = len(BIN_EDGES)
+    x = np.full((n, 6000), -40.0, np.float32)
+    x[:, ::2] = -np.inf
+    for r, (_, d) in enumerate(BIN_EDGES):
+        at = rng.permutation(6000)
+        x[r, at[:above]], x[r, at[above:above + ties]] = d, 0.0
+    noise = rng.exponential(size=x.shape)
+    kw = {"temperature": [t for t, _ in BIN_EDGES], "top_k": [above + (r % ties) + 1 for r in range(n)]}
+    _check_sample(x, noise, io, **kw)
+    _check_sample(x, noise, io, **kw, top_p=[0.999999] * n)
