@@ -2,10 +2,11 @@
 //
 // Per token and channel, with kappa = c softplus(lam) of the channel:
 //     l = -kappa sigma(ra),  a = e^l,  s = sqrt(1 - a^2),  b = s sigma(rx) u,  h' = a h + b.
-// A slow channel has 1 - a near 1e-4 or less, so a is formed as 1 - m from
+// A slow channel has 1 - a near 1e-4 or less, so there a is formed as 1 - m from
 // m = -expm1(l): the subtraction rounds once, without the bias that an exp near
 // 1 carries through thousands of products, and 1 - a^2 = m (2 - m) keeps its
-// relative accuracy where 1 - a*a would cancel.
+// relative accuracy where 1 - a*a would cancel.  A fast channel's a is the exponential
+// itself: 1 - m would hold it to 2^-25 of 1, which is nothing of a at l = -17.
 #pragma once
 
 #include "s6_device.h"
@@ -20,33 +21,38 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// m = 1 - e^y for y <= 0, relative error about 2e-7:
-//   y > -0.35 : -y (1 + y/2 (1 + y/3 (1 + ... y/7))), truncation below 2e-8
-//   otherwise : 1 - e^y, cancellation below 2^-24 * 0.7 / 0.3
+// a = e^y and m = 1 - a for y <= 0, relative errors about 2e-7 (a's beyond y = -4: 2^-24 |y|):
+//   y > -0.35 : m = -y (1 + y/2 (1 + y/3 (1 + ... y/7))), truncation below 2e-8; a = 1 - m
+//   otherwise : a = e^y; m = 1 - a, cancellation below 2^-24 * 0.7 / 0.3
 // near: the caller knows the first to hold in the whole wave (kappa < 0.35 bounds -l, the
-// usual case: a channel that forgets within a few tokens is rare), which saves 6 of some
+// usual case: a channel that forgets within a few tokens is rare), which saves 7 of some
 // 40 instruction slots per element.
 constexpr float kNearExp = 0.35f;
-__device__ __forceinline__ float one_minus_exp(float y, bool near) {
+__device__ __forceinline__ void decay_pair(float y, bool near, float& a, float& m) {
   float p = __builtin_fmaf(y, 1.0f / 5040.0f, 1.0f / 720.0f);
   p = __builtin_fmaf(y, p, 1.0f / 120.0f);
   p = __builtin_fmaf(y, p, 1.0f / 24.0f);
   p = __builtin_fmaf(y, p, 1.0f / 6.0f);
   p = __builtin_fmaf(y, p, 0.5f);
   p = __builtin_fmaf(y, p, 1.0f);
-  float m = -y * p;
+  m = -y * p;
+  a = 1.0f - m;
   if (!near) {
-    float far = 1.0f - ex2(y * kLog2e);
-    asm volatile("" : "+v"(far));  // a branch, not a select
-    m = y > -kNearExp ? m : far;
+    float e = ex2(y * kLog2e);
+    asm volatile("" : "+v"(e));  // a branch, not a select
+    m = y > -kNearExp ? m : 1.0f - e;
+    a = y > -kNearExp ? a : e;
   }
-  return m;
 }
 
 // The decay e^y of a whole run from the sum y of its l (-inf after a reset: exactly 0).  A
 // product of the run's decays would lose the second-order terms that are below an ulp of 1,
 // all with the same sign, which a channel of long memory adds up over the sequence.
-__device__ __forceinline__ float run_decay(float y) { return 1.0f - one_minus_exp(y, false); }
+__device__ __forceinline__ float run_decay(float y) {
+  float a, m;
+  decay_pair(y, false, a, m);
+  return a;
+}
 
 // sigma(v) and 1 - sigma(v), each to a few ulp relative; saturates without NaN.
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-v * kLog2e)); }
@@ -61,10 +67,11 @@ __device__ __forceinline__ void sigmoid_pair(float v, float& sg, float& om) {
 __device__ __forceinline__ void gated_token(float ra, float rx, float u, float kappa, bool slow, bool reset, float& a,
                                             float& b, float& l) {
   l = -kappa * sigmoid(ra);
-  const float m = one_minus_exp(l, slow);
+  float m;
+  decay_pair(l, slow, a, m);
   const float s = __builtin_amdgcn_sqrtf(m * (2.0f - m));
   const float x = sigmoid(rx) * u;
-  a = reset ? 0.0f : 1.0f - m;
+  a = reset ? 0.0f : a;
   b = reset ? x : s * x;
 }
 
@@ -80,9 +87,9 @@ __device__ __forceinline__ GatedGrad gated_grad(float ra, float rx, float kappa,
   sigmoid_pair(ra, sa, g.oa);
   sigmoid_pair(rx, g.sx, g.ox);
   const float l = -kappa * sa;
-  const float m = one_minus_exp(l, slow);
+  float a, m;
+  decay_pair(l, slow, a, m);
   const float s2 = m * (2.0f - m);
-  const float a = 1.0f - m;
   const float rs = __builtin_amdgcn_rsqf(fmaxf(s2, 1.0e-37f));  // l and s2 are 0 together, then so are s and q
   const float s = s2 * rs;
   const float q = a * a * (l * rs);

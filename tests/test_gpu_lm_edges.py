@@ -6,7 +6,7 @@ Tolerances are those of test_gpu_lm.py where no other is derived at a test."""
 import numpy as np
 import pytest
 
-from test_gpu_lm import _check_sample, _host, _logits
+from test_gpu_lm import DT, _check_gated, _check_sample, _dev, _gated_inputs, _host, _lib, _logits
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -88,3 +88,63 @@ def test_top_k_that_ends_at_the_edge_of_a_bin(above, ties, io):
     kw = {"temperature": [t for t, _ in BIN_EDGES], "top_k": [above + (r % ties) + 1 for r in range(n)]}
     _check_sample(x, noise, io, **kw)
     _check_sample(x, noise, io, **kw, top_p=[0.999999] * n)
+
+
+# ---------------------------------------------------------------------------------- gated recurrence
+
+# relative bound per element of products of up to 60 decays: the exponent's rounding, 2^-24 of a sum of
+# logarithms of 85 at most and of its partial sums (some 1e-5), and a few ulp of each factor (60 * 2e-7)
+PRODUCT_TOL = 1e-4
+
+
+def _rate(lam, c):
+    return c * np.log1p(np.exp(np.float64(np.float32(lam))))
+
+
+def _lam_for(l, c):
+    """lam of the decay e^l of one token at gate_a = 0."""
+    return np.log(np.expm1(-2.0 * l / c)).astype(np.float32)
+
+
+def _relative(got, want):
+    return float(np.max(np.abs(_host(got) / want - 1.0)))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("c", [1.0, 8.0, 30.0])
+@pytest.mark.parametrize("l,L", [(-0.01, 60), (-0.3, 60), (-0.4, 60), (-1.0, 60), (-4.0, 20), (-8.0, 1), (-8.0, 9),
+                                 (-12.0, 6), (-16.0, 1), (-16.0, 5), (-30.0, 2), (-60.0, 1)])
+def test_decays_keep_their_relative_accuracy(l, L, c, io):
+    """Without inputs a state is the product of its decays, and so is the gradient that reaches h0: channels
+    that forget within a token or two, each rate alone, element by element."""
+    lib = _lib()
+    batch, D = 2, 72
+    rng = np.random.default_rng(int(-l * 100) + L)
+    lam = _lam_for(np.full(D, l), c)
+    kappa = _rate(lam, c)[None]
+    h0, dlast = 1.0 + rng.random((batch, D)).astype(np.float32), 1.0 + rng.random((batch, D)).astype(np.float32)
+    zero = torch.zeros((batch, L, D), device="cuda", dtype=DT[io])
+    args = (zero, zero, zero, _dev(lam))
+    decay = np.exp(-0.5 * kappa * L)
+    out, last, states = lib.mamba_gated_scan_fwd(*args, h0=_dev(h0), c=c, return_states=True)
+    assert _relative(last, decay * h0) <= PRODUCT_TOL
+    state = _dev(h0)
+    for _ in range(L):
+        lib.mamba_gated_state_update(state, zero[:, 0].contiguous(), zero[:, 0].contiguous(), zero[:, 0].contiguous(),
+                                     args[3], c=c)
+    assert _relative(state, decay * h0) <= PRODUCT_TOL
+    g = lib.mamba_gated_scan_bwd(*args, zero, h0=_dev(h0), c=c, states=states, dlast_state=_dev(dlast))
+    assert _relative(g["dh0"], decay * dlast) <= PRODUCT_TOL
+    # dL/dl is the same product for every token, and gate_a = 0 halves it times -kappa
+    e = decay * h0 * dlast
+    assert _relative(g["dgate_a"], (-0.25 * kappa * e)[:, None].repeat(L, 1)) <= (PRODUCT_TOL if io == "f32" else 2e-2)
+    dkappa = c / (1.0 + np.exp(-lam.astype(np.float64)))
+    assert _relative(g["dlam"], (-0.5 * dkappa * L * e).sum(0)) <= PRODUCT_TOL
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lam", [0.0, 1.0, 2.0, 4.0])
+@pytest.mark.parametrize("c", [0.5, 8.0])
+def test_layers_of_channels_that_all_forget_fast(c, lam, io):
+    p, opt, dout, dlast = _gated_inputs(2, 300, 70, io, 17, lam=np.full(70, lam))
+    _check_gated(p, opt, dout, dlast, io, c=c, label=(c, lam))
