@@ -130,7 +130,8 @@ struct ScanShared {
 __device__ __forceinline__ uint32_t published(float v) { return v != v ? 0x7fc00000u : __float_as_uint(v); }
 __device__ __forceinline__ float apply(float A, float H, float h) { return A == 0.0f ? H : __builtin_fmaf(A, h, H); }
 
-// (A, H) of the waves before `wave`, in order.
+// (A, H) of the waves before `wave`, in order.  A wave with a reset (S of -inf) starts A anew: added
+// to it, a NaN gate of the waves before would pass the reset.
 template <int C, int W>
 __device__ __forceinline__ void maps_before(int wave, uint32_t lane, float (&A)[C], float (&H)[C],
                                             const ScanShared<C, W>& sm) {
@@ -142,7 +143,8 @@ __device__ __forceinline__ void maps_before(int wave, uint32_t lane, float (&A)[
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         H[c] = apply(sm.A[w][lane * C + c], sm.H[w][lane * C + c], H[c]);
-        A[c] += sm.S[w][lane * C + c];
+        const float S = sm.S[w][lane * C + c];
+        A[c] = S == -__builtin_inff() ? S : A[c] + S;
       }
     }
 #pragma unroll
@@ -569,7 +571,7 @@ __global__ __launch_bounds__(64 * (W + 1), 4) void gated_bwd_kernel(GatedBwdArgs
       p2[i] = b * q.ox;
       e0[i] = __builtin_fmaf(ah, q.l, -q.q * x);
       oa[i] = q.oa;
-      S[0] = cut ? -__builtin_inff() : S[0] + q.l;
+      S[0] += q.l;
       dy[i] = value<1>(raw.dout[i], 0);
       if (HASZ) {
         float sz, dsz;
@@ -580,6 +582,8 @@ __global__ __launch_bounds__(64 * (W + 1), 4) void gated_bwd_kernel(GatedBwdArgs
       fix(a[i]), fix(p1[i]), fix(p2[i]), fix(e0[i]), fix(oa[i]), fix(dy[i]);
       __builtin_amdgcn_sched_barrier(0);
     }
+    // (in whatever place: a NaN before the reset is in H, one behind it does not leave the run)
+    if (HASR && reset != 0) S[0] = -__builtin_inff();
     if (raw.last_token >= 0) {
 #pragma unroll
       for (int i = 0; i < T; ++i) dy[i] += i == raw.last_token ? raw.dlast : 0.0f;

@@ -3,10 +3,11 @@ sums that a small weight decides, temperatures, differences of logits, rates, ga
 of their ranges.
 
 Tolerances are those of test_gpu_lm.py where no other is derived at a test."""
+import lm_ref as R
 import numpy as np
 import pytest
 
-from test_gpu_lm import DT, _check_gated, _check_sample, _dev, _gated_inputs, _host, _lib, _logits
+from test_gpu_lm import (DT, _check_gated, _check_sample, _dev, _gated_dev, _gated_inputs, _host, _lib, _logits)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -148,3 +149,31 @@ def test_decays_keep_their_relative_accuracy(l, L, c, io):
 def test_layers_of_channels_that_all_forget_fast(c, lam, io):
     p, opt, dout, dlast = _gated_inputs(2, 300, 70, io, 17, lam=np.full(70, lam))
     _check_gated(p, opt, dout, dlast, io, c=c, label=(c, lam))
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("which", ["u", "ra", "rx", "z"])
+@pytest.mark.parametrize("shape", [(2, 300, 70), (1, 3000, 64), (2, 700, 4100)], ids=str)
+def test_a_fault_ends_at_a_reset(shape, which, value):
+    """Inputs that are no numbers show where the definition has them and leave the other sequences of the
+    row alone, to the bit: on the same wave, on others of its tile of tokens, and on later tiles."""
+    lib = _lib()
+    batch, L, D = shape
+    for io in ("f32", "bf16"):
+        p, opt, _, _ = _gated_inputs(*shape, io, 18, reset=0)
+        opt["reset"] = np.zeros((batch, L), bool)
+        opt["reset"][:, [L // 3, L // 3 + 5, 2 * L // 3]] = True
+        args, kw = _gated_dev(p, opt, io)
+        clean, clast = lib.mamba_gated_scan_fwd(*args, **kw)
+        holder = p if which in p else opt
+        for r, t, d in ((0, L // 3 - 1, 0), (0, L // 3 + 1, 7), (batch - 1, 2 * L // 3 - 40, D - 1)):
+            holder[which][r, t, d] = value
+        args, kw = _gated_dev(p, opt, io)
+        out, last = lib.mamba_gated_scan_fwd(*args, **kw)
+        with np.errstate(invalid="ignore", over="ignore"):
+            want, wlast, _ = R.gated_fwd(**{k: v.astype(np.float64) for k, v in p.items()}, c=8.0, **opt)
+        assert np.array_equal(np.isfinite(_host(out)), np.isfinite(want))
+        assert torch.equal(last, clast)
+        same = torch.from_numpy(np.isfinite(want)).cuda()
+        if value != value or which in ("u", "z"):  # (an infinite gate gives other numbers, not faults)
+            assert torch.equal(out[same], clean[same])
