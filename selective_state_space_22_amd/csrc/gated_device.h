@@ -47,11 +47,14 @@ __device__ __forceinline__ void decay_pair(float y, bool near, float& a, float& 
 
 // The decay e^y of a whole run from the sum y of its l (-inf after a reset: exactly 0).  A
 // product of the run's decays would lose the second-order terms that are below an ulp of 1,
-// all with the same sign, which a channel of long memory adds up over the sequence.
+// all with the same sign, which a channel of long memory adds up over the sequence.  Only a reset's
+// is 0, the sign to drop an older state: one that underflows is the least normal number, nothing
+// of a state that is a number, while an infinite or NaN one stays what it is.
+constexpr float kLeastDecay = 1.17549435e-38f;
 __device__ __forceinline__ float run_decay(float y) {
   float a, m;
   decay_pair(y, false, a, m);
-  return a;
+  return y == -__builtin_inff() ? 0.0f : fmaxf(a, kLeastDecay);
 }
 
 // sigma(v) and 1 - sigma(v), each to a few ulp relative; saturates without NaN.

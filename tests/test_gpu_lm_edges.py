@@ -177,3 +177,29 @@ def test_a_fault_ends_at_a_reset(shape, which, value):
         same = torch.from_numpy(np.isfinite(want)).cuda()
         if value != value or which in ("u", "z"):  # (an infinite gate gives other numbers, not faults)
             assert torch.equal(out[same], clean[same])
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("c", [0.05, 8.0])
+def test_a_fault_outlasts_every_decay(c, value):
+    """Without a reset a state that is no number stays so, in channels that forget within a token and in
+    those of long memory, through every hand-over; a decay that underflows is no reset."""
+    lib = _lib()
+    p, opt, dout, dlast = _gated_inputs(2, 2500, 70, "f32", 21, z=False, reset=0, lam=np.linspace(-6.0, 2.0, 70))
+    at = 100 + 7 * np.arange(70)
+    for d in range(70):
+        p["u"][1, at[d], d] = value
+    args, kw = _gated_dev(p, opt, "f32")
+    out, last, states = lib.mamba_gated_scan_fwd(*args, c=c, **kw, return_states=True)
+    bad = ~np.isfinite(_host(out))
+    assert not bad[0].any()
+    assert np.array_equal(bad[1], np.arange(2500)[:, None] >= at[None])
+    assert torch.isfinite(last[0]).all() and not torch.isfinite(last[1]).any()
+    p["u"][1] = 0.0  # and a gradient that is no number, towards the first token
+    dout[1, at, np.arange(70)] = value
+    args, kw = _gated_dev(p, opt, "f32")
+    g = lib.mamba_gated_scan_bwd(*args, _dev(dout, "f32"), c=c, **kw, dlast_state=_dev(dlast))
+    assert torch.isfinite(g["dh0"][0]).all() and not torch.isfinite(g["dh0"][1]).any()
+    bad = ~np.isfinite(_host(g["du"]))
+    assert not bad[0].any()
+    assert np.array_equal(bad[1], np.arange(2500)[:, None] <= at[None])
