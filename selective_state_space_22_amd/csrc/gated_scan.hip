@@ -551,7 +551,8 @@ __global__ __launch_bounds__(64 * (W + 1), 4) void gated_bwd_kernel(GatedBwdArgs
   while (true) {
     const float kappa = f.c * softplus(raw.lam);
     const bool slow = __all(kappa < kNearExp);
-    const uint32_t reset = HASR ? (uint32_t)__ballot(raw.reset != 0) : 0;
+    // (past the end every token is a reset: whatever the state there is, its share of dlam is 0)
+    const uint32_t reset = HASR ? ((uint32_t)__ballot(raw.reset != 0) | ~0u << p.n) & ((1u << T) - 1) : 0;
     const Rows r_dz(g.dz, (size_t)p.row * stride, stride, p.n);
     const uint32_t off = bytes<IO>(p.off);
     // The way forward.  A token past the end has loaded zeros: its gradient is 0 and

@@ -203,3 +203,26 @@ def test_a_fault_outlasts_every_decay(c, value):
     bad = ~np.isfinite(_host(g["du"]))
     assert not bad[0].any()
     assert np.array_equal(bad[1], np.arange(2500)[:, None] <= at[None])
+
+
+@pytest.mark.parametrize("shape", [(2, 520, 70), (1, 130, 64), (9, 60, 1024), (3, 2, 5)], ids=str)
+@pytest.mark.parametrize("where", ["h0", "u"])
+def test_values_that_a_reset_cuts_off_stay_out_of_the_sums(where, shape):
+    """h0 before a first token that starts anew, or the input of a last token whose state nothing reads:
+    infinities and NaN there do not reach dlam, whatever is left of the last tile of tokens."""
+    lib = _lib()
+    batch, L, D = shape
+    p, opt, dout, dlast = _gated_inputs(*shape, "f32", 20, z=False, reset=0)
+    opt["reset"] = np.zeros((batch, L), bool)
+    opt["reset"][:, 0 if where == "h0" else -1] = True
+    args, kw = _gated_dev(p, opt, "f32")
+    clean = lib.mamba_gated_scan_bwd(*args, _dev(dout, "f32"), **kw, dlast_state=_dev(dlast))
+    bad = {k: v.copy() for k, v in (("h0", opt["h0"]), ("u", p["u"]))}
+    bad["h0"][:, ::2], bad["h0"][:, 1::2] = np.nan, np.inf
+    bad["u"][:, -1, ::2], bad["u"][:, -1, 1::2] = np.nan, np.inf
+    args, kw = _gated_dev({**p, "u": bad["u"]} if where == "u" else p, {**opt, "h0": bad["h0"]} if where == "h0" else opt,
+                          "f32")
+    g = lib.mamba_gated_scan_bwd(*args, _dev(dout, "f32"), **kw, dlast_state=_dev(dlast))
+    assert torch.isfinite(g["dlam"]).all()
+    for k in ("dlam", "dh0", "du", "dgate_a"):
+        assert torch.equal(g[k], clean[k]), k
