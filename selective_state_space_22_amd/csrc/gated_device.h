@@ -57,10 +57,11 @@ __device__ __forceinline__ float run_decay(float y) {
   return y == -__builtin_inff() ? 0.0f : fmaxf(a, kLeastDecay);
 }
 
-// sigma(v) and 1 - sigma(v), each to a few ulp relative; saturates without NaN.
+// sigma(v) and 1 - sigma(v), each to a few ulp relative; saturates without NaN, a NaN stays one.
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-v * kLog2e)); }
 __device__ __forceinline__ void sigmoid_pair(float v, float& sg, float& om) {
-  const float e = ex2(fminf(-v * kLog2e, 126.0f));  // finite, so that e * sg is a number
+  // finite, so that e * sg is a number; of a NaN and a number, `minimum` takes the NaN
+  const float e = ex2(__builtin_elementwise_minimum(-v * kLog2e, 126.0f));
   sg = rcp(1.0f + e);
   om = e * sg;
 }
@@ -79,15 +80,15 @@ __device__ __forceinline__ void gated_token(float ra, float rx, float u, float k
 }
 
 // The same with what the backward needs:
-//   s, sx = sigma(rx), ox = 1 - sx, oa = 1 - sigma(ra), l (0 on a reset), and
+//   s, sx = sigma(rx), ox = 1 - sx, oa = 1 - sigma(ra), l (both 0 on a reset), and
 //   q = a^2 l / s, 0 where s is 0 (l/s -> 0 with l) and on a reset.
 struct GatedGrad {
   float a, s, sx, ox, oa, l, q;
 };
 __device__ __forceinline__ GatedGrad gated_grad(float ra, float rx, float kappa, bool slow, bool reset) {
   GatedGrad g;
-  float sa;
-  sigmoid_pair(ra, sa, g.oa);
+  float sa, oa;
+  sigmoid_pair(ra, sa, oa);
   sigmoid_pair(rx, g.sx, g.ox);
   const float l = -kappa * sa;
   float a, m;
@@ -99,6 +100,7 @@ __device__ __forceinline__ GatedGrad gated_grad(float ra, float rx, float kappa,
   g.a = reset ? 0.0f : a;
   g.s = reset ? 1.0f : s;
   g.l = reset ? 0.0f : l;
+  g.oa = reset ? 0.0f : oa;  // (a NaN gate left out by a reset does not reach its gradient)
   g.q = reset ? 0.0f : q;
   return g;
 }

@@ -226,3 +226,40 @@ def test_values_that_a_reset_cuts_off_stay_out_of_the_sums(where, shape):
     assert torch.isfinite(g["dlam"]).all()
     for k in ("dlam", "dh0", "du", "dgate_a"):
         assert torch.equal(g[k], clean[k]), k
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("which", ["ra", "rx", "z"])
+def test_gates_that_are_no_numbers_show_in_the_gradients(which, io):
+    """A NaN gate makes NaN what depends on it, in the backward as in the forward, and nothing else."""
+    lib = _lib()
+    p, opt, dout, dlast = _gated_inputs(2, 300, 70, io, 18, reset=0, lam=np.linspace(-6.0, 2.0, 70))
+    opt["reset"] = np.zeros((2, 300), bool)
+    opt["reset"][:, 180] = True
+    (p if which in p else opt)[which][0, 100, 7] = np.nan
+    (p if which in p else opt)[which][1, 233, 69] = np.nan
+    args, kw = _gated_dev(p, opt, io)
+    p64 = {k: v.astype(np.float64) for k, v in p.items()}
+    want = R.gated_bwd(**p64, c=8.0, dout=dout, dlast=dlast, **opt)
+    out, last, states = lib.mamba_gated_scan_fwd(*args, **kw, return_states=True)
+    for given in (states, None):
+        g = lib.mamba_gated_scan_bwd(*args, _dev(dout, io), **kw, states=given, dlast_state=_dev(dlast))
+        for k in want:
+            assert np.array_equal(np.isnan(_host(g[k])), np.isnan(want[k])), k
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_a_gate_that_a_reset_leaves_out_has_no_gradient(io):
+    """l does not enter at a reset token: whatever gate_a holds there, its gradient is 0 and no other sees it."""
+    lib = _lib()
+    p, opt, dout, dlast = _gated_inputs(2, 100, 70, io, 19, reset=0)
+    opt["reset"] = np.zeros((2, 100), bool)
+    opt["reset"][:, [0, 37, 99]] = True
+    args, kw = _gated_dev(p, opt, io)
+    clean = lib.mamba_gated_scan_bwd(*args, _dev(dout, io), **kw, dlast_state=_dev(dlast))
+    for value in (np.nan, np.inf, -np.inf):
+        p["ra"][:, [0, 37, 99]] = value
+        g = lib.mamba_gated_scan_bwd(*_gated_dev(p, opt, io)[0], _dev(dout, io), **kw, dlast_state=_dev(dlast))
+        assert not _host(g["dgate_a"])[:, [0, 37, 99]].any()
+        for k in clean:
+            assert torch.equal(g[k], clean[k]), (value, k)
