@@ -68,11 +68,19 @@ class TokenModel(torch.nn.Module):
         kappa = -torch.log(torch.linspace(0.5, 0.999, dim)) / 8
         self.lam = torch.nn.Parameter(torch.log(torch.expm1(kappa)).to(device))
 
+    @staticmethod
+    def one_document(ids):
+        """The reset marks of rows that each hold one document from its first token on."""
+        reset = torch.zeros(ids.shape, dtype=torch.bool, device=ids.device)
+        reset[:, :1] = True
+        return reset
+
     def inputs(self, x):
         return [p.contiguous() for p in (x @ self.w_in).chunk(4, -1)]
 
     def forward(self, ids, reset=None):
-        """Logits (batch, L, vocab) of ids (batch, L); reset as in mamba_gated_scan_fwd."""
+        """Logits (batch, L, vocab) of ids (batch, L); reset as in mamba_gated_scan_fwd, None: one document a row."""
+        reset = self.one_document(ids) if reset is None else reset
         x = _Embedding.apply(ids, self.table, self.scale)
         u, a, g, z = self.inputs(x)
         y = _GatedScan.apply(u, a, g, self.lam, z, reset)
@@ -83,7 +91,7 @@ class TokenModel(torch.nn.Module):
         """The last token's logits (batch, vocab) and the state behind it."""
         x = mamba_embed_fwd(ids, self.table, self.scale)
         u, a, g, z = self.inputs(x)
-        y, state = mamba_gated_scan_fwd(u, a, g, self.lam, z=z)
+        y, state = mamba_gated_scan_fwd(u, a, g, self.lam, z=z, reset=self.one_document(ids))
         return (x[:, -1] + y[:, -1] @ self.w_out) @ self.table.t(), state
 
     @torch.no_grad()
