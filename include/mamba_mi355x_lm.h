@@ -44,8 +44,8 @@ extern "C" {
  *                               h0 or zero), for mamba_gated_scan_bwd
  *   workspace                 : mamba_gated_scan_fwd_workspace_size() bytes of
  *                               scratch (may be NULL when that is 0)
- * Limits: 0 <= batch <= 65535, seqlen >= 0, 0 <= dim <= 4194304, and
- * batch * ceil(dim / 64) * ceil(seqlen / 64) < 2^31; a c out of range is
+ * Limits: 0 <= batch <= 65535, 0 <= seqlen <= 2^40, 0 <= dim <= 4194304, and
+ * batch * ceil(dim / 64) * ceil(seqlen / 56) < 2^31; a c out of range is
  * MAMBA_ERR_OPTION.  seqlen == 0 writes only last_state (= h0 or zero).
  * Where a sequence is split over workgroups they hand their states over in
  * bounded waits as mamba_scan_fwd's chunks do: mamba_stream_status reports one
