@@ -14,7 +14,8 @@
 // to the bracket, 20 for the scores, 10 for the exact end; a copy of logits and noise would
 // take 46).  One row of 50000 bf16, all filters: 18 us, nearly all of it latency (passes 8,
 // list 4, search and end 6); 64 rows of 50001 without filters 17, some 18 vector instructions
-// to an element on 64 of the 256 compute units.
+// to an element on 64 of the 256 compute units.  A list of more than kList elements costs a row's
+// whole search: 64 rows of 50001 bf16 with a top_k of 50, 600 and 3000 take 19, 31 and 120 us.
 //
 // Masses that are added by atomics are integers (w 2^s, s = 62 - log2 of the row length),
 // so that no sum depends on an order.
@@ -132,9 +133,9 @@ struct Row {
   }
   // f(pieces, base, prefetch) for batch after batch of kElems elements to a thread; f calls
   // prefetch() behind its own loads.  The loops are rolled: a short row takes a few batches in
-  // each pass, and fetching long code costs more than running it.  Eight elements: 256 rows of
-  // 128000 f32, top_p, take 83 us, with four 90, with sixteen 115 (registers spill); 64 rows of
-  // 50001 bf16 19.5 us, with sixteen 22.9.
+  // each pass, and fetching long code costs more than running it.  Eight elements, of what it cost
+  // when they were chosen: 256 rows of 128000 f32, top_p, 83 us, with four 90, with sixteen 115
+  // (registers spill); 64 rows of 50001 bf16 19.5 us, with sixteen 22.9.
   static constexpr int kElems = 8, kBatch = kElems / VEC;
   template <typename F>
   __device__ __forceinline__ void batches(F f) const {
@@ -465,9 +466,9 @@ __device__ __forceinline__ unsigned long long select_listed(const Row<IO>& row, 
   }
 }
 
-// The same for a list of n <= kFew, without steps (1 x 50000, top_k 50 and top_p: 22 us a call
-// in place of 31): each entry's rank is counted, and the
-// masses are summed in the ranks' order (by each wave for itself).  The element with which
+// The same for a list of n <= kFew, without steps (1 x 50000, top_k 50 and top_p: 22 us a call in
+// place of 31 when it came, 20 now): each entry's rank is counted, and the masses are summed in the
+// ranks' order (by each wave for itself).  The element with which
 // the first `most` entries end or, if that is asked for, at which their mass reaches target
 // (0: the share p of it).  mass: that of the thread's first entry.
 template <typename IO>
