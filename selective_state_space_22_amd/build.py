@@ -18,7 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmamba_mi355x.so")
 SOURCES = ["api.cpp", "scan_kernels.hip", "scan_wg.hip", "scan_wp.hip", "scan_bwd.hip", "selection.hip", "scan_complex.hip", "noalloc.hip", "calibrate.hip",
-           "api_lm.cpp", "gated_scan.hip", "embed.hip", "sample.hip"]
+           "api_lm.cpp", "gated_scan.hip", "embed.hip", "sample.hip",
+           "api_layer.cpp", "conv.hip", "ssm_step.hip", "norm.hip", "verify.hip"]
 ARCH = os.environ.get("MAMBA_MI355X_ARCH", "gfx950")
 
 
