@@ -29,7 +29,7 @@ int check_conv(const char* where, int64_t batch, int64_t seqlen, int64_t dim, in
   if (dim > kMaxDim) return fail(MAMBA_ERR_DIM, where, "dim > 4194304");
   if (seqlen > (int64_t(1) << 40)) return fail(MAMBA_ERR_DIM, where, "seqlen > 2^40");
   if (width < 2 || width > 4) return fail(MAMBA_ERR_UNSUPPORTED, where, "width");
-  if (!s6::conv_fits(batch, seqlen, dim)) return fail(MAMBA_ERR_DIM, where, "tensor too large");
+  if (!s6::conv_fits(batch, seqlen, dim, io)) return fail(MAMBA_ERR_DIM, where, "tensor too large");
   return MAMBA_OK;
 }
 
@@ -123,7 +123,7 @@ int mamba_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, in
 
 size_t mamba_conv_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype) {
   if (check_conv("mamba_conv_bwd_workspace_size", batch, seqlen, dim, width, io_dtype) != MAMBA_OK) return 0;
-  return s6::conv_bwd_ws_bytes(batch, seqlen, dim, width);
+  return s6::conv_bwd_ws_bytes(batch, seqlen, dim, width, io_dtype);
 }
 
 int mamba_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype, const void* x,
@@ -149,7 +149,7 @@ int mamba_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, in
   pc.opt(workspace, "workspace");
   if (pc.status != MAMBA_OK) return pc.status;
   if (dim == 0) return MAMBA_OK;
-  const size_t need = s6::conv_bwd_ws_bytes(batch, seqlen, dim, width);
+  const size_t need = s6::conv_bwd_ws_bytes(batch, seqlen, dim, width, io_dtype);
   if (need > 0 && (!workspace || workspace_bytes < need)) return fail(MAMBA_ERR_WORKSPACE, where, "workspace");
   s6::ConvBwdArgs a{};
   a.f = s6::ConvArgs{x, weight, bias, window, reset, nullptr, nullptr, nullptr, batch, seqlen, dim, (int32_t)width,

@@ -18,18 +18,26 @@ namespace s6 {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int V = 4;              // channels per thread
-constexpr int kAhead = 8;         // tokens whose loads are in flight together
-constexpr int64_t kFwdChunk = 64;  // tokens per thread, forward
-constexpr int64_t kThreads = 256 * 8 * 64;  // threads that fill the chip
+// Tokens of a tile: its loads are in flight together while the tile before it is computed.
+constexpr int kTile = 4;
+constexpr int kTileBwd = 4;
+// Channels per thread.
+template <typename IO>
+constexpr int kGroupFwd = sizeof(IO) == 2 ? 2 : 4;
+template <typename IO>
+constexpr int kGroupBwd = 2;
+template <typename IO>
+constexpr int kGroupStep = sizeof(IO) == 2 ? 2 : 4;
+constexpr int64_t kLeastFwd = 8, kMostFwd = 32, kLeastBwd = 8, kMostBwd = 128;  // tokens per thread
+constexpr int64_t kThreads = 256 * 16 * 64;                                   // threads that fill the chip
 
-int64_t groups(int64_t D) { return (D + V - 1) / V; }
+int64_t groups(int64_t D, int v) { return (D + v - 1) / v; }
 
-// Tokens per thread: as many as leave the chip filled, between 8 and `most` (a multiple of 8).
-int64_t chunk_of(int64_t batch, int64_t L, int64_t D, int64_t most) {
-  const double t = (double)batch * (double)L * (double)groups(D) / (double)kThreads;
-  int64_t c = t >= (double)most ? most : (int64_t)t / 8 * 8;
-  return c < 8 ? 8 : c;
+// Tokens per thread: as many as leave the chip filled, between `least` and `most`.
+int64_t chunk_of(int64_t batch, int64_t L, int64_t D, int v, int64_t least, int64_t most) {
+  const double t = (double)batch * (double)L * (double)groups(D, v) / (double)kThreads;
+  const int64_t c = t >= (double)most ? most : (int64_t)t / 8 * 8;
+  return c < least ? least : c;
 }
 
 struct Item {
@@ -40,6 +48,7 @@ struct Item {
 };
 
 // Work item of this thread: channel group fastest (coalesced), then chunk, then batch row.
+template <int V>
 __device__ __forceinline__ Item item_of(int64_t batch, int64_t nchunks, int64_t D) {
   const int64_t G = (D + V - 1) / V;
   const int64_t id = (int64_t)blockIdx.x * kBlock + threadIdx.x;
@@ -65,17 +74,48 @@ __device__ __forceinline__ Item item_of(int64_t batch, int64_t nchunks, int64_t 
   return it;
 }
 
-// Tokens since the last reset as they stand behind token t - 1, at most W.
+// Reset marks as bits: bit k of the marks at token t is the mark of token t - k.  Token t sees the input o
+// tokens back if none of its marks 0 .. o - 1 is set.
+__device__ __forceinline__ bool sees(uint32_t marks, int o) { return (marks & ((1u << o) - 1u)) == 0u; }
+
+// The marks at token t - 1, as far back as they matter.
 template <int W>
-__device__ __forceinline__ int age_before(const uint8_t* reset, int64_t t) {
-  int age = W;
+__device__ __forceinline__ uint32_t marks_before(const uint8_t* reset, int64_t t) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int o = W - 2; o >= 0; --o)
-    if (t - 1 - o >= 0 && reset[t - 1 - o]) age = o;
-  return age;
+  for (int k = 0; k < W - 1; ++k)
+    if (t - 1 - k >= 0 && reset[t - 1 - k]) m |= 1u << k;
+  return m;
 }
 
-template <typename IO, int W, bool FULL>
+// The reset bytes of tokens t .. t + T - 1 of a row that ends at `to`, the first token's lowest.  They stay raw
+// until their tile is computed: looking at them earlier would wait for the loads around them.
+template <int T>
+using bytes_t = std::conditional_t<T == 4, uint32_t, uint64_t>;
+template <int T>
+__device__ __forceinline__ bytes_t<T> reset_bytes(const uint8_t* reset, int64_t t, int64_t to) {
+  static_assert(T == 4 || T == 8, "bytes of a word");
+  bytes_t<T> m = 0;
+  if (t + T <= to) {
+    __builtin_memcpy(&m, reset + t, T);
+  } else {
+#pragma unroll
+    for (int u = 0; u < T; ++u)
+      if (t + u < to) m |= (bytes_t<T>)reset[t + u] << (8 * u);
+  }
+  return m;
+}
+// As marks, the first token highest.
+template <int T>
+__device__ __forceinline__ uint32_t marks_of(bytes_t<T> bytes) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int u = 0; u < T; ++u)
+    if (bytes & ((bytes_t<T>)0xff << (8 * u))) m |= 1u << (T - 1 - u);
+  return m;
+}
+
+template <typename IO, int V, int W, bool FULL>
 __device__ __forceinline__ raw_t<IO, V> row_before(const ConvArgs& a, const Item& it, int64_t t) {
   // input row t < L; negative t: the carried window
   if (t >= 0) return load_raw<IO, V, FULL>(static_cast<const IO*>(a.x) + (it.b * a.L + t) * a.D + it.d0, it.nv);
@@ -83,86 +123,118 @@ __device__ __forceinline__ raw_t<IO, V> row_before(const ConvArgs& a, const Item
   return load_raw<IO, V, FULL>(static_cast<const IO*>(a.window) + (it.b * (W - 1) + (t + W - 1)) * a.D + it.d0, it.nv);
 }
 
-template <typename IO, int W, bool FULL>
-__device__ __forceinline__ void load_weights(const ConvArgs& a, const Item& it, float (&w)[W][V],
-                                             float (&bias)[V]) {
+// Weights by tap, and the bias, of the item's channels.
+template <int V, int W, bool FULL>
+__device__ __forceinline__ void load_weights(const float* weight, const float* bias, int64_t d0, int nv,
+                                             float (&w)[W][V], float (&b)[V]) {
+  float q[W][V];  // the V W weights side by side
+#pragma unroll
+  for (int k = 0; k < W; ++k) widen<float, V>(load_raw<float, V, FULL>(weight + d0 * W + k * V, nv * W - k * V), q[k]);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const bool in = FULL || i < it.nv;
+    b[i] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = in ? a.weight[(it.d0 + i) * W + j] : 0.0f;
-    bias[i] = in && a.bias ? a.bias[it.d0 + i] : 0.0f;
+    for (int j = 0; j < W; ++j) w[j][i] = q[(i * W + j) / V][(i * W + j) % V];
+  }
+  if (bias) widen<float, V>(load_raw<float, V, FULL>(bias + d0, nv), b);
+}
+
+// c_t of one token: x[-o] is the input o tokens back; CUT: of these only what its marks let it see.
+template <int V, int W, bool CUT>
+__device__ __forceinline__ void conv_sum(const float (&w)[W][V], const float (&bias)[V], const float (*x)[V],
+                                         uint32_t marks, float (&c)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) c[i] = bias[i];
+#pragma unroll
+  for (int o = W - 1; o >= 0; --o) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float s = __builtin_fmaf(w[W - 1 - o][i], x[-o][i], c[i]);
+      c[i] = !CUT || sees(marks, o) ? s : c[i];
+    }
   }
 }
 
 // The last W - 1 inputs of the row, zero bits where a reset behind them cut them off.
-template <typename IO, int W, bool FULL>
+template <typename IO, int V, int W, bool FULL>
 __device__ __forceinline__ void conv_tail(const ConvArgs& a, const Item& it, int64_t len) {
-  const int age = a.reset ? age_before<W>(a.reset + it.b * a.L, len) : W;
+  const uint32_t marks = a.reset ? marks_before<W>(a.reset + it.b * a.L, len) : 0u;
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     const int back = W - 2 - j;  // tokens between the entry and the last token
-    const raw_t<IO, V> v = back <= age ? row_before<IO, W, FULL>(a, it, len - 1 - back) : raw_t<IO, V>(0u);
+    const raw_t<IO, V> v = sees(marks, back) ? row_before<IO, V, W, FULL>(a, it, len - 1 - back) : raw_t<IO, V>(0u);
     store_raw<IO, V, FULL>(static_cast<IO*>(a.last) + (it.b * (W - 1) + j) * a.D + it.d0, v, it.nv);
   }
 }
 
-template <typename IO, int W, bool RESET, bool FULL>
+template <typename IO, int V, int W, bool ACT, bool RESET, bool FULL>
 __device__ __forceinline__ void conv_chunk(const ConvArgs& a, const Item& it, int64_t t0, int64_t t1, int64_t len) {
-  IO* out = static_cast<IO*>(a.out) + it.b * a.L * a.D + it.d0;
-  const IO* x = static_cast<const IO*>(a.x) + it.b * a.L * a.D + it.d0;
-  const int64_t e1 = t1 < len ? t1 : len;
-  if (t0 < e1) {
-    float w[W][V], bias[V];
-    load_weights<IO, W, FULL>(a, it, w, bias);
-    raw_t<IO, V> row[W - 1 + kAhead];  // the W - 1 rows before the batch, then the batch
+  constexpr int T = kTile;
+  const int64_t D = a.D;
+  IO* out = static_cast<IO*>(a.out) + (it.b * a.L + t0) * D + it.d0;
+  const IO* x = static_cast<const IO*>(a.x) + (it.b * a.L + t0) * D + it.d0;
+  const uint8_t* reset = RESET ? a.reset + it.b * a.L + t0 : nullptr;
+  const int n = (int)((t1 < len ? t1 : len) - t0);  // tokens of the chunk that exist
+  if (n > 0) {
+    float w[W][V], bias[V], row[W - 1 + T][V];  // row: the W - 1 inputs before the tile, then the tile
+    load_weights<V, W, FULL>(a.weight, a.bias, it.d0, it.nv, w, bias);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) row[j] = row_before<IO, W, FULL>(a, it, t0 - (W - 1) + j);
-    int age = W;
-    if constexpr (RESET) age = age_before<W>(a.reset + it.b * a.L, t0);
-    raw_t<IO, V> next[kAhead];
+    for (int j = 0; j < W - 1; ++j) widen<IO, V>(row_before<IO, V, W, FULL>(a, it, t0 - (W - 1) + j), row[j]);
+    uint32_t marks = RESET ? marks_before<W>(a.reset + it.b * a.L, t0) : 0u;
+    raw_t<IO, V> next[T];
+    bytes_t<T> nr = 0;  // the tile's reset bytes
+    auto load = [&](int t) {
+      if (t + T <= n) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      next[u] = t0 + u < e1 ? load_raw<IO, V, FULL>(x + (t0 + u) * a.D, it.nv) : raw_t<IO, V>(0u);
-    for (int64_t t = t0; t < e1; t += kAhead) {
+        for (int u = 0; u < T; ++u) next[u] = load_raw<IO, V, FULL>(x + u * D, it.nv);
+      } else {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) row[W - 1 + u] = next[u];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (t + kAhead + u < e1) next[u] = load_raw<IO, V, FULL>(x + (t + kAhead + u) * a.D, it.nv);
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (t + u >= e1) break;
-        if constexpr (RESET) age = a.reset[it.b * a.L + t + u] ? 0 : (age < W ? age + 1 : W);
-        float c[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) c[i] = bias[i];
-#pragma unroll
-        for (int o = W - 1; o >= 0; --o) {
-          float v[V];
-          widen<IO, V>(row[W - 1 + u - o], v);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float s = __builtin_fmaf(w[W - 1 - o][i], v[i], c[i]);
-            c[i] = !RESET || o <= age ? s : c[i];
-          }
+        for (int u = 0; u < T; ++u) {
+          next[u] = raw_t<IO, V>(0u);
+          if (t + u < n) next[u] = load_raw<IO, V, FULL>(x + u * D, it.nv);
         }
-        if (a.silu)
+      }
+      if (RESET) nr = reset_bytes<T>(reset, t, n);
+    };
+    load(0);
+    for (int t = 0; t < n; t += T) {
+#pragma unroll
+      for (int u = 0; u < T; ++u) widen<IO, V>(next[u], row[W - 1 + u]);
+      const bool cut = RESET && (nr != 0 || !sees(marks, W - 2));
+      marks = (marks << T) | (RESET ? marks_of<T>(nr) : 0u);
+      x += T * D;
+      load(t + T);
+      auto token = [&](int u, auto masked) {
+        float c[V];
+        conv_sum<V, W, decltype(masked)::value>(w, bias, &row[W - 1 + u], marks >> (T - 1 - u), c);
+        if constexpr (ACT)
 #pragma unroll
           for (int i = 0; i < V; ++i) c[i] = silu(c[i]);
-        store_raw<IO, V, FULL>(out + (t + u) * a.D, narrow<IO, V>(c), it.nv);
-      }
+        if (t + u < n) store_raw<IO, V, FULL>(out + u * D, narrow<IO, V>(c), it.nv);
+      };
+      // few tiles hold a reset or the tokens behind one: only those mask their taps
+      if (RESET && __any(cut)) {
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) row[j] = row[kAhead + j];
+        for (int u = 0; u < T; ++u) token(u, std::true_type());
+      } else {
+#pragma unroll
+        for (int u = 0; u < T; ++u) token(u, std::false_type());
+      }
+      out += T * D;
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) row[j][i] = row[T + j][i];
     }
   }
-  for (int64_t t = t0 > len ? t0 : len; t < t1; ++t) store_raw<IO, V, FULL>(out + t * a.D, raw_t<IO, V>(0u), it.nv);
+  IO* behind = static_cast<IO*>(a.out) + it.b * a.L * D + it.d0;
+  for (int64_t t = t0 > len ? t0 : len; t < t1; ++t) store_raw<IO, V, FULL>(behind + t * D, raw_t<IO, V>(0u), it.nv);
 }
 
-template <typename IO, int W, bool RESET>
+template <typename IO, int V, int W, bool ACT, bool RESET>
 __global__ __launch_bounds__(kBlock) void conv_fwd_kernel(ConvArgs a, int64_t nchunks, int64_t chunk) {
   // one more item per (row, channel group) than there are chunks: the window carried on
-  const Item it = item_of(a.batch, nchunks + 1, a.D);
+  const Item it = item_of<V>(a.batch, nchunks + 1, a.D);
   if (!it.in) return;
   int64_t len = a.L;
   if (a.lengths) {
@@ -172,148 +244,225 @@ __global__ __launch_bounds__(kBlock) void conv_fwd_kernel(ConvArgs a, int64_t nc
   const bool full = it.nv == V;
   if (it.chunk == nchunks) {
     if (!a.last) return;
-    if (full) conv_tail<IO, W, true>(a, it, len);
-    else conv_tail<IO, W, false>(a, it, len);
+    if (full) conv_tail<IO, V, W, true>(a, it, len);
+    else conv_tail<IO, V, W, false>(a, it, len);
     return;
   }
   const int64_t t0 = it.chunk * chunk, t1 = t0 + chunk < a.L ? t0 + chunk : a.L;
-  if (full) conv_chunk<IO, W, RESET, true>(a, it, t0, t1, len);
-  else conv_chunk<IO, W, RESET, false>(a, it, t0, t1, len);
+  if (full) conv_chunk<IO, V, W, ACT, RESET, true>(a, it, t0, t1, len);
+  else conv_chunk<IO, V, W, ACT, RESET, false>(a, it, t0, t1, len);
 }
 
 // ---------------------------------------------------------------- backward
 
-// Part sums of dweight and dbias: (item row, W + 1, D), an item row per (batch row, chunk).
-template <typename IO, int W, bool RESET, bool FULL>
+// Part sums of dweight and dbias: (item row, W + 1, D), an item row per (batch row, chunk).  An item adds the
+// sums of its tokens [t0, t1) and writes dx of the tokens that these complete, [t0 - (W - 1), t1 - (W - 1)),
+// and the last of a row up to the sequence's end; the dc of the W - 1 tokens before t0 is formed again.
+// Whole tiles that no reset cuts take the unrolled path, anything else goes token by token.
+template <typename IO, int V, int W, bool ACT, bool RESET, bool FULL>
 __device__ __forceinline__ void conv_bwd_chunk(const ConvBwdArgs& a, const Item& it, int64_t t0, int64_t t1,
                                                float* part) {
+  constexpr int T = kTileBwd, H = W - 1;
   const ConvArgs& f = a.f;
-  const int64_t L = f.L, D = f.D, base = it.b * L * D + it.d0;
+  const int64_t D = f.D, base = it.b * f.L * D + it.d0;
   const IO* x = static_cast<const IO*>(f.x) + base;
   const IO* dout = static_cast<const IO*>(a.dout) + base;
   IO* dx = static_cast<IO*>(a.dx) + base;
-  const raw_t<IO, V> zero(0u);
-  float w[W][V], bias[V];
-  load_weights<IO, W, FULL>(f, it, w, bias);
-  float dw[W][V], db[V], acc[W][V];  // acc[o]: gradient so far at token t - o
-  raw_t<IO, V> hist[W - 1];               // input rows t - (W - 1) .. t - 1
+  const uint8_t* reset = RESET ? f.reset + it.b * f.L : nullptr;
+  float w[W][V], bias[V], dw[W][V], db[V];
+  load_weights<V, W, FULL>(f.weight, f.bias, it.d0, it.nv, w, bias);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     db[i] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][i] = acc[j][i] = 0.0f;
+    for (int j = 0; j < W; ++j) dw[j][i] = 0.0f;
   }
+  float row[H + T][V], g[H + T][V];  // inputs and dc of the W - 1 tokens before the tile, then the tile
+  const int64_t first = t0 < H ? 0 : t0 - H;
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) hist[j] = row_before<IO, W, FULL>(f, it, t0 - (W - 1) + j);
-  int age = W;
-  if constexpr (RESET) age = age_before<W>(f.reset + it.b * L, t0);
-  // The W - 1 tokens behind the chunk still send gradients into it; behind the sequence there is
-  // only what the carried window sends.
-  const int64_t end = t1 + W - 1, live = end < L ? end : L;
-  raw_t<IO, V> nx[kAhead], nd[kAhead];
+  for (int j = 0; j < H; ++j) {
+    widen<IO, V>(row_before<IO, V, W, FULL>(f, it, first - H + j), row[j]);
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
-    nx[u] = t0 + u < live ? load_raw<IO, V, FULL>(x + (t0 + u) * D, it.nv) : zero;
-    nd[u] = t0 + u < live ? load_raw<IO, V, FULL>(dout + (t0 + u) * D, it.nv) : zero;
+    for (int i = 0; i < V; ++i) g[j][i] = 0.0f;
   }
-  for (int64_t tb = t0; tb < end; tb += kAhead) {
-    raw_t<IO, V> cx[kAhead], cd[kAhead];
+  uint32_t marks = RESET ? marks_before<W>(reset, first) : 0u;
+
+  raw_t<IO, V> nx[T], nd[T];  // the next tokens' inputs and dout
+  bytes_t<T> nr = 0;            // their reset bytes
+  auto load = [&](int64_t t, int64_t to) {
+    if (t + T <= to) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      cx[u] = nx[u];
-      cd[u] = nd[u];
-    }
+      for (int u = 0; u < T; ++u) {
+        nx[u] = load_raw<IO, V, FULL>(x + (t + u) * D, it.nv);
+        nd[u] = load_raw<IO, V, FULL>(dout + (t + u) * D, it.nv);
+      }
+    } else {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (tb + kAhead + u < live) {
-        nx[u] = load_raw<IO, V, FULL>(x + (tb + kAhead + u) * D, it.nv);
-        nd[u] = load_raw<IO, V, FULL>(dout + (tb + kAhead + u) * D, it.nv);
+      for (int u = 0; u < T; ++u) {
+        nx[u] = nd[u] = raw_t<IO, V>(0u);
+        if (t + u < to) {
+          nx[u] = load_raw<IO, V, FULL>(x + (t + u) * D, it.nv);
+          nd[u] = load_raw<IO, V, FULL>(dout + (t + u) * D, it.nv);
+        }
       }
     }
+    if (RESET) nr = reset_bytes<T>(reset, t, to);
+  };
+  // One token, whatever it is: before the chunk (only its dc counts), in it, or behind the sequence (only
+  // what leaves).
+  auto single = [&](int64_t t, raw_t<IO, V> rx, raw_t<IO, V> rd, bool mark) {
+    widen<IO, V>(rx, row[H]);
+    widen<IO, V>(rd, g[H]);
+    marks = (marks << 1) | (RESET && mark ? 1u : 0u);
+    if (t < t1) {
+      if constexpr (ACT) {
+        float c[V];
+        conv_sum<V, W, RESET>(w, bias, &row[H], marks, c);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int64_t t = tb + u;
-      if (t >= end) break;
-      if (t < live) {
-        if constexpr (RESET) age = f.reset[it.b * L + t] ? 0 : (age < W ? age + 1 : W);
-        float tap[W][V], g[V];  // tap[o]: input t - o
-        widen<IO, V>(cx[u], tap[0]);
-#pragma unroll
-        for (int o = 1; o < W; ++o) widen<IO, V>(hist[W - 1 - o], tap[o]);
-        widen<IO, V>(cd[u], g);
-        if (f.silu) {
-          float c[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) c[i] = bias[i];
-#pragma unroll
-          for (int o = W - 1; o >= 0; --o)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float s = __builtin_fmaf(w[W - 1 - o][i], tap[o][i], c[i]);
-              c[i] = !RESET || o <= age ? s : c[i];
-            }
-#pragma unroll
-          for (int i = 0; i < V; ++i) g[i] *= silu_slope(c[i]);
-        }
-#pragma unroll
-        for (int o = 0; o < W; ++o) {
-          const bool on = !RESET || o <= age;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float s = __builtin_fmaf(w[W - 1 - o][i], g[i], acc[o][i]);
-            acc[o][i] = on ? s : acc[o][i];
-          }
-          if (t < t1) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float s = __builtin_fmaf(g[i], tap[o][i], dw[W - 1 - o][i]);
-              dw[W - 1 - o][i] = on ? s : dw[W - 1 - o][i];
-            }
-          }
-        }
-        if (t < t1)
-#pragma unroll
-          for (int i = 0; i < V; ++i) db[i] += g[i];
+        for (int i = 0; i < V; ++i) g[H][i] *= silu_slope(c[i]);
       }
-      // token (or window entry) p = t - (W - 1) has all its gradients
-      const int64_t p = t - (W - 1);
-      if (t >= L && a.dlast && (!RESET || L - 1 - p <= age)) {
+      if (t >= t0) {
+#pragma unroll
+        for (int o = 0; o < W; ++o)
+          if (!RESET || sees(marks, o))
+#pragma unroll
+            for (int i = 0; i < V; ++i) dw[H - o][i] = __builtin_fmaf(g[H][i], row[H - o][i], dw[H - o][i]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) db[i] += g[H][i];
+      }
+    }
+    if (t >= t0) {
+      // the token (or window entry) p = t - (W - 1) has all its gradients: token p + o sees p if none of
+      // the marks of tokens p + 1 .. p + o is set
+      const int64_t p = t - H;
+      float acc[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll
+      for (int o = 0; o < W; ++o)
+        if (!RESET || sees(marks >> (H - o), o))
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[H - o][i], g[o][i], acc[i]);
+      if (t >= f.L && a.dlast && (!RESET || sees(marks, H))) {
         float v[V];
-        widen<IO, V>(load_raw<IO, V, FULL>(
-                      static_cast<const IO*>(a.dlast) + (it.b * (W - 1) + (p - (L - (W - 1)))) * D + it.d0, it.nv), v);
+        widen<IO, V>(load_raw<IO, V, FULL>(static_cast<const IO*>(a.dlast) + (it.b * H + (t - f.L)) * D + it.d0, it.nv), v);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[W - 1][i] += v[i];
+        for (int i = 0; i < V; ++i) acc[i] += v[i];
       }
-      if (p >= t0) store_raw<IO, V, FULL>(dx + p * D, narrow<IO, V>(acc[W - 1]), it.nv);
-      else if (t0 == 0 && a.dwindow)
-        store_raw<IO, V, FULL>(static_cast<IO*>(a.dwindow) + (it.b * (W - 1) + (p + W - 1)) * D + it.d0,
-                            narrow<IO, V>(acc[W - 1]), it.nv);
+      if (p >= 0) store_raw<IO, V, FULL>(dx + p * D, narrow<IO, V>(acc), it.nv);
+      else if (a.dwindow)
+        store_raw<IO, V, FULL>(static_cast<IO*>(a.dwindow) + (it.b * H + (p + H)) * D + it.d0, narrow<IO, V>(acc), it.nv);
+    }
 #pragma unroll
-      for (int o = W - 1; o > 0; --o)
+    for (int j = 0; j < H; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[o][i] = acc[o - 1][i];
+      for (int i = 0; i < V; ++i) {
+        row[j][i] = row[j + 1][i];
+        g[j][i] = g[j + 1][i];
+      }
+  };
+
+  // the first of those in flight
+  auto pop = [&](int64_t t) {
+    single(t, nx[0], nd[0], (nr & 0xffu) != 0);
+    nr >>= 8;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[0][i] = 0.0f;
+    for (int u = 0; u + 1 < T; ++u) {
+      nx[u] = nx[u + 1];
+      nd[u] = nd[u + 1];
+    }
+  };
+  {
+    // a chunk that is not the first has the W - 1 tokens before it
+    raw_t<IO, V> px[H], pd[H];
+    uint32_t pm = 0;
 #pragma unroll
-      for (int j = 0; j + 1 < W - 1; ++j) hist[j] = hist[j + 1];
-      hist[W - 2] = cx[u];
+    for (int u = 0; u < H; ++u) {
+      px[u] = pd[u] = raw_t<IO, V>(0u);
+      if (first + u < t0) {
+        px[u] = load_raw<IO, V, FULL>(x + (first + u) * D, it.nv);
+        pd[u] = load_raw<IO, V, FULL>(dout + (first + u) * D, it.nv);
+        if (RESET) pm |= (uint32_t)reset[first + u] << (8 * u);
+      }
+    }
+    load(t0, t1);
+#pragma unroll 1
+    for (int64_t t = first; t < t0; ++t) {
+      single(t, px[0], pd[0], (pm & 0xffu) != 0);
+      pm >>= 8;
+#pragma unroll
+      for (int u = 0; u + 1 < H; ++u) {
+        px[u] = px[u + 1];
+        pd[u] = pd[u + 1];
+      }
     }
   }
+  int64_t t = t0;
+  for (; t + T <= t1; t += T) {
+    if (__any(t < H || (RESET && (nr != 0 || !sees(marks, W - 2))))) {
+#pragma unroll 1
+      for (int u = 0; u < T; ++u) pop(t + u);
+      load(t + T, t1);
+      continue;
+    }
+#pragma unroll
+    for (int u = 0; u < T; ++u) {
+      widen<IO, V>(nx[u], row[H + u]);
+      widen<IO, V>(nd[u], g[H + u]);
+    }
+    marks <<= T;
+    load(t + T, t1);
+#pragma unroll
+    for (int u = 0; u < T; ++u) {
+      if constexpr (ACT) {
+        float c[V];
+        conv_sum<V, W, false>(w, bias, &row[H + u], 0u, c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[H + u][i] *= silu_slope(c[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        db[i] += g[H + u][i];
+#pragma unroll
+        for (int o = 0; o < W; ++o) dw[H - o][i] = __builtin_fmaf(g[H + u][i], row[H + u - o][i], dw[H - o][i]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < T; ++u) {
+      float acc[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        acc[i] = 0.0f;
+#pragma unroll
+        for (int o = 0; o < W; ++o) acc[i] = __builtin_fmaf(w[H - o][i], g[u + o][i], acc[i]);
+      }
+      store_raw<IO, V, FULL>(dx + (t + u - H) * D, narrow<IO, V>(acc), it.nv);
+    }
+#pragma unroll
+    for (int j = 0; j < H; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        row[j][i] = row[T + j][i];
+        g[j][i] = g[T + j][i];
+      }
+  }
+  const int64_t end = t1 < f.L ? t1 : f.L + H;
+#pragma unroll 1
+  for (; t < end; ++t) pop(t);  // what is behind t1 was loaded as zeros and no marks
 #pragma unroll
   for (int j = 0; j <= W; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (FULL || i < it.nv) part[(int64_t)j * D + it.d0 + i] = j < W ? dw[j < W ? j : 0][i] : db[i];
+    store_raw<float, V, FULL>(part + j * D + it.d0, narrow<float, V>(j < W ? dw[j < W ? j : 0] : db), it.nv);
 }
 
-template <typename IO, int W, bool RESET>
-__global__ __launch_bounds__(kBlock) void conv_bwd_kernel(ConvBwdArgs a, int64_t nchunks, int64_t chunk, float* part) {
-  const Item it = item_of(a.f.batch, nchunks, a.f.D);
+template <typename IO, int V, int W, bool ACT, bool RESET>
+__global__ __launch_bounds__(kBlock) void conv_bwd_kernel(ConvBwdArgs a, int64_t nchunks, int64_t chunk,
+                                                             float* part) {
+  const Item it = item_of<V>(a.f.batch, nchunks, a.f.D);
   if (!it.in) return;
   const int64_t t0 = it.chunk * chunk, t1 = t0 + chunk < a.f.L ? t0 + chunk : a.f.L;
   float* p = part + (it.b * nchunks + it.chunk) * (W + 1) * a.f.D;
-  if (it.nv == V) conv_bwd_chunk<IO, W, RESET, true>(a, it, t0, t1, p);
-  else conv_bwd_chunk<IO, W, RESET, false>(a, it, t0, t1, p);
+  if (it.nv == V) conv_bwd_chunk<IO, V, W, ACT, RESET, true>(a, it, t0, t1, p);
+  else conv_bwd_chunk<IO, V, W, ACT, RESET, false>(a, it, t0, t1, p);
 }
 
 // dweight and dbias: the part sums of a column (one of (W + 1) D).
@@ -329,24 +478,18 @@ __global__ __launch_bounds__(1024) void conv_sum_kernel(const float* part, int64
 
 // ---------------------------------------------------------------- one token
 
-template <typename IO, int W, bool FULL>
+template <typename IO, int V, int W, bool FULL>
 __device__ __forceinline__ void conv_step(const ConvStepArgs& a, const Item& it, int64_t slot) {
   IO* win = static_cast<IO*>(a.window) + slot * (W - 1) * a.D + it.d0;
   raw_t<IO, V> row[W];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) row[j] = load_raw<IO, V, FULL>(win + j * a.D, it.nv);
   row[W - 1] = load_raw<IO, V, FULL>(static_cast<const IO*>(a.x) + it.b * a.D + it.d0, it.nv);
-  float c[V];
+  float w[W][V], bias[V], v[W][V], c[V];
+  load_weights<V, W, FULL>(a.weight, a.bias, it.d0, it.nv, w, bias);
 #pragma unroll
-  for (int i = 0; i < V; ++i) c[i] = a.bias && (FULL || i < it.nv) ? a.bias[it.d0 + i] : 0.0f;
-#pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float v[V];
-    widen<IO, V>(row[j], v);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      c[i] = __builtin_fmaf(FULL || i < it.nv ? a.weight[(it.d0 + i) * W + j] : 0.0f, v[i], c[i]);
-  }
+  for (int j = 0; j < W; ++j) widen<IO, V>(row[j], v[j]);
+  conv_sum<V, W, false>(w, bias, &v[W - 1], 0u, c);
   if (a.silu)
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = silu(c[i]);
@@ -355,14 +498,14 @@ __device__ __forceinline__ void conv_step(const ConvStepArgs& a, const Item& it,
   for (int j = 0; j < W - 1; ++j) store_raw<IO, V, FULL>(win + j * a.D, row[j + 1], it.nv);
 }
 
-template <typename IO, int W>
+template <typename IO, int V, int W>
 __global__ __launch_bounds__(kBlock) void conv_step_kernel(ConvStepArgs a) {
-  const Item it = item_of(a.batch, 1, a.D);
+  const Item it = item_of<V>(a.batch, 1, a.D);
   if (!it.in) return;
   const int64_t slot = a.slots ? a.slots[it.b] : it.b;
   if (slot < 0 || slot >= a.nslots) return;
-  if (it.nv == V) conv_step<IO, W, true>(a, it, slot);
-  else conv_step<IO, W, false>(a, it, slot);
+  if (it.nv == V) conv_step<IO, V, W, true>(a, it, slot);
+  else conv_step<IO, V, W, false>(a, it, slot);
 }
 
 // ---------------------------------------------------------------- plans and launches
@@ -371,33 +514,39 @@ struct ConvPlan {
   int64_t chunk, nchunks;
 };
 
-ConvPlan plan_fwd(int64_t batch, int64_t L, int64_t D) {
-  const int64_t c = chunk_of(batch, L, D, kFwdChunk);
+int group_fwd(int io) { return io == kIoBF16 ? kGroupFwd<uint16_t> : kGroupFwd<float>; }
+int group_bwd(int io) { return io == kIoBF16 ? kGroupBwd<uint16_t> : kGroupBwd<float>; }
+int group_step(int io) { return io == kIoBF16 ? kGroupStep<uint16_t> : kGroupStep<float>; }
+
+ConvPlan plan_fwd(int64_t batch, int64_t L, int64_t D, int io) {
+  const int64_t c = chunk_of(batch, L, D, group_fwd(io), kLeastFwd, kMostFwd);
   return {c, (L + c - 1) / c};
 }
 
-ConvPlan plan_conv_bwd(int64_t batch, int64_t L, int64_t D) {
-  const int64_t c = chunk_of(batch, L, D, 128);
+ConvPlan plan_conv_bwd(int64_t batch, int64_t L, int64_t D, int io) {
+  const int64_t c = chunk_of(batch, L, D, group_bwd(io), kLeastBwd, kMostBwd);
   const int64_t n = (L + c - 1) / c;
   return {c, n < 1 ? 1 : n};  // a sequence of no tokens still hands dlast_window on
 }
 
-unsigned blocks(int64_t batch, int64_t n, int64_t D) {
-  return (unsigned)((batch * n * groups(D) + kBlock - 1) / kBlock);
+unsigned blocks(int64_t batch, int64_t n, int64_t D, int v) {
+  return (unsigned)((batch * n * groups(D, v) + kBlock - 1) / kBlock);
 }
 
-template <typename IO, int W>
+template <typename IO, int W, bool ACT>
 void fwd_w(const ConvArgs& a, const ConvPlan& p, unsigned grid, hipStream_t s) {
-  if (a.reset) hipLaunchKernelGGL((conv_fwd_kernel<IO, W, true>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk);
-  else hipLaunchKernelGGL((conv_fwd_kernel<IO, W, false>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk);
+  if (a.reset)
+    hipLaunchKernelGGL((conv_fwd_kernel<IO, kGroupFwd<IO>, W, ACT, true>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk);
+  else
+    hipLaunchKernelGGL((conv_fwd_kernel<IO, kGroupFwd<IO>, W, ACT, false>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk);
 }
 
-template <typename IO, int W>
+template <typename IO, int W, bool ACT>
 void bwd_w(const ConvBwdArgs& a, const ConvPlan& p, unsigned grid, float* part, hipStream_t s) {
   if (a.f.reset)
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, W, true>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk, part);
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, kGroupBwd<IO>, W, ACT, true>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk, part);
   else
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, W, false>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk, part);
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, kGroupBwd<IO>, W, ACT, false>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk, part);
 }
 
 template <typename F>
@@ -416,30 +565,38 @@ hipError_t by_type_and_width(int io, int W, F f) {
 
 }  // namespace
 
-bool conv_fits(int64_t batch, int64_t L, int64_t D) {
+bool conv_fits(int64_t batch, int64_t L, int64_t D, int io) {
   // a launch counts its threads in 32 bits; the forward has one item more per row than it has chunks
-  const double g = (double)batch * (double)groups(D), most = 4294967296.0 - kBlock;
-  return g * ((double)plan_fwd(batch, L, D).nchunks + 1.0) < most && g * (double)plan_conv_bwd(batch, L, D).nchunks < most;
+  const double b = (double)batch, most = 4294967296.0 - kBlock;
+  return b * (double)groups(D, group_fwd(io)) * ((double)plan_fwd(batch, L, D, io).nchunks + 1.0) < most &&
+         b * (double)groups(D, group_bwd(io)) * (double)plan_conv_bwd(batch, L, D, io).nchunks < most &&
+         b * (double)groups(D, group_step(io)) < most;
 }
 
 hipError_t launch_conv_fwd(const ConvArgs& a, int io, hipStream_t s) {
-  const ConvPlan p = plan_fwd(a.batch, a.L, a.D);
-  const unsigned grid = blocks(a.batch, p.nchunks + 1, a.D);
-  return by_type_and_width(io, a.W, [&](auto t, auto w) { fwd_w<decltype(t), decltype(w)::value>(a, p, grid, s); });
+  const ConvPlan p = plan_fwd(a.batch, a.L, a.D, io);
+  const unsigned grid = blocks(a.batch, p.nchunks + 1, a.D, group_fwd(io));
+  return by_type_and_width(io, a.W, [&](auto t, auto w) {
+    if (a.silu) fwd_w<decltype(t), decltype(w)::value, true>(a, p, grid, s);
+    else fwd_w<decltype(t), decltype(w)::value, false>(a, p, grid, s);
+  });
 }
 
-size_t conv_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int64_t W) {
-  return (size_t)batch * (size_t)plan_conv_bwd(batch, L, D).nchunks * (size_t)(W + 1) * (size_t)D * sizeof(float);
+size_t conv_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int64_t W, int io) {
+  return (size_t)batch * (size_t)plan_conv_bwd(batch, L, D, io).nchunks * (size_t)(W + 1) * (size_t)D * sizeof(float);
 }
 
 hipError_t launch_conv_bwd(const ConvBwdArgs& a, int io, void* workspace, hipStream_t s) {
   const ConvArgs& f = a.f;
-  const ConvPlan p = plan_conv_bwd(f.batch, f.L, f.D);
+  const ConvPlan p = plan_conv_bwd(f.batch, f.L, f.D, io);
   float* part = static_cast<float*>(workspace);
   if (f.batch > 0) {
-    const unsigned grid = blocks(f.batch, p.nchunks, f.D);
+    const unsigned grid = blocks(f.batch, p.nchunks, f.D, group_bwd(io));
     const hipError_t e = by_type_and_width(
-        io, f.W, [&](auto t, auto w) { bwd_w<decltype(t), decltype(w)::value>(a, p, grid, part, s); });
+        io, f.W, [&](auto t, auto w) {
+          if (f.silu) bwd_w<decltype(t), decltype(w)::value, true>(a, p, grid, part, s);
+          else bwd_w<decltype(t), decltype(w)::value, false>(a, p, grid, part, s);
+        });
     if (e != hipSuccess) return e;
   }
   const int64_t cols = (f.W + 1) * f.D;
@@ -449,10 +606,10 @@ hipError_t launch_conv_bwd(const ConvBwdArgs& a, int io, void* workspace, hipStr
 }
 
 hipError_t launch_conv_step(const ConvStepArgs& a, int io, hipStream_t s) {
-  const unsigned grid = blocks(a.batch, 1, a.D);
+  const unsigned grid = blocks(a.batch, 1, a.D, group_step(io));
   return by_type_and_width(io, a.W, [&](auto t, auto w) {
     using T = decltype(t);
-    hipLaunchKernelGGL((conv_step_kernel<T, decltype(w)::value>), dim3(grid), dim3(kBlock), 0, s, a);
+    hipLaunchKernelGGL((conv_step_kernel<T, kGroupStep<T>, decltype(w)::value>), dim3(grid), dim3(kBlock), 0, s, a);
   });
 }
 

@@ -70,12 +70,12 @@ __device__ __forceinline__ raw_t<T, V> narrow(const float (&f)[V]) {
   return v;
 }
 
-// sigma(v) = 1 / (1 + e^-v), and SiLU'(v) = sigma (1 + v (1 - sigma)).  Where sigma underflows to 0
-// (v below -88) the slope is 0: its product with an infinite v would be no number.
+// sigma(v) = 1 / (1 + e^-v), and SiLU'(v) = sigma (1 + v (1 - sigma)).  Like SiLU itself, the slope at
+// -infinity is no number.
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-v * kLog2e)); }
 __device__ __forceinline__ float silu_slope(float v) {
   const float s = sigmoid(v);
-  return s == 0.0f ? 0.0f : s * __builtin_fmaf(v, 1.0f - s, 1.0f);
+  return s * __builtin_fmaf(v, 1.0f - s, 1.0f);
 }
 
 // Sums of the columns of part (rows, cols), a column per threadIdx.x % 32 of a 1024-thread block: 32

@@ -92,34 +92,54 @@ __device__ __forceinline__ int64_t place_of(const SsmStepArgs& a, int64_t b) {
   return s < a.nslots ? s : -1;
 }
 
-// x_c of four channels of one row, which also moves the window on.
+// x_c of four channels of kItems rows, kBlock threads apart, which also moves the windows on.  All loads are
+// issued before the first of them is needed.
+constexpr int kItems = kRows * kSlice / 4 / kBlock;
+
 template <typename IO, int W, bool FULL>
-__device__ __forceinline__ void conv_four(const SsmStepArgs& a, int64_t b, int64_t slot, int64_t d0, int nv,
-                                          float (&c)[4]) {
-  IO* win = static_cast<IO*>(a.window) + slot * (W - 1) * a.D + d0;
-  raw_t<IO, 4> row[W];
+__device__ __forceinline__ void conv_four(const SsmStepArgs& a, int64_t b0, int r0, int64_t d0, int nv, float* xc,
+                                          float (&c)[kItems][4]) {
+  constexpr int kApart = kBlock / (kSlice / 4);  // rows between two items of a thread
+  int64_t slot[kItems];
+  raw_t<IO, 4> row[kItems][W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) row[j] = load_raw<IO, 4, FULL>(win + j * a.D, nv);
-  row[W - 1] = load_raw<IO, 4, FULL>(static_cast<const IO*>(a.x) + b * a.D + d0, nv);
-  float w[4 * W], bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < kItems; ++i) slot[i] = place_of(a, b0 + r0 + i * kApart);
 #pragma unroll
-  for (int i = 0; i < 4 * W; ++i) w[i] = FULL || i < nv * W ? a.conv_weight[d0 * W + i] : 0.0f;
-  if (a.conv_bias)
+  for (int i = 0; i < kItems; ++i) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bias[i] = FULL || i < nv ? a.conv_bias[d0 + i] : 0.0f;
+    for (int j = 0; j < W; ++j) row[i][j] = raw_t<IO, 4>(0u);
+    if (slot[i] < 0) continue;
+    row[i][W - 1] = load_raw<IO, 4, FULL>(static_cast<const IO*>(a.x) + (b0 + r0 + i * kApart) * a.D + d0, nv);
+    const IO* win = static_cast<const IO*>(a.window) + slot[i] * (W - 1) * a.D + d0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = bias[i];
-#pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float v[4];
-    widen<IO, 4>(row[j], v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(w[i * W + j], v[i], c[i]);
+    for (int j = 0; j < W - 1; ++j) row[i][j] = load_raw<IO, 4, FULL>(win + j * a.D, nv);
   }
+  float w[W][4], bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // the 4 W weights side by side
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = FULL || i < nv ? silu(c[i]) : 0.0f;
+  for (int k = 0; k < W; ++k)
+    widen<float, 4>(load_raw<float, 4, FULL>(a.conv_weight + d0 * W + 4 * k, nv * W - 4 * k), w[k]);
+  if (a.conv_bias) widen<float, 4>(load_raw<float, 4, FULL>(a.conv_bias + d0, nv), bias);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_raw<IO, 4, FULL>(win + j * a.D, row[j + 1], nv);
+  for (int i = 0; i < kItems; ++i) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[i][k] = 0.0f;
+    if (slot[i] < 0) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[i][k] = bias[k];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      float v[4];
+      widen<IO, 4>(row[i][j], v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[i][k] = __builtin_fmaf(w[(k * W + j) / 4][(k * W + j) % 4], v[k], c[i][k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[i][k] = FULL || k < nv ? silu(c[i][k]) : 0.0f;
+    IO* win = static_cast<IO*>(a.window) + slot[i] * (W - 1) * a.D + d0;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) store_raw<IO, 4, FULL>(win + j * a.D, row[i][j + 1], nv);
+    store_raw<float, 4, FULL>(xc + (b0 + r0 + i * kApart) * a.D + d0, narrow<float, 4>(c[i]), nv);
+  }
 }
 
 // xc: (batch, D) fp32.  part: (slices, batch, F) fp32, F = R + 2 N.
@@ -149,22 +169,15 @@ __global__ __launch_bounds__(kBlock) void ssm_front_kernel(SsmStepArgs a, int ti
     }
   };
   load_b(w);  // in flight during the convolution
+  {
+    const int r = threadIdx.x / (kSlice / 4), g = threadIdx.x % (kSlice / 4) * 4;
+    const int64_t d = d0 + g;
+    float c[kItems][4] = {};
+    if (d + 4 <= a.D) conv_four<IO, W, true>(a, b0, r, d, 4, xc, c);
+    else if (d < a.D) conv_four<IO, W, false>(a, b0, r, d, (int)(a.D - d), xc, c);
 #pragma unroll
-  for (int i = 0; i < kRows * kSlice / 4 / kBlock; ++i) {
-    const int e = i * kBlock + threadIdx.x, r = e / (kSlice / 4), g = e % (kSlice / 4) * 4;
-    const int64_t b = b0 + r, d = d0 + g, slot = place_of(a, b);
-    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (slot >= 0 && d < a.D) {
-      const int nv = a.D - d < 4 ? (int)(a.D - d) : 4;
-      if (nv == 4) {
-        conv_four<IO, W, true>(a, b, slot, d, 4, c);
-        store_raw<float, 4, true>(xc + b * a.D + d, narrow<float, 4>(c), 4);
-      } else {
-        conv_four<IO, W, false>(a, b, slot, d, nv, c);
-        store_raw<float, 4, false>(xc + b * a.D + d, narrow<float, 4>(c), nv);
-      }
-    }
-    *reinterpret_cast<float4*>(&xs[r][g]) = make_float4(c[0], c[1], c[2], c[3]);
+    for (int i = 0; i < kItems; ++i)
+      *reinterpret_cast<float4*>(&xs[r + i * (kBlock / (kSlice / 4))][g]) = make_float4(c[i][0], c[i][1], c[i][2], c[i][3]);
   }
   __syncthreads();
   OperandA<IO> op[KS];
@@ -191,122 +204,181 @@ __global__ __launch_bounds__(kBlock) void ssm_front_kernel(SsmStepArgs a, int ti
   }
 }
 
+// Sum over the slices of one value, in their order, 16 loads in flight.
+__device__ __forceinline__ float slice_sum(const float* p, int64_t stride, int slices) {
+  float v = 0.0f;
+  int s = 0;
+  for (; s + 16 <= slices; s += 16) {
+    float q[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) q[i] = p[(s + i) * stride];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += q[i];
+  }
+  for (; s + 4 <= slices; s += 4) {
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = p[(s + i) * stride];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v += q[i];
+  }
+  for (; s < slices; ++s) v += p[s * stride];
+  return v;
+}
+
 // out: (batch, F), the slices' parts added in their order.
 __global__ __launch_bounds__(kBlock) void ssm_join_kernel(const float* part, int64_t count, int slices, float* out) {
   const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-  if (i >= count) return;
-  float v = 0.0f;
-#pragma unroll 8
-  for (int s = 0; s < slices; ++s) v += part[s * count + i];
-  out[i] = v;
+  if (i < count) out[i] = slice_sum(part + i, count, slices);
 }
+
+constexpr int kChannels = 64;  // channels of a back workgroup
 
 template <int N>
 struct Lanes {
-  static constexpr int kStates = N < 4 ? N : 4;       // states per lane
-  static constexpr int kPer = N / kStates;            // lanes per channel
-  static constexpr int kChannels = kBlock / kPer;     // channels per workgroup
+  static constexpr int kStates = N < 4 ? N : 4;                    // states per lane
+  static constexpr int kPer = N / kStates;                         // lanes per channel
+  static constexpr int kGroups = kBlock / (kChannels * kPer);      // row groups: a lane has every kGroups-th row
+  static constexpr int kRowsPer = kRows / kGroups;                 // rows per lane
 };
 
 // sel: (slices, batch, F) part sums of r, B, C.
 template <typename IO, int N>
-__global__ __launch_bounds__(kBlock) void ssm_back_kernel(SsmStepArgs a, int tiles, int ldx, const float* xc,
+__global__ __launch_bounds__(kBlock, 3) void ssm_back_kernel(SsmStepArgs a, int tiles, int ldx, const float* xc,
                                                           const float* sel, int slices) {
-  constexpr int NS = Lanes<N>::kStates, LPC = Lanes<N>::kPer, CB = Lanes<N>::kChannels;
-  constexpr int CT = CB / 16 / 4;  // channel tiles of 16 per wave
+  constexpr int NS = Lanes<N>::kStates, LPC = Lanes<N>::kPer, RG = Lanes<N>::kGroups, RP = Lanes<N>::kRowsPer;
+  constexpr int CB = kChannels, LD = CB + kPad;
+  constexpr int PRE = 6;  // matrix steps whose weights are loaded ahead
+  __shared__ int place[kRows];
   extern __shared__ __attribute__((aligned(16))) float lds[];
-  float* xd = lds;                        // (kRows, ldx): r, B, C of the rows
-  float* dl = lds + kRows * ldx;          // (kRows, CB + kPad): r W_dt^T
+  float* xd = lds;               // (kRows, ldx): r, B, C of the rows
+  float* dl = xd + kRows * ldx;  // (kRows, LD): r W_dt^T
+  float* xl = dl + kRows * LD;   // (kRows, LD): x_c
+  float* zl = xl + kRows * LD;   // (kRows, LD): z, then out
   const int tile = blockIdx.x % (uint32_t)tiles;
   const int64_t d0 = (int64_t)(blockIdx.x / (uint32_t)tiles) * CB, b0 = (int64_t)tile * kRows;
   const int nrows = a.batch - b0 < kRows ? (int)(a.batch - b0) : kRows;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q = lane >> 4;
   const int64_t F = a.R + 2 * N;
-  // this lane's channel and states
-  const int cl = threadIdx.x / LPC, n0 = threadIdx.x % LPC * NS;
+  const int64_t RK = (a.R + kStep<IO> - 1) / kStep<IO> * kStep<IO>;
+  // this lane's channel, states and first row
+  const int cl = threadIdx.x / LPC % CB, n0 = threadIdx.x % LPC * NS, rg = threadIdx.x / (LPC * CB);
   const int64_t d = d0 + cl;
   const bool in = d < a.D;
-  float h[kRows][NS];
-  int64_t at[kRows];
+  if (threadIdx.x < kRows) place[threadIdx.x] = (int)place_of(a, b0 + threadIdx.x);
+  // weights of r, ahead of everything that waits; wave w multiplies channels 16 w .. 16 w + 15
+  const int64_t cw = d0 + w * 16 + r16;
+  const IO* wdt = static_cast<const IO*>(a.Wdt) + (cw < a.D ? cw : 0) * a.R;
+  raw_t<IO, kShare<IO>> pre[PRE];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int64_t slot = r < nrows ? place_of(a, b0 + r) : -1;
-    at[r] = in && slot >= 0 ? (slot * a.D + d) * N + n0 : -1;
+  for (int p = 0; p < PRE; ++p) pre[p] = operand_b<IO>(wdt, p * kStep<IO> + q * kShare<IO>, a.R, cw < a.D);
+  // the states: needed last, so they travel while the rest is formed
+  float h[RP][NS];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) h[r][n] = 0.0f;
-    if (at[r] >= 0) {
+  for (int i = 0; i < RP; ++i) {
+    const int64_t slot = place_of(a, b0 + i * RG + rg);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[i][n] = 0.0f;
+    if (in && slot >= 0) {
+      const float* st = a.state + (slot * a.D + d) * N + n0;
       if constexpr (NS == 4) {
-        const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a.state + at[r]));
+        const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(st));
 #pragma unroll
-        for (int n = 0; n < 4; ++n) h[r][n] = v[n];
+        for (int n = 0; n < 4; ++n) h[i][n] = v[n];
       } else {
 #pragma unroll
-        for (int n = 0; n < NS; ++n) h[r][n] = a.state[at[r] + n];
+        for (int n = 0; n < NS; ++n) h[i][n] = st[n];
       }
     }
   }
-  // r, B, C of the tile's rows; what lies behind r in a matrix step is zero
-  const int64_t RK = (a.R + kStep<IO> - 1) / kStep<IO> * kStep<IO>;
-  float* xr = xd;                  // r at 0 .. RK, B and C behind
-  for (int e = threadIdx.x; e < kRows * ldx; e += kBlock) {
+  // r, B, C of the tile's rows (r at 0 .. RK, zero behind R; B and C behind that), x_c and z
+  for (int e = threadIdx.x; e < nrows * ldx; e += kBlock) {
     const int r = e / ldx, c = e % ldx;
     const int64_t f = c < RK ? c : a.R + (c - RK);
     float v = 0.0f;
-    if (r < nrows && (c < a.R || (c >= RK && f < F)))
-      for (int s = 0; s < slices; ++s) v += sel[((int64_t)s * a.batch + b0 + r) * F + f];
-    xr[e] = v;
+    if (c < a.R || (c >= RK && f < F)) v = slice_sum(sel + (b0 + r) * F + f, a.batch * F, slices);
+    xd[e] = v;
+  }
+  for (int e = nrows * ldx + threadIdx.x; e < kRows * ldx; e += kBlock) xd[e] = 0.0f;
+  for (int e = threadIdx.x; e < nrows * (CB / 4); e += kBlock) {
+    const int r = e / (CB / 4), g = e % (CB / 4) * 4;
+    const int64_t dg = d0 + g, i = (b0 + r) * a.D + dg;
+    const int nv = a.D - dg < 4 ? (int)(a.D - dg) : 4;
+    raw_t<float, 4> xv(0u);
+    raw_t<IO, 4> zv(0u);
+    if (nv == 4) {
+      xv = load_raw<float, 4, true>(xc + i, 4);
+      if (a.z) zv = load_raw<IO, 4, true>(static_cast<const IO*>(a.z) + i, 4);
+    } else {
+      xv = load_raw<float, 4, false>(xc + i, nv);
+      if (a.z) zv = load_raw<IO, 4, false>(static_cast<const IO*>(a.z) + i, nv);
+    }
+    float z4[4];
+    widen<IO, 4>(zv, z4);
+    *reinterpret_cast<raw_t<float, 4>*>(xl + r * LD + g) = xv;
+    *reinterpret_cast<float4*>(zl + r * LD + g) = make_float4(z4[0], z4[1], z4[2], z4[3]);
   }
   __syncthreads();
-  const IO* wdt = static_cast<const IO*>(a.Wdt);
-  f32x4 acc[CT];
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int t = 0; t < CT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t k = 0; k < RK; k += kStep<IO>) {
+  for (int p = 0; p < PRE; ++p) {
+    if (p * kStep<IO> >= RK) break;
+    OperandA<IO> op;
+    op.set(xd + r16 * ldx + p * kStep<IO> + q * kShare<IO>);
+    acc = op.times(pre[p], acc);
+  }
+  for (int64_t k = PRE * kStep<IO>; k < RK; k += kStep<IO>) {
     OperandA<IO> op;
     op.set(xd + r16 * ldx + k + q * kShare<IO>);
-#pragma unroll
-    for (int t = 0; t < CT; ++t) {
-      const int64_t c = d0 + (w * CT + t) * 16 + r16;
-      acc[t] = op.times(operand_b<IO>(wdt + (c < a.D ? c : 0) * a.R, k + q * kShare<IO>, a.R, c < a.D), acc[t]);
-    }
+    acc = op.times(operand_b<IO>(wdt, k + q * kShare<IO>, a.R, cw < a.D), acc);
   }
 #pragma unroll
-  for (int t = 0; t < CT; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dl[(4 * q + i) * (CB + kPad) + (w * CT + t) * 16 + r16] = acc[t][i];
+  for (int i = 0; i < 4; ++i) dl[(4 * q + i) * LD + w * 16 + r16] = acc[i];
   __syncthreads();
-  if (!in) return;
-  ChanConst<NS> cc;
+  if (in) {
+    ChanConst<NS> cc;
 #pragma unroll
-  for (int n = 0; n < NS; ++n) cc.set(n, a.A[d * N + n0 + n]);
-  const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f, dskip = a.dskip ? a.dskip[d] : 0.0f;
+    for (int n = 0; n < NS; ++n) cc.set(n, a.A[d * N + n0 + n]);
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f, dskip = a.dskip ? a.dskip[d] : 0.0f;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (at[r] < 0) continue;  // the channel's lanes agree
-    const int64_t i = (b0 + r) * a.D + d;
-    const float* sel_r = xd + r * ldx + RK;
-    float Bt[NS], Ct[NS];
+    for (int i = 0; i < RP; ++i) {
+      const int r = i * RG + rg;
+      const int64_t slot = place[r];
+      if (slot < 0) continue;  // the channel's lanes agree
+      const float* sel_r = xd + r * ldx + RK;
+      float Bt[NS], Ct[NS];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      Bt[n] = sel_r[n0 + n];
-      Ct[n] = sel_r[N + n0 + n];
+      for (int n = 0; n < NS; ++n) {
+        Bt[n] = sel_r[n0 + n];
+        Ct[n] = sel_r[N + n0 + n];
+      }
+      const float x = xl[r * LD + cl];
+      const TokenFront f = make_front(dl[r * LD + cl], bias, true);
+      float y = token_step<NS>(cc, f, x, Bt, Ct, h[i]);
+      if constexpr (LPC >= 2) y += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(y), 0xB1, 0xf, 0xf, false));
+      if constexpr (LPC == 4) y += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(y), 0x4E, 0xf, 0xf, false));
+      float* st = a.state + (slot * a.D + d) * N + n0;
+      if constexpr (NS == 4) {
+        const f32x4 v = {h[i][0], h[i][1], h[i][2], h[i][3]};
+        __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(st));
+      } else {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) st[n] = h[i][n];
+      }
+      if (n0 == 0) zl[r * LD + cl] = epilogue(y, x, dskip, a.z != nullptr, zl[r * LD + cl]);
     }
-    const float x = xc[i];
-    const TokenFront f = make_front(dl[r * (CB + kPad) + cl], bias, true);
-    float y = token_step<NS>(cc, f, x, Bt, Ct, h[r]);
-    if constexpr (LPC >= 2) y += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(y), 0xB1, 0xf, 0xf, false));
-    if constexpr (LPC == 4) y += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(y), 0x4E, 0xf, 0xf, false));
-    if constexpr (NS == 4) {
-      const f32x4 v = {h[r][0], h[r][1], h[r][2], h[r][3]};
-      __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(a.state + at[r]));
-    } else {
-#pragma unroll
-      for (int n = 0; n < NS; ++n) a.state[at[r] + n] = h[r][n];
-    }
-    if (n0 == 0)
-      store_io(static_cast<IO*>(a.out), i,
-               epilogue(y, x, dskip, a.z != nullptr, a.z ? load_io(static_cast<const IO*>(a.z), i) : 0.0f));
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < nrows * (CB / 4); e += kBlock) {
+    const int r = e / (CB / 4), g = e % (CB / 4) * 4;
+    const int64_t dg = d0 + g;
+    if (dg >= a.D || place[r] < 0) continue;
+    const float4 v = *reinterpret_cast<const float4*>(zl + r * LD + g);
+    const float o[4] = {v.x, v.y, v.z, v.w};
+    IO* out = static_cast<IO*>(a.out) + (b0 + r) * a.D + dg;
+    if (a.D - dg >= 4) store_raw<IO, 4, true>(out, narrow<IO, 4>(o), 4);
+    else store_raw<IO, 4, false>(out, narrow<IO, 4>(o), (int)(a.D - dg));
   }
 }
 
@@ -335,8 +407,8 @@ StepPlan plan_step(int64_t batch, int64_t D, int64_t N, int64_t R, int io) {
 template <typename IO, int N>
 hipError_t back(const SsmStepArgs& a, const StepPlan& p, const float* xc, const float* sel, int slices,
                 hipStream_t s) {
-  constexpr int CB = Lanes<N>::kChannels;
-  const size_t lds = (size_t)kRows * (p.ldx + CB + kPad) * sizeof(float);
+  constexpr int CB = kChannels;
+  const size_t lds = (size_t)kRows * (p.ldx + 3 * (CB + kPad)) * sizeof(float);
   hipLaunchKernelGGL((ssm_back_kernel<IO, N>), dim3((unsigned)(p.tiles * ((a.D + CB - 1) / CB))), dim3(kBlock), lds, s,
                      a, p.tiles, p.ldx, xc, sel, slices);
   return hipGetLastError();
