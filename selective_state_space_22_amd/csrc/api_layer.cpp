@@ -190,7 +190,7 @@ int mamba_conv_update(int64_t batch, int64_t dim, int64_t width, int io_dtype, i
 
 size_t mamba_conv_ssm_update_workspace_size(int64_t batch, int64_t dim, int64_t dstate, int64_t dt_rank, int io_dtype) {
   if (check_ssm("mamba_conv_ssm_update_workspace_size", batch, dim, dstate, dt_rank, io_dtype) != MAMBA_OK) return 0;
-  return s6::ssm_step_ws_bytes(batch, dim, dstate, dt_rank, io_dtype);
+  return s6::ssm_step_ws_bytes(batch, dim, dstate, dt_rank);
 }
 
 int mamba_conv_ssm_update(int64_t batch, int64_t dim, int64_t dstate, int64_t dt_rank, int64_t width, int io_dtype,
@@ -222,7 +222,7 @@ int mamba_conv_ssm_update(int64_t batch, int64_t dim, int64_t dstate, int64_t dt
   pc.opt(workspace, "workspace");
   if (pc.status != MAMBA_OK) return pc.status;
   if (!any) return MAMBA_OK;
-  const size_t need = s6::ssm_step_ws_bytes(batch, dim, dstate, dt_rank, io_dtype);
+  const size_t need = s6::ssm_step_ws_bytes(batch, dim, dstate, dt_rank);
   if (!workspace || workspace_bytes < need) return fail(MAMBA_ERR_WORKSPACE, where, "workspace");
   const s6::SsmStepArgs a{state, window, x,     conv_weight, conv_bias, W_x, W_dt,   dt_bias, A,
                           Dskip, z,      slots, out,         batch,     dim, dstate, dt_rank, nslots,

@@ -72,7 +72,7 @@ struct SsmStepArgs {
   int32_t W;
 };
 
-size_t ssm_step_ws_bytes(int64_t batch, int64_t D, int64_t N, int64_t R, int io);
+size_t ssm_step_ws_bytes(int64_t batch, int64_t D, int64_t N, int64_t R);
 hipError_t launch_ssm_step(const SsmStepArgs& a, int io, void* workspace, hipStream_t stream);
 
 // ---------------------------------------------------------------- norms around a block (norm.hip)

@@ -30,7 +30,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kRows = 16;     // batch rows of a tile: the matrix instruction's rows
 constexpr int kSlice = 128;   // channels of a front workgroup
 constexpr int kBlock = 256;
-constexpr int kPad = 4;       // floats behind an LDS row: lanes of a quarter wave on distinct banks
+constexpr int kPad = 4;       // floats behind an LDS row
 
 // K elements of one matrix step, and of each lane's share (lane l: row l % 16, share l / 16 of the step).
 template <typename IO>
@@ -38,42 +38,62 @@ constexpr int kStep = sizeof(IO) == 2 ? 32 : 16;
 template <typename IO>
 constexpr int kShare = kStep<IO> / 4;
 
-// The A operand of one step, from fp32 values: bf16 as three parts, fp32 as it is.
+// The A operands of a tile's rows in LDS, split once for all waves: bf16 as three parts, fp32 as it is.  K
+// elements to a row, and 16 bytes more: the 16 rows that a quarter wave reads lie on distinct banks.
 template <typename IO>
-struct OperandA;
+struct Operands;
 template <>
-struct OperandA<uint16_t> {
-  bf16x8 part[3];
-  __device__ __forceinline__ void set(const float* v) {
+struct Operands<uint16_t> {
+  static __host__ __device__ constexpr size_t bytes(int64_t rows, int64_t K) { return 3 * rows * (K + 8) * 2; }
+  // Three bf16 values whose sum is f to 24 bits.
+  static __device__ __forceinline__ void put(uint8_t* base, int rows, int K, int r, int k, float f) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(base) + r * (K + 8) + k;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float f = v[i];
-#pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        const __bf16 h = (__bf16)f;
-        part[p][i] = h;
-        f -= (float)h;  // exact: the rounding error of h
-      }
+    for (int i = 0; i < 3; ++i) {
+      const uint16_t h = f32_to_bf16(f);
+      p[i * rows * (K + 8)] = h;
+      f -= bf16_to_f32(h);  // exact: the rounding error of h
     }
   }
-  __device__ __forceinline__ f32x4 times(raw_t<uint16_t, 8> b, f32x4 c) const {
+  static __device__ __forceinline__ void put4(uint8_t* base, int rows, int K, int r, int k, const float (&v)[4]) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(base) + r * (K + 8) + k;
+    float f[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const raw_t<uint16_t, 4> h = narrow<uint16_t, 4>(f);
+      *reinterpret_cast<raw_t<uint16_t, 4>*>(p + i * rows * (K + 8)) = h;
+      float back[4];
+      widen<uint16_t, 4>(h, back);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] -= back[e];
+    }
+  }
+  // c + (row's elements k0 + 8 q .. + 7 and those of the other shares) times b
+  static __device__ __forceinline__ f32x4 times(const uint8_t* base, int rows, int K, int r, int k, raw_t<uint16_t, 8> b,
+                                                f32x4 c) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + r * (K + 8) + k;
     const bf16x8 bb = __builtin_bit_cast(bf16x8, b);
 #pragma unroll
-    for (int p = 2; p >= 0; --p) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[p], bb, c, 0, 0, 0);
+    for (int i = 2; i >= 0; --i)
+      c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8*>(p + i * rows * (K + 8)), bb, c, 0, 0, 0);
     return c;
   }
 };
 template <>
-struct OperandA<float> {
-  float f[4];
-  __device__ __forceinline__ void set(const float* v) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = v[i];
+struct Operands<float> {
+  static __host__ __device__ constexpr size_t bytes(int64_t rows, int64_t K) { return rows * (K + 4) * 4; }
+  static __device__ __forceinline__ void put(uint8_t* base, int, int K, int r, int k, float f) {
+    reinterpret_cast<float*>(base)[r * (K + 4) + k] = f;
   }
-  __device__ __forceinline__ f32x4 times(raw_t<float, 4> b, f32x4 c) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(f[i], __uint_as_float(b[i]), c, 0, 0, 0);
-    return c;
+  static __device__ __forceinline__ void put4(uint8_t* base, int, int K, int r, int k, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + r * (K + 4) + k) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  static __device__ __forceinline__ f32x4 times(const uint8_t* base, int, int K, int r, int k, raw_t<float, 4> b, f32x4 c) {
+    const float4 f = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + r * (K + 4) + k);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(f.x, __uint_as_float(b[0]), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(f.y, __uint_as_float(b[1]), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(f.z, __uint_as_float(b[2]), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(f.w, __uint_as_float(b[3]), c, 0, 0, 0);
   }
 };
 
@@ -148,7 +168,7 @@ __global__ __launch_bounds__(kBlock) void ssm_front_kernel(SsmStepArgs a, int ti
                                                            float* part) {
   constexpr int KS = kSlice / kStep<IO>;
   constexpr int TW = 3;  // column tiles of 16 that a wave multiplies together
-  __shared__ __attribute__((aligned(16))) float xs[kRows][kSlice + kPad];
+  __shared__ __attribute__((aligned(16))) uint8_t xs[Operands<IO>::bytes(kRows, kSlice)];
   // the tiles of a slice read the same rows of W_x: ids congruent mod 8 (one XCD), 8 apart
   const int id = blockIdx.x, round = id / (8 * tiles), rem = id % (8 * tiles);
   const int slice = round * 8 + rem % 8, tile = rem / 8;
@@ -176,20 +196,16 @@ __global__ __launch_bounds__(kBlock) void ssm_front_kernel(SsmStepArgs a, int ti
     if (d + 4 <= a.D) conv_four<IO, W, true>(a, b0, r, d, 4, xc, c);
     else if (d < a.D) conv_four<IO, W, false>(a, b0, r, d, (int)(a.D - d), xc, c);
 #pragma unroll
-    for (int i = 0; i < kItems; ++i)
-      *reinterpret_cast<float4*>(&xs[r + i * (kBlock / (kSlice / 4))][g]) = make_float4(c[i][0], c[i][1], c[i][2], c[i][3]);
+    for (int i = 0; i < kItems; ++i) Operands<IO>::put4(xs, kRows, kSlice, r + i * (kBlock / (kSlice / 4)), g, c[i]);
   }
   __syncthreads();
-  OperandA<IO> op[KS];
-#pragma unroll
-  for (int k = 0; k < KS; ++k) op[k].set(&xs[r16][k * kStep<IO> + q * kShare<IO>]);
   for (int t0 = w; t0 < ntiles; t0 += 4 * TW) {
     f32x4 acc[TW];
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
       acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int k = 0; k < KS; ++k) acc[t] = op[k].times(wb[t][k], acc[t]);
+      for (int k = 0; k < KS; ++k) acc[t] = Operands<IO>::times(xs, kRows, kSlice, r16, k * kStep<IO> + q * kShare<IO>, wb[t][k], acc[t]);
     }
     if (t0 + 4 * TW < ntiles) load_b(t0 + 4 * TW);
 #pragma unroll
@@ -204,23 +220,17 @@ __global__ __launch_bounds__(kBlock) void ssm_front_kernel(SsmStepArgs a, int ti
   }
 }
 
-// Sum over the slices of one value, in their order, 16 loads in flight.
+// Sum over the slices of one value, in their order, U loads in flight.
+template <int U>
 __device__ __forceinline__ float slice_sum(const float* p, int64_t stride, int slices) {
   float v = 0.0f;
   int s = 0;
-  for (; s + 16 <= slices; s += 16) {
-    float q[16];
+  for (; s + U <= slices; s += U) {
+    float q[U];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = p[(s + i) * stride];
+    for (int i = 0; i < U; ++i) q[i] = p[(s + i) * stride];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += q[i];
-  }
-  for (; s + 4 <= slices; s += 4) {
-    float q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = p[(s + i) * stride];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v += q[i];
+    for (int i = 0; i < U; ++i) v += q[i];
   }
   for (; s < slices; ++s) v += p[s * stride];
   return v;
@@ -229,44 +239,48 @@ __device__ __forceinline__ float slice_sum(const float* p, int64_t stride, int s
 // out: (batch, F), the slices' parts added in their order.
 __global__ __launch_bounds__(kBlock) void ssm_join_kernel(const float* part, int64_t count, int slices, float* out) {
   const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-  if (i < count) out[i] = slice_sum(part + i, count, slices);
+  if (i < count) out[i] = slice_sum<8>(part + i, count, slices);
 }
 
-constexpr int kChannels = 64;  // channels of a back workgroup
+constexpr int kChannels = 128;        // channels of a back workgroup
+constexpr int kBack = 4 * kChannels;  // its threads: four lanes per channel at N = 16
+constexpr int kFewRows = 4;           // up to these, the back adds the slices itself
+constexpr int kBackRows = 8;          // batch rows of its tile otherwise (at most the matrix instruction's 16)
 
-template <int N>
+template <int N, int ROWS>
 struct Lanes {
   static constexpr int kStates = N < 4 ? N : 4;                    // states per lane
   static constexpr int kPer = N / kStates;                         // lanes per channel
-  static constexpr int kGroups = kBlock / (kChannels * kPer);      // row groups: a lane has every kGroups-th row
-  static constexpr int kRowsPer = kRows / kGroups;                 // rows per lane
+  static constexpr int kGroups = kBack / (kChannels * kPer);      // row groups: a lane has every kGroups-th row
+  static constexpr int kRowsPer = (ROWS + kGroups - 1) / kGroups;  // rows per lane
 };
 
-// sel: (slices, batch, F) part sums of r, B, C.
-template <typename IO, int N>
-__global__ __launch_bounds__(kBlock, 3) void ssm_back_kernel(SsmStepArgs a, int tiles, int ldx, const float* xc,
-                                                          const float* sel, int slices) {
-  constexpr int NS = Lanes<N>::kStates, LPC = Lanes<N>::kPer, RG = Lanes<N>::kGroups, RP = Lanes<N>::kRowsPer;
+// sel: (slices, batch, F) part sums of r, B, C; ROWS = kBackRows: joined, one slice.
+template <typename IO, int N, int ROWS>
+__global__ __launch_bounds__(kBack) void ssm_back_kernel(SsmStepArgs a, int tiles, const float* xc, const float* sel,
+                                                             int slices) {
+  constexpr int NS = Lanes<N, ROWS>::kStates, LPC = Lanes<N, ROWS>::kPer, RG = Lanes<N, ROWS>::kGroups, RP = Lanes<N, ROWS>::kRowsPer;
   constexpr int CB = kChannels, LD = CB + kPad;
   constexpr int PRE = 6;  // matrix steps whose weights are loaded ahead
-  __shared__ int place[kRows];
-  extern __shared__ __attribute__((aligned(16))) float lds[];
-  float* xd = lds;               // (kRows, ldx): r, B, C of the rows
-  float* dl = xd + kRows * ldx;  // (kRows, LD): r W_dt^T
-  float* xl = dl + kRows * LD;   // (kRows, LD): x_c
-  float* zl = xl + kRows * LD;   // (kRows, LD): z, then out
+  __shared__ int place[ROWS];
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int RK = (int)((a.R + kStep<IO> - 1) / kStep<IO> * kStep<IO>);
+  uint8_t* rd = lds;                                                                    // r of the rows, as operands
+  float* bc = reinterpret_cast<float*>(lds + Operands<IO>::bytes(ROWS, RK));  // (ROWS, 2 N): B, C
+  float* dl = bc + ROWS * 2 * N;                                                   // (ROWS, LD): dt
+  float* xl = dl + ROWS * LD;                                                      // (ROWS, LD): x_c
+  float* yl = xl + ROWS * LD;                                                      // (ROWS, LD): C . h
   const int tile = blockIdx.x % (uint32_t)tiles;
-  const int64_t d0 = (int64_t)(blockIdx.x / (uint32_t)tiles) * CB, b0 = (int64_t)tile * kRows;
-  const int nrows = a.batch - b0 < kRows ? (int)(a.batch - b0) : kRows;
+  const int64_t d0 = (int64_t)(blockIdx.x / (uint32_t)tiles) * CB, b0 = (int64_t)tile * ROWS;
+  const int nrows = a.batch - b0 < ROWS ? (int)(a.batch - b0) : ROWS;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q = lane >> 4;
   const int64_t F = a.R + 2 * N;
-  const int64_t RK = (a.R + kStep<IO> - 1) / kStep<IO> * kStep<IO>;
   // this lane's channel, states and first row
   const int cl = threadIdx.x / LPC % CB, n0 = threadIdx.x % LPC * NS, rg = threadIdx.x / (LPC * CB);
   const int64_t d = d0 + cl;
   const bool in = d < a.D;
-  if (threadIdx.x < kRows) place[threadIdx.x] = (int)place_of(a, b0 + threadIdx.x);
+  if (threadIdx.x < ROWS) place[threadIdx.x] = (int)place_of(a, b0 + threadIdx.x);
   // weights of r, ahead of everything that waits; wave w multiplies channels 16 w .. 16 w + 15
   const int64_t cw = d0 + w * 16 + r16;
   const IO* wdt = static_cast<const IO*>(a.Wdt) + (cw < a.D ? cw : 0) * a.R;
@@ -277,7 +291,7 @@ __global__ __launch_bounds__(kBlock, 3) void ssm_back_kernel(SsmStepArgs a, int 
   float h[RP][NS];
 #pragma unroll
   for (int i = 0; i < RP; ++i) {
-    const int64_t slot = place_of(a, b0 + i * RG + rg);
+    const int64_t slot = i * RG + rg < ROWS ? place_of(a, b0 + i * RG + rg) : -1;
 #pragma unroll
     for (int n = 0; n < NS; ++n) h[i][n] = 0.0f;
     if (in && slot >= 0) {
@@ -292,70 +306,71 @@ __global__ __launch_bounds__(kBlock, 3) void ssm_back_kernel(SsmStepArgs a, int 
       }
     }
   }
-  // r, B, C of the tile's rows (r at 0 .. RK, zero behind R; B and C behind that), x_c and z
-  for (int e = threadIdx.x; e < nrows * ldx; e += kBlock) {
-    const int r = e / ldx, c = e % ldx;
-    const int64_t f = c < RK ? c : a.R + (c - RK);
-    float v = 0.0f;
-    if (c < a.R || (c >= RK && f < F)) v = slice_sum(sel + (b0 + r) * F + f, a.batch * F, slices);
-    xd[e] = v;
+  // r (zero behind R), B and C of the tile's rows: a wave per row, more where there are fewer rows
+  {
+    const int per = nrows == 1 ? kBack : (nrows == 2 ? kBack / 2 : (nrows <= 4 ? kBack / 4 : 64));
+    const int cols = RK + 2 * N;
+    for (int r = threadIdx.x / per; r < nrows; r += kBack / per)
+      for (int c = threadIdx.x & (per - 1); c < cols; c += per) {
+        const float* p = sel + (b0 + r) * F + (c < RK ? c : a.R + (c - RK));
+        float v = 0.0f;
+        if (c < a.R || c >= RK) v = ROWS == kFewRows ? slice_sum<20>(p, a.batch * F, slices) : *p;
+        if (c >= RK) bc[r * 2 * N + (c - RK)] = v;
+        else Operands<IO>::put(rd, ROWS, RK, r, c, v);
+      }
   }
-  for (int e = nrows * ldx + threadIdx.x; e < kRows * ldx; e += kBlock) xd[e] = 0.0f;
-  for (int e = threadIdx.x; e < nrows * (CB / 4); e += kBlock) {
-    const int r = e / (CB / 4), g = e % (CB / 4) * 4;
-    const int64_t dg = d0 + g, i = (b0 + r) * a.D + dg;
-    const int nv = a.D - dg < 4 ? (int)(a.D - dg) : 4;
-    raw_t<float, 4> xv(0u);
-    raw_t<IO, 4> zv(0u);
-    if (nv == 4) {
-      xv = load_raw<float, 4, true>(xc + i, 4);
-      if (a.z) zv = load_raw<IO, 4, true>(static_cast<const IO*>(a.z) + i, 4);
-    } else {
-      xv = load_raw<float, 4, false>(xc + i, nv);
-      if (a.z) zv = load_raw<IO, 4, false>(static_cast<const IO*>(a.z) + i, nv);
-    }
-    float z4[4];
-    widen<IO, 4>(zv, z4);
-    *reinterpret_cast<raw_t<float, 4>*>(xl + r * LD + g) = xv;
-    *reinterpret_cast<float4*>(zl + r * LD + g) = make_float4(z4[0], z4[1], z4[2], z4[3]);
+  const int er = threadIdx.x / (CB / 4), eg = threadIdx.x % (CB / 4) * 4;  // row and channels that this thread stages
+  const int64_t ed = d0 + eg;
+  const int env = a.D - ed < 4 ? (int)(a.D - ed) : 4;
+#pragma unroll
+  for (int i = 0; i < (ROWS * CB / 4 + kBack - 1) / kBack; ++i) {
+    const int r = er + i * (kBack / (CB / 4));
+    if (r >= nrows) break;
+    const float* p = xc + (b0 + r) * a.D + ed;
+    *reinterpret_cast<raw_t<float, 4>*>(xl + r * LD + eg) =
+        env == 4 ? load_raw<float, 4, true>(p, 4) : load_raw<float, 4, false>(p, env);
   }
+  const float bias = a.dt_bias && cw < a.D ? a.dt_bias[cw] : 0.0f;
   __syncthreads();
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  {
+    // rows that are not there repeat one that is: their products are not looked at
+    const int r = r16 < nrows ? r16 : 0;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int p = 0; p < PRE; ++p) {
-    if (p * kStep<IO> >= RK) break;
-    OperandA<IO> op;
-    op.set(xd + r16 * ldx + p * kStep<IO> + q * kShare<IO>);
-    acc = op.times(pre[p], acc);
-  }
-  for (int64_t k = PRE * kStep<IO>; k < RK; k += kStep<IO>) {
-    OperandA<IO> op;
-    op.set(xd + r16 * ldx + k + q * kShare<IO>);
-    acc = op.times(operand_b<IO>(wdt, k + q * kShare<IO>, a.R, cw < a.D), acc);
-  }
+    for (int p = 0; p < PRE; ++p) {
+      if (p * kStep<IO> >= RK) break;
+      acc = Operands<IO>::times(rd, ROWS, RK, r, p * kStep<IO> + q * kShare<IO>, pre[p], acc);
+    }
+    for (int k = PRE * kStep<IO>; k < RK; k += kStep<IO>)
+      acc = Operands<IO>::times(rd, ROWS, RK, r, k + q * kShare<IO>,
+                                operand_b<IO>(wdt, k + q * kShare<IO>, a.R, cw < a.D), acc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dl[(4 * q + i) * LD + w * 16 + r16] = acc[i];
+    for (int i = 0; i < 4; ++i)
+      if (4 * q + i < ROWS) dl[(4 * q + i) * LD + w * 16 + r16] = softplus(acc[i] + bias);
+  }
   __syncthreads();
   if (in) {
     ChanConst<NS> cc;
 #pragma unroll
     for (int n = 0; n < NS; ++n) cc.set(n, a.A[d * N + n0 + n]);
-    const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f, dskip = a.dskip ? a.dskip[d] : 0.0f;
 #pragma unroll
     for (int i = 0; i < RP; ++i) {
       const int r = i * RG + rg;
-      const int64_t slot = place[r];
+      const int64_t slot = r < ROWS ? place[r] : -1;
       if (slot < 0) continue;  // the channel's lanes agree
-      const float* sel_r = xd + r * ldx + RK;
+      const float* sel_r = bc + r * 2 * N;
       float Bt[NS], Ct[NS];
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         Bt[n] = sel_r[n0 + n];
         Ct[n] = sel_r[N + n0 + n];
       }
-      const float x = xl[r * LD + cl];
-      const TokenFront f = make_front(dl[r * LD + cl], bias, true);
-      float y = token_step<NS>(cc, f, x, Bt, Ct, h[i]);
+      TokenFront f;
+      f.dt = dl[r * LD + cl];
+      f.dt2 = f.dt * f.dt;
+      f.dth = 0.5f * f.dt;
+      f.pos = true;
+      float y = token_step<NS>(cc, f, xl[r * LD + cl], Bt, Ct, h[i]);
       if constexpr (LPC >= 2) y += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(y), 0xB1, 0xf, 0xf, false));
       if constexpr (LPC == 4) y += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(y), 0x4E, 0xf, 0xf, false));
       float* st = a.state + (slot * a.D + d) * N + n0;
@@ -366,37 +381,49 @@ __global__ __launch_bounds__(kBlock, 3) void ssm_back_kernel(SsmStepArgs a, int 
 #pragma unroll
         for (int n = 0; n < NS; ++n) st[n] = h[i][n];
       }
-      if (n0 == 0) zl[r * LD + cl] = epilogue(y, x, dskip, a.z != nullptr, zl[r * LD + cl]);
+      if (n0 == 0) yl[r * LD + cl] = y;
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < nrows * (CB / 4); e += kBlock) {
-    const int r = e / (CB / 4), g = e % (CB / 4) * 4;
-    const int64_t dg = d0 + g;
-    if (dg >= a.D || place[r] < 0) continue;
-    const float4 v = *reinterpret_cast<const float4*>(zl + r * LD + g);
-    const float o[4] = {v.x, v.y, v.z, v.w};
-    IO* out = static_cast<IO*>(a.out) + (b0 + r) * a.D + dg;
-    if (a.D - dg >= 4) store_raw<IO, 4, true>(out, narrow<IO, 4>(o), 4);
-    else store_raw<IO, 4, false>(out, narrow<IO, 4>(o), (int)(a.D - dg));
+#pragma unroll
+  for (int i = 0; i < (ROWS * CB / 4 + kBack - 1) / kBack; ++i) {
+    const int r = er + i * (kBack / (CB / 4));
+    if (r >= nrows || env <= 0 || place[r] < 0) continue;
+    const int64_t at = (b0 + r) * a.D + ed;
+    raw_t<IO, 4> zr(0u);
+    raw_t<float, 4> dr(0u);
+    if (env == 4) {
+      if (a.z) zr = load_raw<IO, 4, true>(static_cast<const IO*>(a.z) + at, 4);
+      if (a.dskip) dr = load_raw<float, 4, true>(a.dskip + ed, 4);
+    } else {
+      if (a.z) zr = load_raw<IO, 4, false>(static_cast<const IO*>(a.z) + at, env);
+      if (a.dskip) dr = load_raw<float, 4, false>(a.dskip + ed, env);
+    }
+    float z[4], ds[4], o[4];
+    widen<IO, 4>(zr, z);
+    widen<float, 4>(dr, ds);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = epilogue(yl[r * LD + eg + k], xl[r * LD + eg + k], ds[k], a.z != nullptr, z[k]);
+    IO* out = static_cast<IO*>(a.out) + at;
+    if (env == 4) store_raw<IO, 4, true>(out, narrow<IO, 4>(o), 4);
+    else store_raw<IO, 4, false>(out, narrow<IO, 4>(o), env);
   }
 }
 
 struct StepPlan {
-  int tiles, slices, ldx;
+  int tiles, back_tiles, slices;
   bool join;
   size_t off_part, off_sel, bytes;
 };
 
-StepPlan plan_step(int64_t batch, int64_t D, int64_t N, int64_t R, int io) {
+StepPlan plan_step(int64_t batch, int64_t D, int64_t N, int64_t R) {
   StepPlan p;
-  const int64_t F = R + 2 * N, step = io == kIoBF16 ? kStep<uint16_t> : kStep<float>;
+  const int64_t F = R + 2 * N;
   p.tiles = (int)((batch + kRows - 1) / kRows);
   p.slices = (int)((D + kSlice - 1) / kSlice);
-  p.ldx = (int)((R + step - 1) / step * step + 2 * N + kPad);
-  p.ldx = (p.ldx + 3) / 4 * 4;
-  // every back workgroup adds its rows' parts again: worth a launch less while they are few
-  p.join = p.slices > 1 && batch > 4;
+  // every back workgroup adds its rows' parts again: cheaper than a launch while they are few
+  p.join = batch > kFewRows;
+  p.back_tiles = p.join ? (int)((batch + kBackRows - 1) / kBackRows) : 1;
   auto al = [](size_t v) { return (v + 255) / 256 * 256; };
   p.off_part = al((size_t)batch * D * 4);
   p.off_sel = p.off_part + al((size_t)p.slices * batch * F * 4);
@@ -404,13 +431,14 @@ StepPlan plan_step(int64_t batch, int64_t D, int64_t N, int64_t R, int io) {
   return p;
 }
 
-template <typename IO, int N>
+template <typename IO, int N, int ROWS>
 hipError_t back(const SsmStepArgs& a, const StepPlan& p, const float* xc, const float* sel, int slices,
                 hipStream_t s) {
   constexpr int CB = kChannels;
-  const size_t lds = (size_t)kRows * (p.ldx + 3 * (CB + kPad)) * sizeof(float);
-  hipLaunchKernelGGL((ssm_back_kernel<IO, N>), dim3((unsigned)(p.tiles * ((a.D + CB - 1) / CB))), dim3(kBlock), lds, s,
-                     a, p.tiles, p.ldx, xc, sel, slices);
+  const size_t lds = Operands<IO>::bytes(ROWS, (a.R + kStep<IO> - 1) / kStep<IO> * kStep<IO>) +
+                     (size_t)ROWS * (2 * N + 3 * (CB + kPad)) * sizeof(float);
+  hipLaunchKernelGGL((ssm_back_kernel<IO, N, ROWS>), dim3((unsigned)(p.back_tiles * ((a.D + CB - 1) / CB))), dim3(kBack), lds, s,
+                     a, p.back_tiles, xc, sel, slices);
   return hipGetLastError();
 }
 
@@ -434,24 +462,28 @@ hipError_t launch_t(const SsmStepArgs& a, const StepPlan& p, uint8_t* ws, hipStr
   } else {
     sel = part;
   }
+  auto go = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    return p.join ? back<IO, N, kBackRows>(a, p, xc, sel, slices, s) : back<IO, N, kFewRows>(a, p, xc, sel, slices, s);
+  };
   switch (a.N) {
-    case 1: return back<IO, 1>(a, p, xc, sel, slices, s);
-    case 2: return back<IO, 2>(a, p, xc, sel, slices, s);
-    case 4: return back<IO, 4>(a, p, xc, sel, slices, s);
-    case 8: return back<IO, 8>(a, p, xc, sel, slices, s);
-    case 16: return back<IO, 16>(a, p, xc, sel, slices, s);
+    case 1: return go(std::integral_constant<int, 1>());
+    case 2: return go(std::integral_constant<int, 2>());
+    case 4: return go(std::integral_constant<int, 4>());
+    case 8: return go(std::integral_constant<int, 8>());
+    case 16: return go(std::integral_constant<int, 16>());
     default: return hipErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-size_t ssm_step_ws_bytes(int64_t batch, int64_t D, int64_t N, int64_t R, int io) {
-  return plan_step(batch, D, N, R, io).bytes;
+size_t ssm_step_ws_bytes(int64_t batch, int64_t D, int64_t N, int64_t R) {
+  return plan_step(batch, D, N, R).bytes;
 }
 
 hipError_t launch_ssm_step(const SsmStepArgs& a, int io, void* workspace, hipStream_t s) {
-  const StepPlan p = plan_step(a.batch, a.D, a.N, a.R, io);
+  const StepPlan p = plan_step(a.batch, a.D, a.N, a.R);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   return io == kIoBF16 ? launch_t<uint16_t>(a, p, ws, s) : launch_t<float>(a, p, ws, s);
 }
