@@ -21,16 +21,28 @@
 namespace s6 {
 namespace {
 
-constexpr int E = 8;  // elements per thread and chunk
+constexpr int E = 4;  // elements per thread and chunk: 16 bytes of fp32, 8 of bf16
+
+// Sum over a wave, the same value in all lanes: within rows of 16 lanes by lane swaps, then the four rows.
+__device__ __forceinline__ float wave_sum(float v) {
+#define S6_DPP_ADD(ctrl) \
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, false))
+  S6_DPP_ADD(0xB1);   // lane ^ 1
+  S6_DPP_ADD(0x4E);   // lane ^ 2
+  S6_DPP_ADD(0x141);  // mirrored in 8
+  S6_DPP_ADD(0x140);  // mirrored in 16
+#undef S6_DPP_ADD
+  const int i = __float_as_int(v);
+  return (__int_as_float(__builtin_amdgcn_readlane(i, 0)) + __int_as_float(__builtin_amdgcn_readlane(i, 16))) +
+         (__int_as_float(__builtin_amdgcn_readlane(i, 32)) + __int_as_float(__builtin_amdgcn_readlane(i, 48)));
+}
 
 // Sum over the NT threads of a row, the same value in all of them.  Rows of more than a wave meet at
 // workgroup barriers: every thread of the workgroup takes part.
 template <int NT, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float (*lds)[K]) {
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v[k] += __shfl_xor(v[k], m, 64);
+  for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
   if constexpr (NT > 64) {
     __syncthreads();  // the last sum has been read
     if ((threadIdx.x & 63) == 0)
@@ -162,35 +174,56 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
   const NormArgs& a = b.f;
   const int lane = threadIdx.x % NT, slot = threadIdx.x / NT;
   const float inv = 1.0f / (float)a.D;
+  const bool first_gate = a.gate && a.gate_first, after_gate = a.gate && !a.gate_first;
+  // The weights stay in registers over the rows (absent ones as 1): post, alpha scale, pre.
+  float post[NV][E], asc[NV][E], pre[NV][E];
   float spost[NV][E], sscale[NV][E], spre[NV][E];
 #pragma unroll
-  for (int c = 0; c < NV; ++c)
+  for (int c = 0; c < NV; ++c) {
+    const int64_t e0 = (c * NT + lane) * E;
 #pragma unroll
-    for (int i = 0; i < E; ++i) spost[c][i] = sscale[c][i] = spre[c][i] = 0.0f;
+    for (int i = 0; i < E; ++i) {
+      post[c][i] = asc[c][i] = pre[c][i] = 1.0f;
+      spost[c][i] = sscale[c][i] = spre[c][i] = 0.0f;
+    }
+    if (a.post) weights_in<EVEN>(a.post, e0, a.D, post[c]);
+    if (a.scale) weights_in<EVEN>(a.scale, e0, a.D, asc[c]);
+    if (a.pre) weights_in<EVEN>(a.pre, e0, a.D, pre[c]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) asc[c][i] *= a.alpha;
+  }
   for (int64_t first = (int64_t)blockIdx.x * RPB; first < a.rows; first += (int64_t)gridDim.x * RPB) {
     // a row behind the last reads as one of no elements: all threads pass the same barriers
-    const int64_t row = first + slot, D = row < a.rows ? a.D : 0, at = row * D;
+    const int64_t row = first + slot, D = row < a.rows ? a.D : 0, at = row * a.D;
     raw_t<IO, E> xr[NV], gr[NV], dor[NV];
     raw_t<RES, E> rr[NV], drr[NV];
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int64_t e0 = (c * NT + lane) * E;
       xr[c] = chunk_in<IO, EVEN>(static_cast<const IO*>(a.x) + at, e0, D);
+      gr[c] = dor[c] = raw_t<IO, E>(0u);
+      rr[c] = drr[c] = raw_t<RES, E>(0u);
       if (a.gate) gr[c] = chunk_in<IO, EVEN>(static_cast<const IO*>(a.gate) + at, e0, D);
       if (a.residual) rr[c] = chunk_in<RES, EVEN>(static_cast<const RES*>(a.residual) + at, e0, D);
       if (b.dout) dor[c] = chunk_in<IO, EVEN>(static_cast<const IO*>(b.dout) + at, e0, D);
       if (b.dres_out) drr[c] = chunk_in<RES, EVEN>(static_cast<const RES*>(b.dres_out) + at, e0, D);
     }
-    // n = v / rms(v)
-    float n[NV][E], s1[1] = {0.0f};
+    // n = v / rms(v); s = SiLU(gate) and its slope sigma + s (1 - sigma)
+    float n[NV][E], s[NV][E], slope[NV][E], s1[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       widen<IO, E>(xr[c], n[c]);
-      if (a.gate && a.gate_first) {
-        float g[E];
-        widen<IO, E>(gr[c], g);
+      if (a.gate) {
+        widen<IO, E>(gr[c], s[c]);
 #pragma unroll
-        for (int i = 0; i < E; ++i) n[c][i] *= silu(g[i]);
+        for (int i = 0; i < E; ++i) {
+          const float sg = sigmoid(s[c][i]);
+          s[c][i] *= sg;
+          slope[c][i] = __builtin_fmaf(s[c][i], 1.0f - sg, sg);
+        }
+        if (first_gate)
+#pragma unroll
+          for (int i = 0; i < E; ++i) n[c][i] *= s[c][i];
       }
 #pragma unroll
       for (int i = 0; i < E; ++i) s1[0] = __builtin_fmaf(n[c][i], n[c][i], s1[0]);
@@ -200,48 +233,33 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
       row_sum<NT, 1>(s1, reinterpret_cast<float(*)[1]>(lds));
       k = rsqrtf(__builtin_fmaf(s1[0], inv, a.eps));
     }
-    // p, r', and the sums of the second norm
+    // what n is multiplied by to give p
+    auto factor = [&](int c, float (&f)[E]) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = post[c][i];
+      if (after_gate)
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] *= s[c][i];
+    };
+    // r', and the sums of the second norm
     float r[NV][E], s2[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int64_t e0 = (c * NT + lane) * E;
-      float w[E];
+      float f[E];
+      factor(c, f);
+      widen<RES, E>(rr[c], r[c]);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         n[c][i] *= k;
-        r[c][i] = n[c][i];
-      }
-      if (a.post) {
-        weights_in<EVEN>(a.post, e0, D, w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) r[c][i] *= w[i];
-      }
-      if (a.gate && !a.gate_first) {
-        widen<IO, E>(gr[c], w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) r[c][i] *= silu(w[i]);
-      }
-      if (a.scale) {
-        weights_in<EVEN>(a.scale, e0, D, w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) r[c][i] *= w[i];
-      }
-      if (a.residual) {
-        widen<RES, E>(rr[c], w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) r[c][i] = __builtin_fmaf(a.alpha, r[c][i], w[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) r[c][i] *= a.alpha;
+        r[c][i] = __builtin_fmaf(asc[c][i], n[c][i] * f[i], r[c][i]);
       }
       if (b.dout) {
         float d[E];
-        weights_in<EVEN>(a.pre, e0, D, w);
         widen<IO, E>(dor[c], d);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
           s2[0] = __builtin_fmaf(r[c][i], r[c][i], s2[0]);
-          s2[1] = __builtin_fmaf(d[i] * w[i], r[c][i], s2[1]);
+          s2[1] = __builtin_fmaf(d[i] * pre[c][i], r[c][i], s2[1]);
         }
       }
     }
@@ -251,51 +269,34 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
       K = rsqrtf(__builtin_fmaf(s2[0], inv, a.eps));
       kk = K * K * (s2[1] * inv);
     }
-    // dr (kept in r), the sums over rows, e (kept in place of nothing that is still needed) and mean(e n)
-    float e[NV][E];
+    // dr, the sums over rows, dp (kept in r) and mean(e n), e = dp f
     s1[0] = 0.0f;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int64_t e0 = (c * NT + lane) * E;
-      float dr[E], w[E], t[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) dr[i] = 0.0f;
-      if (b.dres_out) widen<RES, E>(drr[c], dr);
+      float dr[E], f[E];
+      factor(c, f);
+      widen<RES, E>(drr[c], dr);
       if (b.dout) {
-        widen<IO, E>(dor[c], t);
-        weights_in<EVEN>(a.pre, e0, D, w);
+        float d[E];
+        widen<IO, E>(dor[c], d);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          spre[c][i] = __builtin_fmaf(t[i], r[c][i] * K, spre[c][i]);
-          dr[i] = __builtin_fmaf(K, __builtin_fmaf(-kk, r[c][i], t[i] * w[i]), dr[i]);
+          spre[c][i] = __builtin_fmaf(d[i], r[c][i] * K, spre[c][i]);
+          dr[i] = __builtin_fmaf(K, __builtin_fmaf(-kk, r[c][i], d[i] * pre[c][i]), dr[i]);
         }
       }
-      if (b.dresidual) chunk_out<RES, EVEN>(static_cast<RES*>(b.dresidual) + at, e0, D, dr);
-      // s: the gate behind the norm; t: p / s / post = n
-      float s[E], post[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) s[i] = post[i] = 1.0f;
-      if (a.gate && !a.gate_first) {
-        widen<IO, E>(gr[c], s);
-#pragma unroll
-        for (int i = 0; i < E; ++i) s[i] = silu(s[i]);
-      }
-      if (a.post) weights_in<EVEN>(a.post, e0, D, post);
-      if (a.scale) {
-        weights_in<EVEN>(a.scale, e0, D, w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) sscale[c][i] = __builtin_fmaf(dr[i], n[c][i] * post[i] * s[i], sscale[c][i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) w[i] = 1.0f;
-      }
+      if (b.dresidual) chunk_out<RES, EVEN>(static_cast<RES*>(b.dresidual) + at, (c * NT + lane) * E, D, dr);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const float dp = dr[i] * (a.alpha * w[i]);
-        spost[c][i] = __builtin_fmaf(dp * s[i], n[c][i], spost[c][i]);
-        r[c][i] = dp * post[i];
-        e[c][i] = r[c][i] * s[i];
-        s1[0] = __builtin_fmaf(e[c][i], n[c][i], s1[0]);
+        sscale[c][i] = __builtin_fmaf(dr[i], n[c][i] * f[i], sscale[c][i]);
+        r[c][i] = dr[i] * asc[c][i];
+      }
+      if (a.post) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          spost[c][i] = __builtin_fmaf(after_gate ? r[c][i] * s[c][i] : r[c][i], n[c][i], spost[c][i]);
+          s1[0] = __builtin_fmaf(r[c][i] * f[i], n[c][i], s1[0]);
+        }
       }
     }
     float m = 0.0f;
@@ -306,21 +307,22 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int64_t e0 = (c * NT + lane) * E;
-      float dx[E], dg[E], x[E], g[E];
+      float dx[E], dg[E], f[E];
+      factor(c, f);
 #pragma unroll
-      for (int i = 0; i < E; ++i) dx[i] = k * __builtin_fmaf(-n[c][i], m, e[c][i]);
+      for (int i = 0; i < E; ++i) dx[i] = k * __builtin_fmaf(-n[c][i], m, r[c][i] * f[i]);
       if (a.gate) {
-        widen<IO, E>(gr[c], g);
-        if (a.gate_first) {
+        if (first_gate) {
+          float x[E];
           widen<IO, E>(xr[c], x);
 #pragma unroll
           for (int i = 0; i < E; ++i) {
-            dg[i] = dx[i] * x[i] * silu_slope(g[i]);
-            dx[i] *= silu(g[i]);
+            dg[i] = dx[i] * x[i] * slope[c][i];
+            dx[i] *= s[c][i];
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < E; ++i) dg[i] = r[c][i] * n[c][i] * silu_slope(g[i]);
+          for (int i = 0; i < E; ++i) dg[i] = r[c][i] * post[c][i] * n[c][i] * slope[c][i];
         }
         if (b.dgate) chunk_out<IO, EVEN>(static_cast<IO*>(b.dgate) + at, e0, D, dg);
       }
@@ -369,6 +371,176 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
   }
 }
 
+// Long rows, whose sums over rows would not fit the registers beside the row: first each row's k, K,
+// K^2 mean(dn' r') and mean(e n) ...
+template <typename IO, typename RES, int NT, int NV, bool EVEN>
+__global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* stats) {
+  static_assert(rows_of(NT) == 1, "a workgroup per row");
+  __shared__ float lds[NT / 64][2];
+  const NormArgs& a = b.f;
+  const int lane = threadIdx.x;
+  const int64_t D = a.D, row = blockIdx.x, at = row * D;
+  const float inv = 1.0f / (float)D;
+  const bool after_gate = a.gate && !a.gate_first;
+  float n[NV][E], f[NV][E], r[NV][E], s1[1] = {0.0f}, s2[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    const int64_t e0 = (c * NT + lane) * E;
+    widen<IO, E>(chunk_in<IO, EVEN>(static_cast<const IO*>(a.x) + at, e0, D), n[c]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[c][i] = 1.0f;
+    if (a.gate) {
+      float g[E];
+      widen<IO, E>(chunk_in<IO, EVEN>(static_cast<const IO*>(a.gate) + at, e0, D), g);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (after_gate) f[c][i] = silu(g[i]);
+        else n[c][i] *= silu(g[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) s1[0] = __builtin_fmaf(n[c][i], n[c][i], s1[0]);
+  }
+  float k = 1.0f;
+  if (a.post) {
+    row_sum<NT, 1>(s1, reinterpret_cast<float(*)[1]>(lds));
+    k = rsqrtf(__builtin_fmaf(s1[0], inv, a.eps));
+  }
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    const int64_t e0 = (c * NT + lane) * E;
+    float w[E], d[E];
+    if (a.post) {
+      weights_in<EVEN>(a.post, e0, D, w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[c][i] *= w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      n[c][i] *= k;
+      r[c][i] = a.alpha * n[c][i] * f[c][i];
+    }
+    if (a.scale) {
+      weights_in<EVEN>(a.scale, e0, D, w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) r[c][i] *= w[i];
+    }
+    if (a.residual) {
+      widen<RES, E>(chunk_in<RES, EVEN>(static_cast<const RES*>(a.residual) + at, e0, D), w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) r[c][i] += w[i];
+    }
+    if (b.dout) {
+      widen<IO, E>(chunk_in<IO, EVEN>(static_cast<const IO*>(b.dout) + at, e0, D), d);
+      weights_in<EVEN>(a.pre, e0, D, w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        s2[0] = __builtin_fmaf(r[c][i], r[c][i], s2[0]);
+        s2[1] = __builtin_fmaf(d[i] * w[i], r[c][i], s2[1]);
+      }
+    }
+  }
+  float K = 0.0f, kk = 0.0f;
+  if (b.dout) {
+    row_sum<NT, 2>(s2, lds);
+    K = rsqrtf(__builtin_fmaf(s2[0], inv, a.eps));
+    kk = K * K * (s2[1] * inv);
+  }
+  s1[0] = 0.0f;
+  if (a.post) {
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int64_t e0 = (c * NT + lane) * E;
+      float dr[E], w[E], d[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) dr[i] = 0.0f;
+      if (b.dres_out) widen<RES, E>(chunk_in<RES, EVEN>(static_cast<const RES*>(b.dres_out) + at, e0, D), dr);
+      if (b.dout) {
+        widen<IO, E>(chunk_in<IO, EVEN>(static_cast<const IO*>(b.dout) + at, e0, D), d);
+        weights_in<EVEN>(a.pre, e0, D, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) dr[i] = __builtin_fmaf(K, __builtin_fmaf(-kk, r[c][i], d[i] * w[i]), dr[i]);
+      }
+      if (a.scale) {
+        weights_in<EVEN>(a.scale, e0, D, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) dr[i] *= w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) s1[0] = __builtin_fmaf(a.alpha * dr[i] * f[c][i], n[c][i], s1[0]);
+    }
+    row_sum<NT, 1>(s1, reinterpret_cast<float(*)[1]>(lds));
+  }
+  if (lane == 0) stats[row] = make_float4(k, K, kk, s1[0] * inv);
+}
+
+// ... then everything else element by element: a thread has E columns of the rows of its chunk, and their sums.
+constexpr int kColRows = 4;  // row chunks (waves) of a workgroup
+
+template <typename IO, typename RES, bool EVEN>
+__global__ __launch_bounds__(64 * kColRows) void norm_cols_kernel(NormBwdArgs b, const float4* stats, int64_t chunk,
+                                                                  float* part) {
+  const NormArgs& a = b.f;
+  const int64_t D = a.D, e0 = ((int64_t)blockIdx.x * 64 + (threadIdx.x & 63)) * E;
+  const int64_t ch = (int64_t)blockIdx.y * kColRows + (threadIdx.x >> 6);
+  const int64_t r0 = ch * chunk, r1 = r0 + chunk < a.rows ? r0 + chunk : a.rows;
+  if (r0 >= a.rows) return;
+  const bool first_gate = a.gate && a.gate_first, after_gate = a.gate && !a.gate_first;
+  float post[E], asc[E], pre[E], spost[E], sscale[E], spre[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    post[i] = asc[i] = pre[i] = 1.0f;
+    spost[i] = sscale[i] = spre[i] = 0.0f;
+  }
+  if (a.post) weights_in<EVEN>(a.post, e0, D, post);
+  if (a.scale) weights_in<EVEN>(a.scale, e0, D, asc);
+  if (a.pre) weights_in<EVEN>(a.pre, e0, D, pre);
+#pragma unroll
+  for (int i = 0; i < E; ++i) asc[i] *= a.alpha;
+  for (int64_t row = r0; row < r1; ++row) {
+    const int64_t at = row * D;
+    raw_t<IO, E> gr(0u), dor(0u);
+    raw_t<RES, E> rr(0u), drr(0u);
+    const raw_t<IO, E> xr = chunk_in<IO, EVEN>(static_cast<const IO*>(a.x) + at, e0, D);
+    if (a.gate) gr = chunk_in<IO, EVEN>(static_cast<const IO*>(a.gate) + at, e0, D);
+    if (a.residual) rr = chunk_in<RES, EVEN>(static_cast<const RES*>(a.residual) + at, e0, D);
+    if (b.dout) dor = chunk_in<IO, EVEN>(static_cast<const IO*>(b.dout) + at, e0, D);
+    if (b.dres_out) drr = chunk_in<RES, EVEN>(static_cast<const RES*>(b.dres_out) + at, e0, D);
+    const float4 st = stats[row];  // k, K, K^2 mean(dn' r'), mean(e n)
+    float x[E], s[E], slope[E], r[E], d[E], dr[E], dx[E], dg[E];
+    widen<IO, E>(xr, x);
+    widen<IO, E>(gr, s);
+    widen<RES, E>(rr, r);
+    widen<IO, E>(dor, d);
+    widen<RES, E>(drr, dr);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float sg = sigmoid(s[i]);
+      s[i] *= sg;
+      slope[i] = __builtin_fmaf(s[i], 1.0f - sg, sg);
+      const float n = (first_gate ? x[i] * s[i] : x[i]) * st.x;
+      const float f = after_gate ? post[i] * s[i] : post[i];
+      const float q = n * f;
+      r[i] = __builtin_fmaf(asc[i], q, r[i]);
+      spre[i] = __builtin_fmaf(d[i], r[i] * st.y, spre[i]);
+      dr[i] = __builtin_fmaf(st.y, __builtin_fmaf(-st.z, r[i], d[i] * pre[i]), dr[i]);
+      sscale[i] = __builtin_fmaf(dr[i], q, sscale[i]);
+      const float dp = dr[i] * asc[i];
+      spost[i] = __builtin_fmaf(after_gate ? dp * s[i] : dp, n, spost[i]);
+      const float dv = st.x * __builtin_fmaf(-n, st.w, dp * f);
+      dx[i] = first_gate ? dv * s[i] : dv;
+      dg[i] = (first_gate ? dv * x[i] : dp * post[i] * n) * slope[i];
+    }
+    if (b.dresidual) chunk_out<RES, EVEN>(static_cast<RES*>(b.dresidual) + at, e0, D, dr);
+    if (b.dgate) chunk_out<IO, EVEN>(static_cast<IO*>(b.dgate) + at, e0, D, dg);
+    chunk_out<IO, EVEN>(static_cast<IO*>(b.dx) + at, e0, D, dx);
+  }
+  float* out = part + ch * 3 * D;
+  chunk_out<float, EVEN>(out, e0, D, spost);
+  chunk_out<float, EVEN>(out + D, e0, D, sscale);
+  chunk_out<float, EVEN>(out + 2 * D, e0, D, spre);
+}
+
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64_t rows, int64_t D, float alpha,
                                                         float* dpost, float* dscale, float* dpre) {
   const int64_t col = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
@@ -383,60 +555,81 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64
   }
 }
 
-template <typename IO, typename RES, int NT, int NV>
-void fwd_at(const NormArgs& a, hipStream_t s) {
-  constexpr int RPB = rows_of(NT);
-  const dim3 grid((unsigned)((a.rows + RPB - 1) / RPB)), block(NT * RPB);
-  if (a.D % E == 0) hipLaunchKernelGGL((norm_fwd_kernel<IO, RES, NT, NV, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((norm_fwd_kernel<IO, RES, NT, NV, false>), grid, block, 0, s, a);
-}
-
-// A wave per row, or a workgroup where rows are long or too few to fill the chip with waves.
-template <typename IO, typename RES>
-hipError_t fwd_types(const NormArgs& a, hipStream_t s) {
-  const int64_t D = a.D;
-  if (D <= 512) fwd_at<IO, RES, 64, 1>(a, s);
-  else if (D <= 4096 && a.rows >= 2048) {
-    if (D <= 1024) fwd_at<IO, RES, 64, 2>(a, s);
-    else if (D <= 1536) fwd_at<IO, RES, 64, 3>(a, s);
-    else if (D <= 2560) fwd_at<IO, RES, 64, 5>(a, s);
-    else fwd_at<IO, RES, 64, 8>(a, s);
-  } else if (D <= 2048) fwd_at<IO, RES, 256, 1>(a, s);
-  else if (D <= 4096) fwd_at<IO, RES, 256, 2>(a, s);
-  else if (D <= 8192) fwd_at<IO, RES, 256, 4>(a, s);
-  else fwd_at<IO, RES, 512, 4>(a, s);
-  return hipGetLastError();
-}
-
-// The backward holds about 90 registers per chunk and thread, so a thread has one chunk of the row as long as
-// a workgroup's threads suffice.
+// Threads and chunks per thread of a row.
 template <typename F>
-void bwd_shape(int64_t D, F f) {
+void row_shape(int64_t D, F f) {
 #define S6_NORM_SHAPE(nt, nv) f(std::integral_constant<int, nt>(), std::integral_constant<int, nv>())
-  if (D <= 512) S6_NORM_SHAPE(64, 1);
-  else if (D <= 1024) S6_NORM_SHAPE(128, 1);
-  else if (D <= 1536) S6_NORM_SHAPE(192, 1);
-  else if (D <= 2048) S6_NORM_SHAPE(256, 1);
-  else if (D <= 2560) S6_NORM_SHAPE(320, 1);
-  else if (D <= 4096) S6_NORM_SHAPE(512, 1);
-  else if (D <= 8192) S6_NORM_SHAPE(512, 2);
-  else S6_NORM_SHAPE(1024, 2);
+  if (D <= 256) S6_NORM_SHAPE(64, 1);
+  else if (D <= 512) S6_NORM_SHAPE(64, 2);
+  else if (D <= 768) S6_NORM_SHAPE(64, 3);
+  else if (D <= 1024) S6_NORM_SHAPE(128, 2);
+  else if (D <= 1536) S6_NORM_SHAPE(128, 3);
+  else if (D <= 2048) S6_NORM_SHAPE(256, 2);
+  else if (D <= 2560) S6_NORM_SHAPE(320, 2);
+  else if (D <= 4096) S6_NORM_SHAPE(512, 2);
+  else if (D <= 8192) S6_NORM_SHAPE(1024, 2);
+  else S6_NORM_SHAPE(1024, 4);
 #undef S6_NORM_SHAPE
 }
 
-int64_t bwd_blocks(int64_t rows, int64_t D) {
-  int64_t n = 0;
-  bwd_shape(D, [&](auto nt, auto) { n = (rows + rows_of(nt) - 1) / rows_of(nt); });
-  return n < 768 ? n : 768;
+template <typename IO, typename RES>
+hipError_t fwd_types(const NormArgs& a, hipStream_t s) {
+  row_shape(a.D, [&](auto nt, auto nv) {
+    constexpr int NT = decltype(nt)::value, NV = decltype(nv)::value, RPB = rows_of(NT);
+    const dim3 grid((unsigned)((a.rows + RPB - 1) / RPB)), block(NT * RPB);
+    if (a.D % E == 0) hipLaunchKernelGGL((norm_fwd_kernel<IO, RES, NT, NV, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((norm_fwd_kernel<IO, RES, NT, NV, false>), grid, block, 0, s, a);
+  });
+  return hipGetLastError();
+}
+
+// Rows up to here keep the sums over rows beside the row.
+constexpr int64_t kSumsDim = 4096;
+
+struct NormBwdPlan {
+  int64_t parts;  // rows of part sums
+  int64_t chunk;  // long rows: rows per part
+  size_t off_stats, bytes;
+};
+
+NormBwdPlan plan_norm_bwd(int64_t rows, int64_t D) {
+  NormBwdPlan p{0, 0, 0, 0};
+  if (D <= kSumsDim) {
+    row_shape(D, [&](auto nt, auto) { p.parts = (rows + rows_of(nt) - 1) / rows_of(nt); });
+    p.parts = p.parts < 1024 ? p.parts : 1024;  // workgroups that fill the chip (768: 48 us, 1024: 44, 1536: 49 at 16384 x 768)
+  } else {
+    // enough waves for the chip, and at least 16 rows each
+    const int64_t waves = (D + 64 * E - 1) / (64 * E);
+    int64_t n = (4096 + waves - 1) / waves;
+    n = n < (rows + 15) / 16 ? n : (rows + 15) / 16;
+    p.chunk = n < 1 ? 1 : (rows + n - 1) / n;
+    p.parts = p.chunk < 1 ? 0 : (rows + p.chunk - 1) / p.chunk;
+  }
+  p.off_stats = ((size_t)p.parts * 3 * (size_t)D * sizeof(float) + 255) / 256 * 256;
+  p.bytes = D <= kSumsDim ? (size_t)p.parts * 3 * (size_t)D * sizeof(float) : p.off_stats + (size_t)rows * sizeof(float4);
+  return p;
 }
 
 template <typename IO, typename RES>
-hipError_t bwd_types(const NormBwdArgs& b, float* part, hipStream_t s) {
-  bwd_shape(b.f.D, [&](auto nt, auto nv) {
+hipError_t bwd_types(const NormBwdArgs& b, const NormBwdPlan& p, float* part, hipStream_t s) {
+  const int64_t D = b.f.D;
+  row_shape(D, [&](auto nt, auto nv) {
     constexpr int NT = decltype(nt)::value, NV = decltype(nv)::value;
-    const dim3 grid((unsigned)bwd_blocks(b.f.rows, b.f.D)), block(NT * rows_of(NT));
-    if (b.f.D % E == 0) hipLaunchKernelGGL((norm_bwd_kernel<IO, RES, NT, NV, true>), grid, block, 0, s, b, part);
-    else hipLaunchKernelGGL((norm_bwd_kernel<IO, RES, NT, NV, false>), grid, block, 0, s, b, part);
+    if constexpr (NT * NV * E <= kSumsDim) {
+      const dim3 grid((unsigned)p.parts), block(NT * rows_of(NT));
+      if (D % E == 0) hipLaunchKernelGGL((norm_bwd_kernel<IO, RES, NT, NV, true>), grid, block, 0, s, b, part);
+      else hipLaunchKernelGGL((norm_bwd_kernel<IO, RES, NT, NV, false>), grid, block, 0, s, b, part);
+    } else {
+      float4* stats = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(part) + p.off_stats);
+      const dim3 grid((unsigned)((D + 64 * E - 1) / (64 * E)), (unsigned)((p.parts + kColRows - 1) / kColRows));
+      if (D % E == 0) {
+        hipLaunchKernelGGL((norm_stats_kernel<IO, RES, NT, NV, true>), dim3((unsigned)b.f.rows), dim3(NT), 0, s, b, stats);
+        hipLaunchKernelGGL((norm_cols_kernel<IO, RES, true>), grid, dim3(64 * kColRows), 0, s, b, stats, p.chunk, part);
+      } else {
+        hipLaunchKernelGGL((norm_stats_kernel<IO, RES, NT, NV, false>), dim3((unsigned)b.f.rows), dim3(NT), 0, s, b, stats);
+        hipLaunchKernelGGL((norm_cols_kernel<IO, RES, false>), grid, dim3(64 * kColRows), 0, s, b, stats, p.chunk, part);
+      }
+    }
   });
   return hipGetLastError();
 }
@@ -444,7 +637,9 @@ hipError_t bwd_types(const NormBwdArgs& b, float* part, hipStream_t s) {
 }  // namespace
 
 bool norm_fits(int64_t rows, int64_t D) {
-  return rows * (D <= 512 ? 64 : (D <= 8192 ? 256 : 512)) < (int64_t(1) << 32) - 1024;
+  bool fits = true;
+  row_shape(D, [&](auto nt, auto) { fits = rows * nt < (int64_t(1) << 32) - 1024; });
+  return fits;
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int io, int res, hipStream_t s) {
@@ -452,21 +647,22 @@ hipError_t launch_norm_fwd(const NormArgs& a, int io, int res, hipStream_t s) {
   return fwd_types<float, float>(a, s);
 }
 
-size_t norm_bwd_ws_bytes(int64_t rows, int64_t D) { return (size_t)bwd_blocks(rows, D) * 3 * (size_t)D * sizeof(float); }
+size_t norm_bwd_ws_bytes(int64_t rows, int64_t D) { return plan_norm_bwd(rows, D).bytes; }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& b, int io, int res, void* workspace, hipStream_t s) {
   float* part = static_cast<float*>(workspace);
   const int64_t D = b.f.D;
+  const NormBwdPlan p = plan_norm_bwd(b.f.rows, D);
   hipError_t e = hipSuccess;
   if (b.f.rows > 0) {
     if (io == kIoBF16)
-      e = res == kIoBF16 ? bwd_types<uint16_t, uint16_t>(b, part, s) : bwd_types<uint16_t, float>(b, part, s);
+      e = res == kIoBF16 ? bwd_types<uint16_t, uint16_t>(b, p, part, s) : bwd_types<uint16_t, float>(b, p, part, s);
     else
-      e = bwd_types<float, float>(b, part, s);
+      e = bwd_types<float, float>(b, p, part, s);
   }
   if (e != hipSuccess || !(b.dpost || b.dscale || b.dpre)) return e;
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((3 * D + 31) / 32)), dim3(1024), 0, s, part,
-                     b.f.rows > 0 ? bwd_blocks(b.f.rows, D) : 0, D, b.f.alpha, b.dpost, b.dscale, b.dpre);
+  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((3 * D + 31) / 32)), dim3(1024), 0, s, part, p.parts, D,
+                     b.f.alpha, b.dpost, b.dscale, b.dpre);
   return hipGetLastError();
 }
 
