@@ -23,8 +23,10 @@ namespace {
 
 constexpr int E = 4;  // elements per thread and chunk: 16 bytes of fp32, 8 of bf16
 
-// Sum over a wave, the same value in all lanes: within rows of 16 lanes by lane swaps, then the four rows.
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over NT lanes of a wave (16, 32 or 64), the same value in all of them: within rows of 16 lanes by lane
+// swaps, then the rows.
+template <int NT>
+__device__ __forceinline__ float lane_sum(float v) {
 #define S6_DPP_ADD(ctrl) \
   v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, false))
   S6_DPP_ADD(0xB1);   // lane ^ 1
@@ -32,6 +34,8 @@ __device__ __forceinline__ float wave_sum(float v) {
   S6_DPP_ADD(0x141);  // mirrored in 8
   S6_DPP_ADD(0x140);  // mirrored in 16
 #undef S6_DPP_ADD
+  if constexpr (NT == 16) return v;
+  if constexpr (NT == 32) return v + __shfl_xor(v, 16, 64);
   const int i = __float_as_int(v);
   return (__int_as_float(__builtin_amdgcn_readlane(i, 0)) + __int_as_float(__builtin_amdgcn_readlane(i, 16))) +
          (__int_as_float(__builtin_amdgcn_readlane(i, 32)) + __int_as_float(__builtin_amdgcn_readlane(i, 48)));
@@ -42,7 +46,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 template <int NT, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float (*lds)[K]) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
+  for (int k = 0; k < K; ++k) v[k] = lane_sum<(NT < 64 ? NT : 64)>(v[k]);
   if constexpr (NT > 64) {
     __syncthreads();  // the last sum has been read
     if ((threadIdx.x & 63) == 0)
@@ -81,7 +85,7 @@ constexpr int rows_of(int nt) { return nt > 128 ? 1 : 256 / nt; }
 template <typename IO, typename RES, int NT, int NV, bool EVEN>
 __global__ __launch_bounds__(NT* rows_of(NT)) void norm_fwd_kernel(NormArgs a) {
   constexpr int RPB = rows_of(NT);
-  __shared__ float lds[NT / 64 * RPB][1];
+  __shared__ float lds[NT * RPB / 64][1];
   const int lane = threadIdx.x % NT;
   const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / NT;
   // a row behind the last reads as one of no elements
@@ -170,7 +174,7 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_fwd_kernel(NormArgs a) {
 template <typename IO, typename RES, int NT, int NV, bool EVEN>
 __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b, float* part) {
   constexpr int RPB = rows_of(NT);
-  __shared__ float lds[NT / 64 * RPB][2];
+  __shared__ float lds[NT * RPB / 64][2];
   const NormArgs& a = b.f;
   const int lane = threadIdx.x % NT, slot = threadIdx.x / NT;
   const float inv = 1.0f / (float)a.D;
@@ -559,7 +563,9 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64
 template <typename F>
 void row_shape(int64_t D, F f) {
 #define S6_NORM_SHAPE(nt, nv) f(std::integral_constant<int, nt>(), std::integral_constant<int, nv>())
-  if (D <= 256) S6_NORM_SHAPE(64, 1);
+  if (D <= 64) S6_NORM_SHAPE(16, 1);
+  else if (D <= 128) S6_NORM_SHAPE(32, 1);
+  else if (D <= 256) S6_NORM_SHAPE(64, 1);
   else if (D <= 512) S6_NORM_SHAPE(64, 2);
   else if (D <= 768) S6_NORM_SHAPE(64, 3);
   else if (D <= 1024) S6_NORM_SHAPE(128, 2);
