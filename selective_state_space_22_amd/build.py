@@ -1,4 +1,5 @@
-"""Build libmamba_mi355x.so in-tree with hipcc for gfx950.
+"""Build libmamba_mi355x.so in-tree with hipcc for gfx950, and the module _layer that marshals
+layer.py's calls (host code over torch's C++ tensors, which the library itself does not know).
 
     python -m selective_state_space_22_amd.build
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -44,13 +46,30 @@ def link_command(objs: list[str], out: str) -> list[str]:
     return [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", out] + objs
 
 
+BIND = os.path.join(HERE, "_layer.so")
+
+
+def bind_command(out: str) -> list[str]:
+    """Host compiler's command for the marshalling module."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + \
+        [a for d in include for a in ("-isystem", d)] + \
+        [os.path.join(CSRC, "bind_layer.cpp"), "-o", out, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch",
+         "-ltorch_cpu", "-lc10", "-ldl"]
+
+
 def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed: {' '.join(cmd[-3:])}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd[-3:])}")
 
 
 def build(verbose: bool = False) -> str:
@@ -60,11 +79,14 @@ def build(verbose: bool = False) -> str:
     objs = [os.path.join(OBJ_DIR, os.path.splitext(s)[0] + ".o") for s in SOURCES]
     jobs = max(1, min(len(SOURCES), int(os.environ.get("MAX_JOBS", os.cpu_count() or 1))))
     with ThreadPoolExecutor(max_workers=jobs) as pool:
+        bind = pool.submit(_run, bind_command(BIND + ".tmp"), verbose)
         list(pool.map(lambda so: _run(compile_command(os.path.join(CSRC, so[0]), so[1]), verbose),
                       zip(SOURCES, objs)))
+        bind.result()
     tmp = LIB + ".tmp"
     _run(link_command(objs, tmp), verbose)
     os.replace(tmp, LIB)
+    os.replace(BIND + ".tmp", BIND)
     return LIB
 
 

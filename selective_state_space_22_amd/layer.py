@@ -1,17 +1,23 @@
-"""Thin ctypes binding of the layer operators (include/mamba_mi355x_layer.h): the short causal
+"""Thin binding of the layer operators (include/mamba_mi355x_layer.h): the short causal
 convolution, one token of a layer, the norms around a block, verification of drafted tokens.
 
-As in binding.py the functions keep the C names and only marshal torch tensors
-(device memory, the current HIP stream) into the C ABI; there is no fallback.
+As in binding.py the functions keep the C names and only marshal torch tensors (device
+memory, the current HIP stream) into the C ABI; there is no fallback.  The marshalling
+itself is the module _layer (csrc/bind_layer.cpp), which calls the library that ctypes loads.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
-from .binding import MambaError, _io_dtype, load_library
-from .lm import _arg, _reset_bytes, _stream, _workspace
+from .binding import MambaError, load_library
+
+_HERE = os.path.dirname(os.path.abspath(__file__))
+BIND_PATH = os.path.join(_HERE, "_layer.so")
 
 _typed = None
+_module = None
 
 
 def _lib():
@@ -39,6 +45,24 @@ def _lib():
     return lib
 
 
+def _native():
+    """The marshalling module, loaded once.  Raises if it has not been built."""
+    global _module
+    if _module is not None:
+        return _module
+    import torch
+
+    if not os.path.exists(BIND_PATH):
+        raise ImportError(f"{BIND_PATH} is missing: build it with `python -m selective_state_space_22_amd.build`")
+    spec = importlib.util.spec_from_file_location("selective_state_space_22_amd._layer", BIND_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    module.use(_lib()._handle, MambaError, stream)
+    _module = module
+    return module
+
+
 def mamba_conv_fwd(x, weight, bias=None, window=None, reset=None, lengths=None, silu=True, out=None, last_window=None,
                    return_last_window=True):
     """Short causal convolution: c_t = bias + sum_j weight[:, j] x_{t-(W-1)+j}, out = SiLU(c) (c without silu).
@@ -47,24 +71,7 @@ def mamba_conv_fwd(x, weight, bias=None, window=None, reset=None, lengths=None, 
     (batch, W - 1, D), the inputs before the first; reset: (batch, L) bool or uint8, a row's first token of
     each document; lengths: (batch,) int32, rows padded behind them (out is zero there).
     Returns (out, last_window): the window with which the rows go on."""
-    import torch
-
-    lib = _lib()
-    batch, L, D = x.shape
-    W = weight.shape[1]
-    io, dev, f32, t = _io_dtype(x), x.device, torch.float32, x.dtype
-    shape, wshape = (batch, L, D), (batch, W - 1, D)
-    out = torch.empty_like(x) if out is None else out
-    if last_window is None and return_last_window:
-        last_window = torch.empty(wshape, dtype=t, device=dev)
-    st = lib.mamba_conv_fwd(
-        batch, L, D, W, io, _arg(x, "x", t, shape, dev), _arg(weight, "weight", f32, (D, W), dev),
-        _arg(bias, "bias", f32, (D,), dev), _arg(window, "window", t, wshape, dev),
-        _reset_bytes(reset, (batch, L), dev), _arg(lengths, "lengths", torch.int32, (batch,), dev), int(bool(silu)),
-        _arg(out, "out", t, shape, dev), _arg(last_window, "last_window", t, wshape, dev), _stream(dev))
-    if st != 0:
-        raise MambaError("mamba_conv_fwd", st)
-    return out, last_window
+    return _native().conv_fwd(x, weight, bias, window, reset, lengths, silu, out, last_window, return_last_window)
 
 
 def mamba_conv_bwd_workspace_size(batch: int, seqlen: int, dim: int, width: int, io_dtype: int) -> int:
@@ -77,53 +84,18 @@ def mamba_conv_bwd(x, weight, dout, bias=None, window=None, reset=None, silu=Tru
 
     Returns a dict with dx, dweight and those of dbias and dwindow named in ``want``.  Preallocated
     outputs may be passed in ``grads`` (same keys)."""
-    import torch
-
-    lib = _lib()
-    batch, L, D = x.shape
-    W = weight.shape[1]
-    io, dev, f32, t = _io_dtype(x), x.device, torch.float32, x.dtype
-    shape, wshape = (batch, L, D), (batch, W - 1, D)
-    like = {"dx": (shape, t), "dweight": ((D, W), f32), "dbias": ((D,), f32), "dwindow": (wshape, t)}
-    need = ["dx", "dweight"] + list(want)
-    g = dict(grads or {})
-    for k in need:
-        if k not in g:
-            g[k] = torch.empty(like[k][0], dtype=like[k][1], device=dev)
-    workspace, ws, ws_bytes = _workspace(workspace, lib.mamba_conv_bwd_workspace_size(batch, L, D, W, io), dev)
-
-    def gp(k):
-        return _arg(g[k], k, like[k][1], like[k][0], dev) if k in g else None
-
-    st = lib.mamba_conv_bwd(
-        batch, L, D, W, io, _arg(x, "x", t, shape, dev), _arg(weight, "weight", f32, (D, W), dev),
-        _arg(bias, "bias", f32, (D,), dev), _arg(window, "window", t, wshape, dev),
-        _reset_bytes(reset, (batch, L), dev), int(bool(silu)), _arg(dout, "dout", t, shape, dev),
-        _arg(dlast_window, "dlast_window", t, wshape, dev), gp("dx"), gp("dweight"), gp("dbias"), gp("dwindow"), ws,
-        ws_bytes, _stream(dev))
-    if st != 0:
-        raise MambaError("mamba_conv_bwd", st)
-    return {k: g[k] for k in need}
+    g = grads or {}
+    dx, dweight, dbias, dwindow = _native().conv_bwd(
+        x, weight, dout, bias, window, reset, silu, dlast_window, g.get("dx"), g.get("dweight"), g.get("dbias"),
+        g.get("dwindow"), "dbias" in want, "dwindow" in want, workspace)
+    res = {"dx": dx, "dweight": dweight, "dbias": dbias, "dwindow": dwindow}
+    return {k: res[k] for k in ("dx", "dweight", *want)}
 
 
 def mamba_conv_update(window, x, weight, bias=None, slots=None, silu=True, out=None):
     """One token of mamba_conv_fwd in place on window (nslots, W - 1, D); x: (batch, D).  slots: (batch,) int32,
     the window of each row (None: row b has window b), negative for an idle row, whose out is left as it was."""
-    import torch
-
-    lib = _lib()
-    batch, D = x.shape
-    nslots, W = window.shape[0], weight.shape[1]
-    io, dev, f32, t = _io_dtype(x), x.device, torch.float32, x.dtype
-    out = torch.empty_like(x) if out is None else out
-    st = lib.mamba_conv_update(
-        batch, D, W, io, nslots, _arg(window, "window", t, (nslots, W - 1, D), dev), _arg(x, "x", t, (batch, D), dev),
-        _arg(weight, "weight", f32, (D, W), dev), _arg(bias, "bias", f32, (D,), dev),
-        _arg(slots, "slots", torch.int32, (batch,), dev), int(bool(silu)), _arg(out, "out", t, (batch, D), dev),
-        _stream(dev))
-    if st != 0:
-        raise MambaError("mamba_conv_update", st)
-    return out
+    return _native().conv_update(window, x, weight, bias, slots, silu, out)
 
 
 def mamba_conv_ssm_update_workspace_size(batch: int, dim: int, dstate: int, dt_rank: int, io_dtype: int) -> int:
@@ -135,25 +107,19 @@ def mamba_conv_ssm_update(state, window, x, conv_weight, W_x, W_dt, A, conv_bias
     """One token of a layer from its input projection on, in place on state (nslots, D, N) float32 and window
     (nslots, W - 1, D): the convolution with SiLU, the selection projections (W_x (R + 2N, D), W_dt (D, R)) and
     the state update, with fp32 values between them.  x, z: (batch, D); slots as for mamba_conv_update."""
+    return _native().conv_ssm_update(state, window, x, conv_weight, W_x, W_dt, A, conv_bias, z, dt_bias, Dskip, slots, out,
+                                     workspace)
+
+
+def _res_code(res_dtype):
+    """The residual stream's type as the module takes it."""
+    if res_dtype is None:
+        return -1
     import torch
 
-    lib = _lib()
-    batch, D = x.shape
-    nslots, W, N, R = state.shape[0], conv_weight.shape[1], A.shape[1], W_dt.shape[1]
-    io, dev, f32, t = _io_dtype(x), x.device, torch.float32, x.dtype
-    out = torch.empty_like(x) if out is None else out
-    workspace, ws, ws_bytes = _workspace(workspace, lib.mamba_conv_ssm_update_workspace_size(batch, D, N, R, io), dev)
-    st = lib.mamba_conv_ssm_update(
-        batch, D, N, R, W, io, nslots, _arg(state, "state", f32, (nslots, D, N), dev),
-        _arg(window, "window", t, (nslots, W - 1, D), dev), _arg(x, "x", t, (batch, D), dev),
-        _arg(conv_weight, "conv_weight", f32, (D, W), dev), _arg(conv_bias, "conv_bias", f32, (D,), dev),
-        _arg(W_x, "W_x", t, (R + 2 * N, D), dev), _arg(W_dt, "W_dt", t, (D, R), dev),
-        _arg(dt_bias, "dt_bias", f32, (D,), dev), _arg(A, "A", f32, (D, N), dev), _arg(Dskip, "Dskip", f32, (D,), dev),
-        _arg(z, "z", t, (batch, D), dev), _arg(slots, "slots", torch.int32, (batch,), dev),
-        _arg(out, "out", t, (batch, D), dev), ws, ws_bytes, _stream(dev))
-    if st != 0:
-        raise MambaError("mamba_conv_ssm_update", st)
-    return out
+    if res_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"residual must be float32 or bfloat16, got {res_dtype}")
+    return 0 if res_dtype == torch.float32 else 1
 
 
 def mamba_residual_norm_fwd(x, pre_weight=None, gate=None, post_weight=None, scale=None, residual=None, alpha=1.0,
@@ -166,35 +132,8 @@ def mamba_residual_norm_fwd(x, pre_weight=None, gate=None, post_weight=None, sca
     x, gate: (..., D) float32 or bfloat16; residual: the same shape, x's type or float32; the weights and scale:
     (D,) float32.  None leaves that part out.  Returns (out, residual_out); out is None without pre_weight.
     res_dtype: residual_out's type where neither residual nor residual_out gives it (default: x's)."""
-    import torch
-
-    lib = _lib()
-    shape, D = x.shape, x.shape[-1]
-    rows = x.numel() // D if D else 0
-    io, dev, f32, t = _io_dtype(x), x.device, torch.float32, x.dtype
-    rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else res_dtype or t
-    if residual_out is None and return_residual:
-        residual_out = torch.empty(shape, dtype=rt, device=dev)
-    if pre_weight is None:
-        out = None
-    elif out is None:
-        out = torch.empty_like(x)
-    st = lib.mamba_residual_norm_fwd(
-        rows, D, io, _res_dtype(rt, t), _arg(x, "x", t, shape, dev), _arg(gate, "gate", t, shape, dev),
-        int(bool(gate_first)), _arg(post_weight, "post_weight", f32, (D,), dev), _arg(scale, "scale", f32, (D,), dev),
-        _arg(residual, "residual", rt, shape, dev), _arg(pre_weight, "pre_weight", f32, (D,), dev), alpha, eps,
-        _arg(residual_out, "residual_out", rt, shape, dev), _arg(out, "out", t, shape, dev), _stream(dev))
-    if st != 0:
-        raise MambaError("mamba_residual_norm_fwd", st)
-    return out, residual_out
-
-
-def _res_dtype(rt, t):
-    import torch
-
-    if rt not in (t, torch.float32):
-        raise TypeError(f"residual must be {t} or {torch.float32}, got {rt}")
-    return 0 if rt == torch.float32 else 1
+    return _native().norm_fwd(x, pre_weight, gate, post_weight, scale, residual, alpha, eps, gate_first, out, residual_out,
+                              _res_code(res_dtype), return_residual)
 
 
 def mamba_residual_norm_bwd_workspace_size(rows: int, dim: int, io_dtype: int) -> int:
@@ -208,39 +147,17 @@ def mamba_residual_norm_bwd(x, pre_weight=None, dout=None, dresidual_out=None, g
 
     dout is given exactly with pre_weight.  Returns a dict with dx and, of those named in ``want``, the
     gradients of the inputs that are given.  Preallocated outputs may be passed in ``grads`` (same keys)."""
-    import torch
+    g = grads or {}
+    wanted = [("dgate" in want and gate is not None), ("dresidual" in want and residual is not None),
+              ("dpost_weight" in want and post_weight is not None), ("dscale" in want and scale is not None),
+              ("dpre_weight" in want and pre_weight is not None)]
+    given = [g.get(k) if w else None for k, w in zip(_NORM_GRADS, wanted)]
+    made = _native().norm_bwd(x, pre_weight, dout, dresidual_out, gate, post_weight, scale, residual, alpha, eps, gate_first,
+                              _res_code(res_dtype), g.get("dx"), *given, *wanted, workspace)
+    return {"dx": made[0], **{k: t for k, t in zip(_NORM_GRADS, made[1:]) if t is not None}}
 
-    lib = _lib()
-    shape, D = x.shape, x.shape[-1]
-    rows = x.numel() // D if D else 0
-    io, dev, f32, t = _io_dtype(x), x.device, torch.float32, x.dtype
-    if (dout is None) != (pre_weight is None):
-        raise ValueError("dout and pre_weight go together")
-    rt = residual.dtype if residual is not None else dresidual_out.dtype if dresidual_out is not None \
-        else res_dtype or t
-    like = {"dx": (shape, t), "dgate": (shape, t), "dresidual": (shape, rt), "dpost_weight": ((D,), f32),
-            "dscale": ((D,), f32), "dpre_weight": ((D,), f32)}
-    given = {"dgate": gate, "dresidual": residual, "dpost_weight": post_weight, "dscale": scale,
-             "dpre_weight": pre_weight}
-    need = ["dx"] + [k for k in want if given[k] is not None]
-    g = dict(grads or {})
-    for k in need:
-        if k not in g:
-            g[k] = torch.empty(like[k][0], dtype=like[k][1], device=dev)
-    workspace, ws, ws_bytes = _workspace(workspace, lib.mamba_residual_norm_bwd_workspace_size(rows, D, io), dev)
 
-    def gp(k):
-        return _arg(g[k], k, like[k][1], like[k][0], dev) if k in need else None
-
-    st = lib.mamba_residual_norm_bwd(
-        rows, D, io, _res_dtype(rt, t), _arg(x, "x", t, shape, dev), _arg(gate, "gate", t, shape, dev),
-        int(bool(gate_first)), _arg(post_weight, "post_weight", f32, (D,), dev), _arg(scale, "scale", f32, (D,), dev),
-        _arg(residual, "residual", rt, shape, dev), _arg(pre_weight, "pre_weight", f32, (D,), dev), alpha, eps,
-        _arg(dout, "dout", t, shape, dev), _arg(dresidual_out, "dresidual_out", rt, shape, dev), gp("dx"), gp("dgate"),
-        gp("dresidual"), gp("dpost_weight"), gp("dscale"), gp("dpre_weight"), ws, ws_bytes, _stream(dev))
-    if st != 0:
-        raise MambaError("mamba_residual_norm_bwd", st)
-    return {k: g[k] for k in need}
+_NORM_GRADS = ("dgate", "dresidual", "dpost_weight", "dscale", "dpre_weight")
 
 
 def mamba_draft_verify_workspace_size(rows: int, drafts: int, vocab: int, io_dtype: int) -> int:
@@ -255,20 +172,4 @@ def mamba_draft_verify(target, draft, drafted, uniform, noise, counts=None, toke
     target: (rows, K + 1, vocab), draft: (rows, K, vocab) float32 or bfloat16; drafted: (rows, K) int64; uniform:
     (rows, K) and noise: (rows, vocab) float32; counts: (rows,) int32, drafts of each row (None: K).
     Returns (tokens int64 (rows, K + 1), -1 behind the drawn one, accepted int32 (rows,))."""
-    import torch
-
-    lib = _lib()
-    rows, K, V = draft.shape
-    io, dev, f32, t = _io_dtype(target), target.device, torch.float32, target.dtype
-    tokens = torch.empty((rows, K + 1), dtype=torch.int64, device=dev) if tokens is None else tokens
-    accepted = torch.empty((rows,), dtype=torch.int32, device=dev) if accepted is None else accepted
-    workspace, ws, ws_bytes = _workspace(workspace, lib.mamba_draft_verify_workspace_size(rows, K, V, io), dev)
-    st = lib.mamba_draft_verify(
-        rows, K, V, io, _arg(target, "target", t, (rows, K + 1, V), dev), _arg(draft, "draft", t, (rows, K, V), dev),
-        _arg(drafted, "drafted", torch.int64, (rows, K), dev), _arg(uniform, "uniform", f32, (rows, K), dev),
-        _arg(noise, "noise", f32, (rows, V), dev), _arg(counts, "counts", torch.int32, (rows,), dev),
-        _arg(tokens, "tokens", torch.int64, (rows, K + 1), dev),
-        _arg(accepted, "accepted", torch.int32, (rows,), dev), ws, ws_bytes, _stream(dev))
-    if st != 0:
-        raise MambaError("mamba_draft_verify", st)
-    return tokens, accepted
+    return _native().draft_verify(target, draft, drafted, uniform, noise, counts, tokens, accepted, workspace)
