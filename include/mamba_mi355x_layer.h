@@ -46,8 +46,8 @@ extern "C" {
  *                  of the row, the carried window's among them where it is shorter, zero
  *                  where a reset cut them off: the window with which the row goes on
  * Limits: 0 <= batch <= 65535, 0 <= seqlen <= 2^40, 0 <= dim <= 4194304, 2 <= width <= 4
- * (else MAMBA_ERR_UNSUPPORTED), and batch * dim / 4 times the number of 64-token chunks of a
- * sequence and one below 2^32.  seqlen == 0 writes only last_window (= window or zero).
+ * (else MAMBA_ERR_UNSUPPORTED), and batch * ceil(dim / 2) * (ceil(seqlen / 32) + 1) < 2^31.
+ * seqlen == 0 writes only last_window (= window or zero).
  */
 int mamba_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype, const void* x,
                    const float* weight, const float* bias, const void* window, const uint8_t* reset,
@@ -82,7 +82,7 @@ int mamba_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, in
  *                  idle row: nothing of it is read, its out and every window stay as they
  *                  were.  A window named by two rows is written by both in no order.
  *   weight, bias, silu : as for mamba_conv_fwd
- * Limits: 0 <= batch <= 65535, 0 <= dim <= 4194304, batch * dim < 2^33, 0 <= nslots < 2^31, width as there.
+ * Limits: 0 <= batch <= 65535, 0 <= dim <= 4194304, batch * ceil(dim / 2) < 2^30, 0 <= nslots < 2^31, width as there.
  */
 int mamba_conv_update(int64_t batch, int64_t dim, int64_t width, int io_dtype, int64_t nslots, void* window,
                       const void* x, const float* weight, const float* bias, const int32_t* slots, int silu, void* out,
@@ -105,7 +105,7 @@ int mamba_conv_update(int64_t batch, int64_t dim, int64_t width, int io_dtype, i
  *   slots, nslots : as for mamba_conv_update, for state and window alike
  *   workspace    : mamba_conv_ssm_update_workspace_size() bytes of scratch
  * Limits: 0 <= batch <= 65535, 0 <= dim <= 4194304, dstate in {1, 2, 4, 8, 16}, 1 <= dt_rank <= 512,
- * 2 <= width <= 4, 0 <= nslots < 2^31, and ceil(batch / 16) * dim < 2^30.
+ * 2 <= width <= 4, 0 <= nslots < 2^31, and ceil(batch / 16) * dim < 2^28.
  */
 size_t mamba_conv_ssm_update_workspace_size(int64_t batch, int64_t dim, int64_t dstate, int64_t dt_rank, int io_dtype);
 int mamba_conv_ssm_update(int64_t batch, int64_t dim, int64_t dstate, int64_t dt_rank, int64_t width, int io_dtype,
@@ -130,8 +130,8 @@ int mamba_conv_ssm_update(int64_t batch, int64_t dim, int64_t dstate, int64_t dt
  *                  and may be NULL
  *   alpha        : finite host value;  eps : finite and > 0   (else MAMBA_ERR_OPTION)
  * An output may be the very buffer of an input of its shape and type.
- * Limits: 0 <= rows < 2^31, 1 <= dim <= 16384 (0 allowed when rows is 0), and rows times the threads
- * of a row (64 up to 512 elements, 256 up to 8192, 512 beyond) below 2^32.  Squares are summed in
+ * Limits: 0 <= rows < 2^31, 1 <= dim <= 16384 (0 allowed when rows is 0), and rows times 64 (up to 768
+ * elements), 128 (up to 1536), 512 (up to 4096) or 1024 (beyond) below 2^31.  Squares are summed in
  * fp32: a row whose squares sum past 3.4e38 normalises to zero.
  */
 int mamba_residual_norm_fwd(int64_t rows, int64_t dim, int io_dtype, int res_dtype, const void* x, const void* gate,

@@ -29,7 +29,7 @@ int check_conv(const char* where, int64_t batch, int64_t seqlen, int64_t dim, in
   if (dim > kMaxDim) return fail(MAMBA_ERR_DIM, where, "dim > 4194304");
   if (seqlen > (int64_t(1) << 40)) return fail(MAMBA_ERR_DIM, where, "seqlen > 2^40");
   if (width < 2 || width > 4) return fail(MAMBA_ERR_UNSUPPORTED, where, "width");
-  if (!s6::conv_fits(batch, seqlen, dim, io)) return fail(MAMBA_ERR_DIM, where, "tensor too large");
+  if (!s6::conv_fits(batch, seqlen, dim)) return fail(MAMBA_ERR_DIM, where, "tensor too large");
   return MAMBA_OK;
 }
 
@@ -46,7 +46,7 @@ int check_ssm(const char* where, int64_t batch, int64_t dim, int64_t dstate, int
   if (dim > kMaxDim) return fail(MAMBA_ERR_DIM, where, "dim > 4194304");
   if (!s6::dstate_supported(dstate)) return fail(MAMBA_ERR_UNSUPPORTED, where, "dstate");
   if (dt_rank < 1 || dt_rank > kMaxRank) return fail(MAMBA_ERR_DIM, where, "dt_rank");
-  if ((batch + 15) / 16 * dim >= (int64_t(1) << 30)) return fail(MAMBA_ERR_DIM, where, "tensor too large");
+  if ((batch + 15) / 16 * dim >= (int64_t(1) << 28)) return fail(MAMBA_ERR_DIM, where, "tensor too large");
   return MAMBA_OK;
 }
 

@@ -565,12 +565,10 @@ hipError_t by_type_and_width(int io, int W, F f) {
 
 }  // namespace
 
-bool conv_fits(int64_t batch, int64_t L, int64_t D, int io) {
-  // a launch counts its threads in 32 bits; the forward has one item more per row than it has chunks
-  const double b = (double)batch, most = 4294967296.0 - kBlock;
-  return b * (double)groups(D, group_fwd(io)) * ((double)plan_fwd(batch, L, D, io).nchunks + 1.0) < most &&
-         b * (double)groups(D, group_bwd(io)) * (double)plan_conv_bwd(batch, L, D, io).nchunks < most &&
-         b * (double)groups(D, group_step(io)) < most;
+bool conv_fits(int64_t batch, int64_t L, int64_t D) {
+  // A launch counts its threads in 32 bits.  A thread has two channels or more, and 32 tokens or more where there
+  // are 2^23 threads of work; the forward has one item more per row than it has chunks.
+  return (double)batch * (double)groups(D, 2) * (double)((L + 31) / 32 + 1) < 2147483648.0;
 }
 
 hipError_t launch_conv_fwd(const ConvArgs& a, int io, hipStream_t s) {

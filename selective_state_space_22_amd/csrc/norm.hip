@@ -643,9 +643,8 @@ hipError_t bwd_types(const NormBwdArgs& b, const NormBwdPlan& p, float* part, hi
 }  // namespace
 
 bool norm_fits(int64_t rows, int64_t D) {
-  bool fits = true;
-  row_shape(D, [&](auto nt, auto) { fits = rows * nt < (int64_t(1) << 32) - 1024; });
-  return fits;
+  // a launch counts its threads in 32 bits; row_shape() has no more threads a row than these
+  return rows * (D <= 768 ? 64 : (D <= 1536 ? 128 : (D <= 4096 ? 512 : 1024))) < (int64_t(1) << 31);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int io, int res, hipStream_t s) {

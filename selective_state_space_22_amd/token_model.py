@@ -6,10 +6,14 @@ One gated recurrent layer between a lookup and the same table's transpose:
 
     x = s E[ids],  y = SiLU(x W_z) scan(x W_u, x W_a, x W_x; lam),  logits = (x + y W_o) E^T.
 
+With ``conv`` taps u goes through the short convolution first, u = SiLU(conv(x W_u)); with ``norms`` the layer
+reads n(x), and the sum is n(x + c n(y W_o)) with a scale c per channel (n: a norm with weights of its own).
+
 Training packs documents into rows (``reset`` marks each one's first token) and takes the gradients
 of mamba_gated_scan_bwd and mamba_embed_bwd through autograd; generation runs the prompt through the
 scan, keeps its last state, and goes on token by token with mamba_gated_state_update and mamba_sample.
-The matrix products are torch's.
+``speculate`` takes tokens that a smaller model drafts where mamba_draft_verify keeps them.  The matrix products
+are torch's.
 """
 from __future__ import annotations
 
@@ -17,6 +21,8 @@ import math
 
 import torch
 
+from .layer import (mamba_conv_bwd, mamba_conv_fwd, mamba_conv_update, mamba_draft_verify, mamba_residual_norm_bwd,
+                    mamba_residual_norm_fwd)
 from .lm import (mamba_embed_bwd, mamba_embed_fwd, mamba_gated_scan_bwd, mamba_gated_scan_fwd,
                  mamba_gated_state_update, mamba_sample)
 
@@ -50,10 +56,40 @@ class _GatedScan(torch.autograd.Function):
         return g["du"], g["dgate_a"], g["dgate_x"], g["dlam"], g["dz"], None
 
 
-class TokenModel(torch.nn.Module):
-    """vocab tokens, width dim; the table and the products in dtype, lam and the states in float32."""
+class _Conv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, reset):
+        ctx.save_for_backward(x, weight, bias, reset)
+        return mamba_conv_fwd(x, weight, bias=bias, reset=reset, return_last_window=False)[0]
 
-    def __init__(self, vocab, dim, dtype=torch.float32, device="cuda", seed=0):
+    @staticmethod
+    def backward(ctx, dout):
+        x, weight, bias, reset = ctx.saved_tensors
+        g = mamba_conv_bwd(x, weight, dout.contiguous(), bias=bias, reset=reset, want=("dbias",))
+        return g["dx"], g["dweight"], g["dbias"], None
+
+
+class _Norm(torch.autograd.Function):
+    """out and residual_out of mamba_residual_norm_fwd(x, pre, post_weight=post, scale=scale, residual=residual)."""
+
+    @staticmethod
+    def forward(ctx, x, pre, post, scale, residual):
+        ctx.save_for_backward(x, pre, post, scale, residual)
+        return mamba_residual_norm_fwd(x, pre, post_weight=post, scale=scale, residual=residual)
+
+    @staticmethod
+    def backward(ctx, dout, dresidual_out):
+        x, pre, post, scale, residual = ctx.saved_tensors
+        g = mamba_residual_norm_bwd(x, pre, dout.contiguous(), dresidual_out=dresidual_out.contiguous(), post_weight=post,
+                                    scale=scale, residual=residual)
+        return tuple(g.get(k) for k in ("dx", "dpre_weight", "dpost_weight", "dscale", "dresidual"))
+
+
+class TokenModel(torch.nn.Module):
+    """vocab tokens, width dim; the table and the products in dtype, lam, the states and what conv and norms
+    bring in float32.  conv: taps of a short convolution before the recurrence (2 to 4, 0: none)."""
+
+    def __init__(self, vocab, dim, dtype=torch.float32, device="cuda", seed=0, conv=0, norms=False):
         super().__init__()
         rng = torch.Generator().manual_seed(seed)
         self.scale = math.sqrt(dim)
@@ -67,6 +103,14 @@ class TokenModel(torch.nn.Module):
         # e^{-8 softplus(lam)} evenly from 0.5 to 0.999: channels of short and of long memory
         kappa = -torch.log(torch.linspace(0.5, 0.999, dim)) / 8
         self.lam = torch.nn.Parameter(torch.log(torch.expm1(kappa)).to(device))
+        self.conv, self.norms = int(conv), bool(norms)
+        if self.conv:
+            taps = (2 * torch.rand((dim, self.conv), generator=rng) - 1) / math.sqrt(self.conv)
+            self.conv_weight = torch.nn.Parameter(taps.to(device))
+            self.conv_bias = torch.nn.Parameter(torch.zeros(dim, device=device))
+        if self.norms:
+            self.norm_in, self.norm_block, self.norm_out, self.norm_scale = (
+                torch.nn.Parameter(torch.ones(dim, device=device)) for _ in range(4))
 
     @staticmethod
     def one_document(ids):
@@ -76,31 +120,50 @@ class TokenModel(torch.nn.Module):
         return reset
 
     def inputs(self, x):
+        if self.norms:
+            x = _Norm.apply(x, self.norm_in, None, None, None)[0]
         return [p.contiguous() for p in (x @ self.w_in).chunk(4, -1)]
+
+    def logits(self, x, y):
+        """From the layer's input and the recurrence's output."""
+        y = y @ self.w_out
+        if self.norms:
+            x = _Norm.apply(y, self.norm_out, self.norm_block, self.norm_scale, x.contiguous())[0]
+        else:
+            x = x + y
+        return x @ self.table.t()
 
     def forward(self, ids, reset=None):
         """Logits (batch, L, vocab) of ids (batch, L); reset as in mamba_gated_scan_fwd, None: one document a row."""
         reset = self.one_document(ids) if reset is None else reset
         x = _Embedding.apply(ids, self.table, self.scale)
         u, a, g, z = self.inputs(x)
+        if self.conv:
+            u = _Conv.apply(u, self.conv_weight, self.conv_bias, reset)
         y = _GatedScan.apply(u, a, g, self.lam, z, reset)
-        return (x + y @ self.w_out) @ self.table.t()
+        return self.logits(x, y)
 
     @torch.no_grad()
     def prefill(self, ids):
-        """The last token's logits (batch, vocab) and the state behind it."""
+        """The last token's logits (batch, vocab) and the state behind it (with conv: and the window)."""
         x = mamba_embed_fwd(ids, self.table, self.scale)
+        reset = self.one_document(ids)
         u, a, g, z = self.inputs(x)
-        y, state = mamba_gated_scan_fwd(u, a, g, self.lam, z=z, reset=self.one_document(ids))
-        return (x[:, -1] + y[:, -1] @ self.w_out) @ self.table.t(), state
+        if self.conv:
+            u, window = mamba_conv_fwd(u, self.conv_weight, bias=self.conv_bias, reset=reset)
+        y, state = mamba_gated_scan_fwd(u, a, g, self.lam, z=z, reset=reset)
+        return self.logits(x[:, -1], y[:, -1]), (state, window) if self.conv else state
 
     @torch.no_grad()
     def step(self, ids, state):
         """Logits (batch, vocab) behind one more token; state is advanced in place."""
         x = mamba_embed_fwd(ids, self.table, self.scale)
         u, a, g, z = self.inputs(x)
+        if self.conv:
+            state, window = state
+            u = mamba_conv_update(window, u, self.conv_weight, bias=self.conv_bias)
         y = mamba_gated_state_update(state, u, a, g, self.lam, z=z)
-        return (x + y @ self.w_out) @ self.table.t()
+        return self.logits(x, y)
 
     @torch.no_grad()
     def generate(self, ids, tokens, generator=None, **filters):
@@ -116,6 +179,51 @@ class TokenModel(torch.nn.Module):
             if left > 1:
                 logits = self.step(out[-1], state)
         return torch.stack(out, 1)
+
+    @torch.no_grad()
+    def speculate(self, ids, rounds, draft, drafts=4, temperature=1.0, generator=None):
+        """ids (batch, L) continued by rounds of up to drafts + 1 tokens, distributed as this model's own: draft (a
+        TokenModel of the same vocabulary) proposes, this one verifies.  Returns a list of tokens per row."""
+        rows, vocab = ids.shape[0], self.table.shape[0]
+        models, place = (self, draft), torch.arange(rows, device=ids.device)
+
+        def probabilities(logits):
+            return torch.softmax(logits.float() / temperature, -1)
+
+        def copy(state):
+            return tuple(t.clone() for t in state) if isinstance(state, tuple) else state.clone()
+
+        def pick(states, kept):  # each row's state behind its kept tokens
+            if isinstance(states[0], tuple):
+                return tuple(torch.stack(part)[kept, place] for part in zip(*states))
+            return torch.stack(states)[kept, place]
+
+        def noise():
+            return torch.empty((rows, vocab), device=ids.device).exponential_(generator=generator)
+
+        said = [[] for _ in range(rows)]
+        logits, state = zip(*(m.prefill(ids) for m in models))
+        p, q = (probabilities(v) for v in logits)
+        for _ in range(rounds):
+            # one entry per drafted token: the probabilities it was drawn from, and the states behind it
+            ps, qs, drawn, states = [p], [], [], ([copy(state[0])], [copy(state[1])])
+            for k in range(drafts):
+                qs.append(q)
+                drawn.append(mamba_sample(torch.log(q), noise(), return_logprob=False)[0])
+                p, q = (probabilities(m.step(drawn[-1], s)) for m, s in zip(models, state))
+                ps.append(p)
+                for kept, s in zip(states, state):
+                    kept.append(copy(s))
+            uniform = torch.rand((rows, drafts), device=ids.device, generator=generator)
+            tokens, accepted = mamba_draft_verify(torch.stack(ps, 1), torch.stack(qs, 1), torch.stack(drawn, 1), uniform,
+                                                  noise())
+            for row, line, n in zip(said, tokens.tolist(), accepted.tolist()):
+                row.extend(line[: n + 1])
+            # the states behind the kept drafts, then the token drawn in the refused one's place
+            state = tuple(pick(kept, accepted.long()) for kept in states)
+            last = tokens.gather(1, accepted.long().unsqueeze(1)).squeeze(1)
+            p, q = (probabilities(m.step(last, s)) for m, s in zip(models, state))
+        return said
 
 
 def batch_of(rng, rows, length, vocab, period):

@@ -169,3 +169,22 @@ def test_binding_refuses_cpu_tensors(lib):
                  lambda: layer.mamba_draft_verify(z(1, 2, 9), z(1, 1, 9), z(1, 1, dtype=torch.int64), z(1, 1), z(1, 9))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_the_limits_that_the_header_states_are_those_of_the_library(lib):
+    text = " ".join(open(HEADER).read().replace("\n *", " ").split())
+    assert "batch * ceil(dim / 2) * (ceil(seqlen / 32) + 1) < 2^31" in text
+    for seqlen, fits in ((32 * ((1 << 20) - 2), True), (32 * ((1 << 20) - 2) + 1, False)):  # 2^10 x 2 x 2^20
+        assert (layer.mamba_conv_bwd_workspace_size(1024, seqlen, 4, 4, 0) > 0) == fits
+        if not fits:
+            assert _call(lib, "conv_fwd", (1024, seqlen, 4, 4, 0)) == ERR_DIM
+    assert "batch * ceil(dim / 2) < 2^30" in text
+    assert _call(lib, "conv_update", (1 << 15, 1 << 16, 4, 0, 1 << 15)) == ERR_DIM
+    assert "ceil(batch / 16) * dim < 2^28" in text
+    for dim, fits in (((1 << 16) - 1, True), (1 << 16, False)):
+        assert (layer.mamba_conv_ssm_update_workspace_size(65535, dim, 16, 8, 0) > 0) == fits
+    assert "64 (up to 768 elements), 128 (up to 1536), 512 (up to 4096) or 1024 (beyond) below 2^31" in text
+    for dim, threads in ((768, 64), (769, 128), (1536, 128), (1537, 512), (4096, 512), (4097, 1024), (16384, 1024)):
+        most = (1 << 31) // threads
+        assert layer.mamba_residual_norm_bwd_workspace_size(most - 1, dim, 0) > 0
+        assert layer.mamba_residual_norm_bwd_workspace_size(most, dim, 0) == 0
