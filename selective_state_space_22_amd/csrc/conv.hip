@@ -47,8 +47,11 @@ struct Item {
   bool in;
 };
 
-// Work item of this thread: channel group fastest (coalesced), then chunk, then batch row.
-template <int V>
+// Work item of this thread: channel group fastest (coalesced), then chunk, then batch row.  WHOLE: the last group
+// of a row that V does not divide begins earlier and shares channels with the one before, which gives them the same
+// values: a group of fewer channels would hold up the waves it falls into (3 x 1537 x 1101 bf16, forward
+// and gradients: 37 us, so 24).
+template <int V, bool WHOLE>
 __device__ __forceinline__ Item item_of(int64_t batch, int64_t nchunks, int64_t D) {
   const int64_t G = (D + V - 1) / V;
   const int64_t id = (int64_t)blockIdx.x * kBlock + threadIdx.x;
@@ -68,7 +71,7 @@ __device__ __forceinline__ Item item_of(int64_t batch, int64_t nchunks, int64_t 
   Item it;
   it.b = b;
   it.chunk = ch;
-  it.d0 = g * V;
+  it.d0 = WHOLE && g * V + V > D ? D - V : g * V;
   it.nv = D - it.d0 < V ? (int)(D - it.d0) : V;
   it.in = b < batch;
   return it;
@@ -231,26 +234,23 @@ __device__ __forceinline__ void conv_chunk(const ConvArgs& a, const Item& it, in
   for (int64_t t = t0 > len ? t0 : len; t < t1; ++t) store_raw<IO, V, FULL>(behind + t * D, raw_t<IO, V>(0u), it.nv);
 }
 
-template <typename IO, int V, int W, bool ACT, bool RESET>
+// FULL: rows of at least V channels.
+template <typename IO, int V, int W, bool ACT, bool RESET, bool FULL>
 __global__ __launch_bounds__(kBlock) void conv_fwd_kernel(ConvArgs a, int64_t nchunks, int64_t chunk) {
   // one more item per (row, channel group) than there are chunks: the window carried on
-  const Item it = item_of<V>(a.batch, nchunks + 1, a.D);
+  const Item it = item_of<V, FULL>(a.batch, nchunks + 1, a.D);
   if (!it.in) return;
   int64_t len = a.L;
   if (a.lengths) {
     const int64_t l = a.lengths[it.b];
     len = l < 0 ? 0 : (l < a.L ? l : a.L);
   }
-  const bool full = it.nv == V;
   if (it.chunk == nchunks) {
-    if (!a.last) return;
-    if (full) conv_tail<IO, V, W, true>(a, it, len);
-    else conv_tail<IO, V, W, false>(a, it, len);
+    if (a.last) conv_tail<IO, V, W, FULL>(a, it, len);
     return;
   }
   const int64_t t0 = it.chunk * chunk, t1 = t0 + chunk < a.L ? t0 + chunk : a.L;
-  if (full) conv_chunk<IO, V, W, ACT, RESET, true>(a, it, t0, t1, len);
-  else conv_chunk<IO, V, W, ACT, RESET, false>(a, it, t0, t1, len);
+  conv_chunk<IO, V, W, ACT, RESET, FULL>(a, it, t0, t1, len);
 }
 
 // ---------------------------------------------------------------- backward
@@ -454,15 +454,14 @@ __device__ __forceinline__ void conv_bwd_chunk(const ConvBwdArgs& a, const Item&
     store_raw<float, V, FULL>(part + j * D + it.d0, narrow<float, V>(j < W ? dw[j < W ? j : 0] : db), it.nv);
 }
 
-template <typename IO, int V, int W, bool ACT, bool RESET>
+template <typename IO, int V, int W, bool ACT, bool RESET, bool FULL>
 __global__ __launch_bounds__(kBlock) void conv_bwd_kernel(ConvBwdArgs a, int64_t nchunks, int64_t chunk,
                                                              float* part) {
-  const Item it = item_of<V>(a.f.batch, nchunks, a.f.D);
+  const Item it = item_of<V, FULL>(a.f.batch, nchunks, a.f.D);
   if (!it.in) return;
   const int64_t t0 = it.chunk * chunk, t1 = t0 + chunk < a.f.L ? t0 + chunk : a.f.L;
   float* p = part + (it.b * nchunks + it.chunk) * (W + 1) * a.f.D;
-  if (it.nv == V) conv_bwd_chunk<IO, V, W, ACT, RESET, true>(a, it, t0, t1, p);
-  else conv_bwd_chunk<IO, V, W, ACT, RESET, false>(a, it, t0, t1, p);
+  conv_bwd_chunk<IO, V, W, ACT, RESET, FULL>(a, it, t0, t1, p);
 }
 
 // dweight and dbias: the part sums of a column (one of (W + 1) D).
@@ -500,7 +499,7 @@ __device__ __forceinline__ void conv_step(const ConvStepArgs& a, const Item& it,
 
 template <typename IO, int V, int W>
 __global__ __launch_bounds__(kBlock) void conv_step_kernel(ConvStepArgs a) {
-  const Item it = item_of<V>(a.batch, 1, a.D);
+  const Item it = item_of<V, false>(a.batch, 1, a.D);
   if (!it.in) return;
   const int64_t slot = a.slots ? a.slots[it.b] : it.b;
   if (slot < 0 || slot >= a.nslots) return;
@@ -533,20 +532,35 @@ unsigned blocks(int64_t batch, int64_t n, int64_t D, int v) {
   return (unsigned)((batch * n * groups(D, v) + kBlock - 1) / kBlock);
 }
 
-template <typename IO, int W, bool ACT>
-void fwd_w(const ConvArgs& a, const ConvPlan& p, unsigned grid, hipStream_t s) {
-  if (a.reset)
-    hipLaunchKernelGGL((conv_fwd_kernel<IO, kGroupFwd<IO>, W, ACT, true>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk);
-  else
-    hipLaunchKernelGGL((conv_fwd_kernel<IO, kGroupFwd<IO>, W, ACT, false>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk);
+template <typename F>
+void by_flags(bool act, bool reset, bool full, F f) {
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (!full) {  // rows of fewer channels than a thread has
+    if (act) reset ? f(Yes(), Yes(), No()) : f(Yes(), No(), No());
+    else reset ? f(No(), Yes(), No()) : f(No(), No(), No());
+  } else {
+    if (act) reset ? f(Yes(), Yes(), Yes()) : f(Yes(), No(), Yes());
+    else reset ? f(No(), Yes(), Yes()) : f(No(), No(), Yes());
+  }
 }
 
-template <typename IO, int W, bool ACT>
+template <typename IO, int W>
+void fwd_w(const ConvArgs& a, const ConvPlan& p, unsigned grid, hipStream_t s) {
+  constexpr int V = kGroupFwd<IO>;
+  by_flags(a.silu, a.reset, a.D >= V, [&](auto act, auto reset, auto full) {
+    hipLaunchKernelGGL((conv_fwd_kernel<IO, V, W, decltype(act)::value, decltype(reset)::value, decltype(full)::value>),
+                       dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk);
+  });
+}
+
+template <typename IO, int W>
 void bwd_w(const ConvBwdArgs& a, const ConvPlan& p, unsigned grid, float* part, hipStream_t s) {
-  if (a.f.reset)
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, kGroupBwd<IO>, W, ACT, true>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk, part);
-  else
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, kGroupBwd<IO>, W, ACT, false>), dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk, part);
+  constexpr int V = kGroupBwd<IO>;
+  by_flags(a.f.silu, a.f.reset, a.f.D >= V, [&](auto act, auto reset, auto full) {
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, V, W, decltype(act)::value, decltype(reset)::value, decltype(full)::value>),
+                       dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk, part);
+  });
 }
 
 template <typename F>
@@ -574,10 +588,7 @@ bool conv_fits(int64_t batch, int64_t L, int64_t D) {
 hipError_t launch_conv_fwd(const ConvArgs& a, int io, hipStream_t s) {
   const ConvPlan p = plan_fwd(a.batch, a.L, a.D, io);
   const unsigned grid = blocks(a.batch, p.nchunks + 1, a.D, group_fwd(io));
-  return by_type_and_width(io, a.W, [&](auto t, auto w) {
-    if (a.silu) fwd_w<decltype(t), decltype(w)::value, true>(a, p, grid, s);
-    else fwd_w<decltype(t), decltype(w)::value, false>(a, p, grid, s);
-  });
+  return by_type_and_width(io, a.W, [&](auto t, auto w) { fwd_w<decltype(t), decltype(w)::value>(a, p, grid, s); });
 }
 
 size_t conv_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int64_t W, int io) {
@@ -591,10 +602,7 @@ hipError_t launch_conv_bwd(const ConvBwdArgs& a, int io, void* workspace, hipStr
   if (f.batch > 0) {
     const unsigned grid = blocks(f.batch, p.nchunks, f.D, group_bwd(io));
     const hipError_t e = by_type_and_width(
-        io, f.W, [&](auto t, auto w) {
-          if (f.silu) bwd_w<decltype(t), decltype(w)::value, true>(a, p, grid, part, s);
-          else bwd_w<decltype(t), decltype(w)::value, false>(a, p, grid, part, s);
-        });
+        io, f.W, [&](auto t, auto w) { bwd_w<decltype(t), decltype(w)::value>(a, p, grid, part, s); });
     if (e != hipSuccess) return e;
   }
   const int64_t cols = (f.W + 1) * f.D;

@@ -62,27 +62,54 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (*lds)[K]) {
   }
 }
 
-// EVEN: D is a multiple of E, chunks are whole or absent.
-template <typename T, bool EVEN>
+// How rows that E does not divide are read.
+enum Rest {
+  kEven,   // E divides D: chunks are whole or absent
+  kShare,  // D >= E: the last chunk begins earlier and shares elements with the one before; both write them, with the
+           // same values, and the sums over the row leave the shared ones out once
+  kParts,  // the last chunk has fewer elements (rows shorter than a chunk; outputs that are inputs, where a shared
+           // element could be read after it was written).  Its waves hold the row up: 4611 x 1101 fp32 with its
+           // gradients 54 us, shared 45
+};
+// First element of the chunk that begins at e0 < D.
+template <int REST>
+__device__ __forceinline__ int64_t begin_of(int64_t e0, int64_t D) {
+  return REST == kShare && e0 + E > D ? D - E : e0;
+}
+template <typename T, int REST>
 __device__ __forceinline__ raw_t<T, E> chunk_in(const T* row, int64_t e0, int64_t D) {
-  if (e0 + E <= D) return load_raw<T, E, true>(row + e0, E);
-  if (!EVEN && e0 < D) return load_raw<T, E, false>(row + e0, (int)(D - e0));
+  if (REST == kShare) {
+    if (e0 < D) return load_raw<T, E, true>(row + begin_of<REST>(e0, D), E);
+  } else {
+    if (e0 + E <= D) return load_raw<T, E, true>(row + e0, E);
+    if (REST == kParts && e0 < D) return load_raw<T, E, false>(row + e0, (int)(D - e0));
+  }
   return raw_t<T, E>(0u);
 }
-template <typename T, bool EVEN>
+template <typename T, int REST>
 __device__ __forceinline__ void chunk_out(T* row, int64_t e0, int64_t D, const float (&f)[E]) {
-  if (e0 + E <= D) store_raw<T, E, true>(row + e0, narrow<T, E>(f), E);
-  else if (!EVEN && e0 < D) store_raw<T, E, false>(row + e0, narrow<T, E>(f), (int)(D - e0));
+  if (REST == kShare) {
+    if (e0 < D) store_raw<T, E, true>(row + begin_of<REST>(e0, D), narrow<T, E>(f), E);
+  } else {
+    if (e0 + E <= D) store_raw<T, E, true>(row + e0, narrow<T, E>(f), E);
+    else if (REST == kParts && e0 < D) store_raw<T, E, false>(row + e0, narrow<T, E>(f), (int)(D - e0));
+  }
 }
-template <bool EVEN>
+template <int REST>
 __device__ __forceinline__ void weights_in(const float* w, int64_t e0, int64_t D, float (&f)[E]) {
-  widen<float, E>(chunk_in<float, EVEN>(w, e0, D), f);
+  widen<float, E>(chunk_in<float, REST>(w, e0, D), f);
+}
+// sum + a b where element i of the chunk at e0 counts in the row's sums, else sum.
+template <int REST>
+__device__ __forceinline__ float count(float a, float b, float sum, int64_t e0, int i, int64_t D) {
+  const float v = __builtin_fmaf(a, b, sum);
+  return REST == kShare && e0 + E > D && i < (int)(e0 + E - D) ? sum : v;
 }
 
 // Rows per workgroup.
 constexpr int rows_of(int nt) { return nt > 128 ? 1 : 256 / nt; }
 
-template <typename IO, typename RES, int NT, int NV, bool EVEN>
+template <typename IO, typename RES, int NT, int NV, int REST>
 __global__ __launch_bounds__(NT* rows_of(NT)) void norm_fwd_kernel(NormArgs a) {
   constexpr int RPB = rows_of(NT);
   __shared__ float lds[NT * RPB / 64][1];
@@ -94,15 +121,15 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_fwd_kernel(NormArgs a) {
   raw_t<IO, E> xr[NV], gr[NV];
   raw_t<RES, E> rr[NV];
 #pragma unroll
-  for (int c = 0; c < NV; ++c) xr[c] = chunk_in<IO, EVEN>(static_cast<const IO*>(a.x) + at, (c * NT + lane) * E, D);
+  for (int c = 0; c < NV; ++c) xr[c] = chunk_in<IO, REST>(static_cast<const IO*>(a.x) + at, (c * NT + lane) * E, D);
   if (a.gate)
 #pragma unroll
     for (int c = 0; c < NV; ++c)
-      gr[c] = chunk_in<IO, EVEN>(static_cast<const IO*>(a.gate) + at, (c * NT + lane) * E, D);
+      gr[c] = chunk_in<IO, REST>(static_cast<const IO*>(a.gate) + at, (c * NT + lane) * E, D);
   if (a.residual)
 #pragma unroll
     for (int c = 0; c < NV; ++c)
-      rr[c] = chunk_in<RES, EVEN>(static_cast<const RES*>(a.residual) + at, (c * NT + lane) * E, D);
+      rr[c] = chunk_in<RES, REST>(static_cast<const RES*>(a.residual) + at, (c * NT + lane) * E, D);
   float v[NV][E];
   float sum[1] = {0.0f};
 #pragma unroll
@@ -115,7 +142,7 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_fwd_kernel(NormArgs a) {
       for (int i = 0; i < E; ++i) v[c][i] *= silu(g[i]);
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) sum[0] = __builtin_fmaf(v[c][i], v[c][i], sum[0]);
+    for (int i = 0; i < E; ++i) sum[0] = count<REST>(v[c][i], v[c][i], sum[0], (c * NT + lane) * E, i, D);
   }
   float k = 1.0f;
   if (a.post) {
@@ -128,7 +155,7 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_fwd_kernel(NormArgs a) {
     const int64_t e0 = (c * NT + lane) * E;
     float w[E];
     if (a.post) {
-      weights_in<EVEN>(a.post, e0, D, w);
+      weights_in<REST>(a.post, e0, D, w);
 #pragma unroll
       for (int i = 0; i < E; ++i) v[c][i] *= k * w[i];
     }
@@ -139,7 +166,7 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_fwd_kernel(NormArgs a) {
       for (int i = 0; i < E; ++i) v[c][i] *= silu(g[i]);
     }
     if (a.scale) {
-      weights_in<EVEN>(a.scale, e0, D, w);
+      weights_in<REST>(a.scale, e0, D, w);
 #pragma unroll
       for (int i = 0; i < E; ++i) v[c][i] *= w[i];
     }
@@ -151,9 +178,9 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < E; ++i) v[c][i] *= a.alpha;
     }
-    if (a.residual_out) chunk_out<RES, EVEN>(static_cast<RES*>(a.residual_out) + at, e0, D, v[c]);
+    if (a.residual_out) chunk_out<RES, REST>(static_cast<RES*>(a.residual_out) + at, e0, D, v[c]);
 #pragma unroll
-    for (int i = 0; i < E; ++i) sum[0] = __builtin_fmaf(v[c][i], v[c][i], sum[0]);
+    for (int i = 0; i < E; ++i) sum[0] = count<REST>(v[c][i], v[c][i], sum[0], (c * NT + lane) * E, i, D);
   }
   if (!a.pre) return;
   row_sum<NT, 1>(sum, lds);
@@ -162,16 +189,16 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_fwd_kernel(NormArgs a) {
   for (int c = 0; c < NV; ++c) {
     const int64_t e0 = (c * NT + lane) * E;
     float w[E];
-    weights_in<EVEN>(a.pre, e0, D, w);
+    weights_in<REST>(a.pre, e0, D, w);
 #pragma unroll
     for (int i = 0; i < E; ++i) w[i] *= v[c][i] * k;
-    chunk_out<IO, EVEN>(static_cast<IO*>(a.out) + at, e0, D, w);
+    chunk_out<IO, REST>(static_cast<IO*>(a.out) + at, e0, D, w);
   }
 }
 
 // Rows blockIdx.x, + gridDim.x, ... of RPB each; the sums over them go to part (gridDim.x, 3, D):
 // dpost, dscale (without alpha), dpre.
-template <typename IO, typename RES, int NT, int NV, bool EVEN>
+template <typename IO, typename RES, int NT, int NV, int REST>
 __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b, float* part) {
   constexpr int RPB = rows_of(NT);
   __shared__ float lds[NT * RPB / 64][2];
@@ -190,9 +217,9 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
       post[c][i] = asc[c][i] = pre[c][i] = 1.0f;
       spost[c][i] = sscale[c][i] = spre[c][i] = 0.0f;
     }
-    if (a.post) weights_in<EVEN>(a.post, e0, a.D, post[c]);
-    if (a.scale) weights_in<EVEN>(a.scale, e0, a.D, asc[c]);
-    if (a.pre) weights_in<EVEN>(a.pre, e0, a.D, pre[c]);
+    if (a.post) weights_in<REST>(a.post, e0, a.D, post[c]);
+    if (a.scale) weights_in<REST>(a.scale, e0, a.D, asc[c]);
+    if (a.pre) weights_in<REST>(a.pre, e0, a.D, pre[c]);
 #pragma unroll
     for (int i = 0; i < E; ++i) asc[c][i] *= a.alpha;
   }
@@ -204,13 +231,13 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int64_t e0 = (c * NT + lane) * E;
-      xr[c] = chunk_in<IO, EVEN>(static_cast<const IO*>(a.x) + at, e0, D);
+      xr[c] = chunk_in<IO, REST>(static_cast<const IO*>(a.x) + at, e0, D);
       gr[c] = dor[c] = raw_t<IO, E>(0u);
       rr[c] = drr[c] = raw_t<RES, E>(0u);
-      if (a.gate) gr[c] = chunk_in<IO, EVEN>(static_cast<const IO*>(a.gate) + at, e0, D);
-      if (a.residual) rr[c] = chunk_in<RES, EVEN>(static_cast<const RES*>(a.residual) + at, e0, D);
-      if (b.dout) dor[c] = chunk_in<IO, EVEN>(static_cast<const IO*>(b.dout) + at, e0, D);
-      if (b.dres_out) drr[c] = chunk_in<RES, EVEN>(static_cast<const RES*>(b.dres_out) + at, e0, D);
+      if (a.gate) gr[c] = chunk_in<IO, REST>(static_cast<const IO*>(a.gate) + at, e0, D);
+      if (a.residual) rr[c] = chunk_in<RES, REST>(static_cast<const RES*>(a.residual) + at, e0, D);
+      if (b.dout) dor[c] = chunk_in<IO, REST>(static_cast<const IO*>(b.dout) + at, e0, D);
+      if (b.dres_out) drr[c] = chunk_in<RES, REST>(static_cast<const RES*>(b.dres_out) + at, e0, D);
     }
     // n = v / rms(v); s = SiLU(gate) and its slope sigma + s (1 - sigma)
     float n[NV][E], s[NV][E], slope[NV][E], s1[1] = {0.0f};
@@ -230,7 +257,7 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
           for (int i = 0; i < E; ++i) n[c][i] *= s[c][i];
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) s1[0] = __builtin_fmaf(n[c][i], n[c][i], s1[0]);
+      for (int i = 0; i < E; ++i) s1[0] = count<REST>(n[c][i], n[c][i], s1[0], (c * NT + lane) * E, i, D);
     }
     float k = 1.0f;
     if (a.post) {
@@ -262,8 +289,8 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
         widen<IO, E>(dor[c], d);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          s2[0] = __builtin_fmaf(r[c][i], r[c][i], s2[0]);
-          s2[1] = __builtin_fmaf(d[i] * pre[c][i], r[c][i], s2[1]);
+          s2[0] = count<REST>(r[c][i], r[c][i], s2[0], (c * NT + lane) * E, i, D);
+          s2[1] = count<REST>(d[i] * pre[c][i], r[c][i], s2[1], (c * NT + lane) * E, i, D);
         }
       }
     }
@@ -289,7 +316,7 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
           dr[i] = __builtin_fmaf(K, __builtin_fmaf(-kk, r[c][i], d[i] * pre[c][i]), dr[i]);
         }
       }
-      if (b.dresidual) chunk_out<RES, EVEN>(static_cast<RES*>(b.dresidual) + at, (c * NT + lane) * E, D, dr);
+      if (b.dresidual) chunk_out<RES, REST>(static_cast<RES*>(b.dresidual) + at, (c * NT + lane) * E, D, dr);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         sscale[c][i] = __builtin_fmaf(dr[i], n[c][i] * f[i], sscale[c][i]);
@@ -299,7 +326,7 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
 #pragma unroll
         for (int i = 0; i < E; ++i) {
           spost[c][i] = __builtin_fmaf(after_gate ? r[c][i] * s[c][i] : r[c][i], n[c][i], spost[c][i]);
-          s1[0] = __builtin_fmaf(r[c][i] * f[i], n[c][i], s1[0]);
+          s1[0] = count<REST>(r[c][i] * f[i], n[c][i], s1[0], (c * NT + lane) * E, i, D);
         }
       }
     }
@@ -328,9 +355,9 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
 #pragma unroll
           for (int i = 0; i < E; ++i) dg[i] = r[c][i] * post[c][i] * n[c][i] * slope[c][i];
         }
-        if (b.dgate) chunk_out<IO, EVEN>(static_cast<IO*>(b.dgate) + at, e0, D, dg);
+        if (b.dgate) chunk_out<IO, REST>(static_cast<IO*>(b.dgate) + at, e0, D, dg);
       }
-      chunk_out<IO, EVEN>(static_cast<IO*>(b.dx) + at, e0, D, dx);
+      chunk_out<IO, REST>(static_cast<IO*>(b.dx) + at, e0, D, dx);
     }
   }
   // the sums of the workgroup's row slots, in their order
@@ -340,9 +367,9 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int64_t e0 = (c * NT + lane) * E;
-      chunk_out<float, EVEN>(out, e0, D, spost[c]);
-      chunk_out<float, EVEN>(out + D, e0, D, sscale[c]);
-      chunk_out<float, EVEN>(out + 2 * D, e0, D, spre[c]);
+      chunk_out<float, REST>(out, e0, D, spost[c]);
+      chunk_out<float, REST>(out + D, e0, D, sscale[c]);
+      chunk_out<float, REST>(out + 2 * D, e0, D, spre[c]);
     }
   } else {
     __shared__ float acc[3][NT * NV * E];
@@ -368,16 +395,16 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
         const int64_t e0 = (c * NT + lane) * E;
-        chunk_out<float, EVEN>(out, e0, D, spost[c]);
-        chunk_out<float, EVEN>(out + D, e0, D, sscale[c]);
-        chunk_out<float, EVEN>(out + 2 * D, e0, D, spre[c]);
+        chunk_out<float, REST>(out, e0, D, spost[c]);
+        chunk_out<float, REST>(out + D, e0, D, sscale[c]);
+        chunk_out<float, REST>(out + 2 * D, e0, D, spre[c]);
       }
   }
 }
 
 // Long rows, whose sums over rows would not fit the registers beside the row: first each row's k, K,
 // K^2 mean(dn' r') and mean(e n) ...
-template <typename IO, typename RES, int NT, int NV, bool EVEN>
+template <typename IO, typename RES, int NT, int NV, int REST>
 __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* stats) {
   static_assert(rows_of(NT) == 1, "a workgroup per row");
   __shared__ float lds[NT / 64][2];
@@ -390,12 +417,12 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
     const int64_t e0 = (c * NT + lane) * E;
-    widen<IO, E>(chunk_in<IO, EVEN>(static_cast<const IO*>(a.x) + at, e0, D), n[c]);
+    widen<IO, E>(chunk_in<IO, REST>(static_cast<const IO*>(a.x) + at, e0, D), n[c]);
 #pragma unroll
     for (int i = 0; i < E; ++i) f[c][i] = 1.0f;
     if (a.gate) {
       float g[E];
-      widen<IO, E>(chunk_in<IO, EVEN>(static_cast<const IO*>(a.gate) + at, e0, D), g);
+      widen<IO, E>(chunk_in<IO, REST>(static_cast<const IO*>(a.gate) + at, e0, D), g);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         if (after_gate) f[c][i] = silu(g[i]);
@@ -403,7 +430,7 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
       }
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) s1[0] = __builtin_fmaf(n[c][i], n[c][i], s1[0]);
+    for (int i = 0; i < E; ++i) s1[0] = count<REST>(n[c][i], n[c][i], s1[0], (c * NT + lane) * E, i, D);
   }
   float k = 1.0f;
   if (a.post) {
@@ -415,7 +442,7 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
     const int64_t e0 = (c * NT + lane) * E;
     float w[E], d[E];
     if (a.post) {
-      weights_in<EVEN>(a.post, e0, D, w);
+      weights_in<REST>(a.post, e0, D, w);
 #pragma unroll
       for (int i = 0; i < E; ++i) f[c][i] *= w[i];
     }
@@ -425,22 +452,22 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
       r[c][i] = a.alpha * n[c][i] * f[c][i];
     }
     if (a.scale) {
-      weights_in<EVEN>(a.scale, e0, D, w);
+      weights_in<REST>(a.scale, e0, D, w);
 #pragma unroll
       for (int i = 0; i < E; ++i) r[c][i] *= w[i];
     }
     if (a.residual) {
-      widen<RES, E>(chunk_in<RES, EVEN>(static_cast<const RES*>(a.residual) + at, e0, D), w);
+      widen<RES, E>(chunk_in<RES, REST>(static_cast<const RES*>(a.residual) + at, e0, D), w);
 #pragma unroll
       for (int i = 0; i < E; ++i) r[c][i] += w[i];
     }
     if (b.dout) {
-      widen<IO, E>(chunk_in<IO, EVEN>(static_cast<const IO*>(b.dout) + at, e0, D), d);
-      weights_in<EVEN>(a.pre, e0, D, w);
+      widen<IO, E>(chunk_in<IO, REST>(static_cast<const IO*>(b.dout) + at, e0, D), d);
+      weights_in<REST>(a.pre, e0, D, w);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        s2[0] = __builtin_fmaf(r[c][i], r[c][i], s2[0]);
-        s2[1] = __builtin_fmaf(d[i] * w[i], r[c][i], s2[1]);
+        s2[0] = count<REST>(r[c][i], r[c][i], s2[0], e0, i, D);
+        s2[1] = count<REST>(d[i] * w[i], r[c][i], s2[1], e0, i, D);
       }
     }
   }
@@ -458,20 +485,20 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
       float dr[E], w[E], d[E];
 #pragma unroll
       for (int i = 0; i < E; ++i) dr[i] = 0.0f;
-      if (b.dres_out) widen<RES, E>(chunk_in<RES, EVEN>(static_cast<const RES*>(b.dres_out) + at, e0, D), dr);
+      if (b.dres_out) widen<RES, E>(chunk_in<RES, REST>(static_cast<const RES*>(b.dres_out) + at, e0, D), dr);
       if (b.dout) {
-        widen<IO, E>(chunk_in<IO, EVEN>(static_cast<const IO*>(b.dout) + at, e0, D), d);
-        weights_in<EVEN>(a.pre, e0, D, w);
+        widen<IO, E>(chunk_in<IO, REST>(static_cast<const IO*>(b.dout) + at, e0, D), d);
+        weights_in<REST>(a.pre, e0, D, w);
 #pragma unroll
         for (int i = 0; i < E; ++i) dr[i] = __builtin_fmaf(K, __builtin_fmaf(-kk, r[c][i], d[i] * w[i]), dr[i]);
       }
       if (a.scale) {
-        weights_in<EVEN>(a.scale, e0, D, w);
+        weights_in<REST>(a.scale, e0, D, w);
 #pragma unroll
         for (int i = 0; i < E; ++i) dr[i] *= w[i];
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) s1[0] = __builtin_fmaf(a.alpha * dr[i] * f[c][i], n[c][i], s1[0]);
+      for (int i = 0; i < E; ++i) s1[0] = count<REST>(a.alpha * dr[i] * f[c][i], n[c][i], s1[0], e0, i, D);
     }
     row_sum<NT, 1>(s1, reinterpret_cast<float(*)[1]>(lds));
   }
@@ -481,7 +508,7 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
 // ... then everything else element by element: a thread has E columns of the rows of its chunk, and their sums.
 constexpr int kColRows = 4;  // row chunks (waves) of a workgroup
 
-template <typename IO, typename RES, bool EVEN>
+template <typename IO, typename RES, int REST>
 __global__ __launch_bounds__(64 * kColRows) void norm_cols_kernel(NormBwdArgs b, const float4* stats, int64_t chunk,
                                                                   float* part) {
   const NormArgs& a = b.f;
@@ -496,20 +523,20 @@ __global__ __launch_bounds__(64 * kColRows) void norm_cols_kernel(NormBwdArgs b,
     post[i] = asc[i] = pre[i] = 1.0f;
     spost[i] = sscale[i] = spre[i] = 0.0f;
   }
-  if (a.post) weights_in<EVEN>(a.post, e0, D, post);
-  if (a.scale) weights_in<EVEN>(a.scale, e0, D, asc);
-  if (a.pre) weights_in<EVEN>(a.pre, e0, D, pre);
+  if (a.post) weights_in<REST>(a.post, e0, D, post);
+  if (a.scale) weights_in<REST>(a.scale, e0, D, asc);
+  if (a.pre) weights_in<REST>(a.pre, e0, D, pre);
 #pragma unroll
   for (int i = 0; i < E; ++i) asc[i] *= a.alpha;
   for (int64_t row = r0; row < r1; ++row) {
     const int64_t at = row * D;
     raw_t<IO, E> gr(0u), dor(0u);
     raw_t<RES, E> rr(0u), drr(0u);
-    const raw_t<IO, E> xr = chunk_in<IO, EVEN>(static_cast<const IO*>(a.x) + at, e0, D);
-    if (a.gate) gr = chunk_in<IO, EVEN>(static_cast<const IO*>(a.gate) + at, e0, D);
-    if (a.residual) rr = chunk_in<RES, EVEN>(static_cast<const RES*>(a.residual) + at, e0, D);
-    if (b.dout) dor = chunk_in<IO, EVEN>(static_cast<const IO*>(b.dout) + at, e0, D);
-    if (b.dres_out) drr = chunk_in<RES, EVEN>(static_cast<const RES*>(b.dres_out) + at, e0, D);
+    const raw_t<IO, E> xr = chunk_in<IO, REST>(static_cast<const IO*>(a.x) + at, e0, D);
+    if (a.gate) gr = chunk_in<IO, REST>(static_cast<const IO*>(a.gate) + at, e0, D);
+    if (a.residual) rr = chunk_in<RES, REST>(static_cast<const RES*>(a.residual) + at, e0, D);
+    if (b.dout) dor = chunk_in<IO, REST>(static_cast<const IO*>(b.dout) + at, e0, D);
+    if (b.dres_out) drr = chunk_in<RES, REST>(static_cast<const RES*>(b.dres_out) + at, e0, D);
     const float4 st = stats[row];  // k, K, K^2 mean(dn' r'), mean(e n)
     float x[E], s[E], slope[E], r[E], d[E], dr[E], dx[E], dg[E];
     widen<IO, E>(xr, x);
@@ -535,14 +562,14 @@ __global__ __launch_bounds__(64 * kColRows) void norm_cols_kernel(NormBwdArgs b,
       dx[i] = first_gate ? dv * s[i] : dv;
       dg[i] = (first_gate ? dv * x[i] : dp * post[i] * n) * slope[i];
     }
-    if (b.dresidual) chunk_out<RES, EVEN>(static_cast<RES*>(b.dresidual) + at, e0, D, dr);
-    if (b.dgate) chunk_out<IO, EVEN>(static_cast<IO*>(b.dgate) + at, e0, D, dg);
-    chunk_out<IO, EVEN>(static_cast<IO*>(b.dx) + at, e0, D, dx);
+    if (b.dresidual) chunk_out<RES, REST>(static_cast<RES*>(b.dresidual) + at, e0, D, dr);
+    if (b.dgate) chunk_out<IO, REST>(static_cast<IO*>(b.dgate) + at, e0, D, dg);
+    chunk_out<IO, REST>(static_cast<IO*>(b.dx) + at, e0, D, dx);
   }
   float* out = part + ch * 3 * D;
-  chunk_out<float, EVEN>(out, e0, D, spost);
-  chunk_out<float, EVEN>(out + D, e0, D, sscale);
-  chunk_out<float, EVEN>(out + 2 * D, e0, D, spre);
+  chunk_out<float, REST>(out, e0, D, spost);
+  chunk_out<float, REST>(out + D, e0, D, sscale);
+  chunk_out<float, REST>(out + 2 * D, e0, D, spre);
 }
 
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64_t rows, int64_t D, float alpha,
@@ -578,13 +605,31 @@ void row_shape(int64_t D, F f) {
 #undef S6_NORM_SHAPE
 }
 
+template <typename F>
+void by_rest(int64_t D, bool in_place, F f) {
+  if (D % E == 0) f(std::integral_constant<int, kEven>());
+  else if (D > E && !in_place) f(std::integral_constant<int, kShare>());
+  else f(std::integral_constant<int, kParts>());
+}
+
+// Whether an output is an input's buffer.
+template <int M, int N>
+bool share(const void* const (&out)[M], const void* const (&in)[N]) {
+  for (const void* o : out)
+    for (const void* i : in)
+      if (o && o == i) return true;
+  return false;
+}
+
 template <typename IO, typename RES>
 hipError_t fwd_types(const NormArgs& a, hipStream_t s) {
+  const bool in_place = share({a.out, a.residual_out}, {a.x, a.gate, a.residual});
   row_shape(a.D, [&](auto nt, auto nv) {
     constexpr int NT = decltype(nt)::value, NV = decltype(nv)::value, RPB = rows_of(NT);
     const dim3 grid((unsigned)((a.rows + RPB - 1) / RPB)), block(NT * RPB);
-    if (a.D % E == 0) hipLaunchKernelGGL((norm_fwd_kernel<IO, RES, NT, NV, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((norm_fwd_kernel<IO, RES, NT, NV, false>), grid, block, 0, s, a);
+    by_rest(a.D, in_place, [&](auto rest) {
+      hipLaunchKernelGGL((norm_fwd_kernel<IO, RES, NT, NV, decltype(rest)::value>), grid, block, 0, s, a);
+    });
   });
   return hipGetLastError();
 }
@@ -619,23 +664,21 @@ NormBwdPlan plan_norm_bwd(int64_t rows, int64_t D) {
 template <typename IO, typename RES>
 hipError_t bwd_types(const NormBwdArgs& b, const NormBwdPlan& p, float* part, hipStream_t s) {
   const int64_t D = b.f.D;
+  const bool in_place = share({b.dx, b.dgate, b.dresidual}, {b.f.x, b.f.gate, b.f.residual, b.dout, b.dres_out});
   row_shape(D, [&](auto nt, auto nv) {
     constexpr int NT = decltype(nt)::value, NV = decltype(nv)::value;
-    if constexpr (NT * NV * E <= kSumsDim) {
-      const dim3 grid((unsigned)p.parts), block(NT * rows_of(NT));
-      if (D % E == 0) hipLaunchKernelGGL((norm_bwd_kernel<IO, RES, NT, NV, true>), grid, block, 0, s, b, part);
-      else hipLaunchKernelGGL((norm_bwd_kernel<IO, RES, NT, NV, false>), grid, block, 0, s, b, part);
-    } else {
-      float4* stats = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(part) + p.off_stats);
-      const dim3 grid((unsigned)((D + 64 * E - 1) / (64 * E)), (unsigned)((p.parts + kColRows - 1) / kColRows));
-      if (D % E == 0) {
-        hipLaunchKernelGGL((norm_stats_kernel<IO, RES, NT, NV, true>), dim3((unsigned)b.f.rows), dim3(NT), 0, s, b, stats);
-        hipLaunchKernelGGL((norm_cols_kernel<IO, RES, true>), grid, dim3(64 * kColRows), 0, s, b, stats, p.chunk, part);
+    by_rest(D, in_place, [&](auto rest) {
+      constexpr int REST = decltype(rest)::value;
+      if constexpr (NT * NV * E <= kSumsDim) {
+        hipLaunchKernelGGL((norm_bwd_kernel<IO, RES, NT, NV, REST>), dim3((unsigned)p.parts), dim3(NT * rows_of(NT)), 0, s,
+                           b, part);
       } else {
-        hipLaunchKernelGGL((norm_stats_kernel<IO, RES, NT, NV, false>), dim3((unsigned)b.f.rows), dim3(NT), 0, s, b, stats);
-        hipLaunchKernelGGL((norm_cols_kernel<IO, RES, false>), grid, dim3(64 * kColRows), 0, s, b, stats, p.chunk, part);
+        float4* stats = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(part) + p.off_stats);
+        const dim3 grid((unsigned)((D + 64 * E - 1) / (64 * E)), (unsigned)((p.parts + kColRows - 1) / kColRows));
+        hipLaunchKernelGGL((norm_stats_kernel<IO, RES, NT, NV, REST>), dim3((unsigned)b.f.rows), dim3(NT), 0, s, b, stats);
+        hipLaunchKernelGGL((norm_cols_kernel<IO, RES, REST>), grid, dim3(64 * kColRows), 0, s, b, stats, p.chunk, part);
       }
-    }
+    });
   });
   return hipGetLastError();
 }

@@ -565,3 +565,15 @@ def test_calls_on_another_stream_and_twice():
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("D", [513, 1101, 4099, 5001])
+def test_an_infinity_in_a_row_that_chunks_share(D):
+    # rms is infinite: what is finite becomes 0, the infinity itself no number
+    import selective_state_space_22_amd as lib
+
+    x = torch.ones((3, D), device="cuda")
+    x[0, D - 1], x[1, D - 3], x[2, 0] = float("inf"), -float("inf"), float("inf")
+    w = torch.ones(D, device="cuda")
+    out, _ = lib.mamba_residual_norm_fwd(x, w, post_weight=None)
+    assert out.isnan().sum(1).tolist() == [1, 1, 1] and not torch.nan_to_num(out).any()
