@@ -131,7 +131,7 @@ int mamba_conv_ssm_update(int64_t batch, int64_t dim, int64_t dstate, int64_t dt
  *   alpha        : finite host value;  eps : finite and > 0   (else MAMBA_ERR_OPTION)
  * An output may be the very buffer of an input of its shape and type.
  * Limits: 0 <= rows < 2^31, 1 <= dim <= 16384 (0 allowed when rows is 0), and rows times 64 (up to 768
- * elements), 128 (up to 1536), 512 (up to 4096) or 1024 (beyond) below 2^31.  Squares are summed in
+ * elements), 192 (up to 1536), 512 (up to 4096) or 1024 (beyond) below 2^31.  Squares are summed in
  * fp32: a row whose squares sum past 3.4e38 normalises to zero.
  */
 int mamba_residual_norm_fwd(int64_t rows, int64_t dim, int io_dtype, int res_dtype, const void* x, const void* gate,

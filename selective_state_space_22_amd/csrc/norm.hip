@@ -596,7 +596,7 @@ void row_shape(int64_t D, F f) {
   else if (D <= 512) S6_NORM_SHAPE(64, 2);
   else if (D <= 768) S6_NORM_SHAPE(64, 3);
   else if (D <= 1024) S6_NORM_SHAPE(128, 2);
-  else if (D <= 1536) S6_NORM_SHAPE(128, 3);
+  else if (D <= 1536) S6_NORM_SHAPE(192, 2);
   else if (D <= 2048) S6_NORM_SHAPE(256, 2);
   else if (D <= 2560) S6_NORM_SHAPE(320, 2);
   else if (D <= 4096) S6_NORM_SHAPE(512, 2);
@@ -646,8 +646,13 @@ struct NormBwdPlan {
 NormBwdPlan plan_norm_bwd(int64_t rows, int64_t D) {
   NormBwdPlan p{0, 0, 0, 0};
   if (D <= kSumsDim) {
-    row_shape(D, [&](auto nt, auto) { p.parts = (rows + rows_of(nt) - 1) / rows_of(nt); });
-    p.parts = p.parts < 1024 ? p.parts : 1024;  // workgroups that fill the chip (768: 48 us, 1024: 44, 1536: 49 at 16384 x 768)
+    row_shape(D, [&](auto nt, auto nv) {
+      // as many workgroups as run at once: with more than one chunk a thread's registers leave two waves per SIMD
+      // (16384 x 768 bf16: 512 workgroups 38 us, 640 53, 768 48, 1024 44)
+      const int64_t most = 256 * (nv == 1 ? 4 : (nt * rows_of(nt) <= 256 ? 2 : 1));
+      p.parts = (rows + rows_of(nt) - 1) / rows_of(nt);
+      p.parts = p.parts < most ? p.parts : most;
+    });
   } else {
     // enough waves for the chip, and at least 16 rows each
     const int64_t waves = (D + 64 * E - 1) / (64 * E);
@@ -687,7 +692,7 @@ hipError_t bwd_types(const NormBwdArgs& b, const NormBwdPlan& p, float* part, hi
 
 bool norm_fits(int64_t rows, int64_t D) {
   // a launch counts its threads in 32 bits; row_shape() has no more threads a row than these
-  return rows * (D <= 768 ? 64 : (D <= 1536 ? 128 : (D <= 4096 ? 512 : 1024))) < (int64_t(1) << 31);
+  return rows * (D <= 768 ? 64 : (D <= 1536 ? 192 : (D <= 4096 ? 512 : 1024))) < (int64_t(1) << 31);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int io, int res, hipStream_t s) {

@@ -183,8 +183,8 @@ def test_the_limits_that_the_header_states_are_those_of_the_library(lib):
     assert "ceil(batch / 16) * dim < 2^28" in text
     for dim, fits in (((1 << 16) - 1, True), (1 << 16, False)):
         assert (layer.mamba_conv_ssm_update_workspace_size(65535, dim, 16, 8, 0) > 0) == fits
-    assert "64 (up to 768 elements), 128 (up to 1536), 512 (up to 4096) or 1024 (beyond) below 2^31" in text
-    for dim, threads in ((768, 64), (769, 128), (1536, 128), (1537, 512), (4096, 512), (4097, 1024), (16384, 1024)):
-        most = (1 << 31) // threads
+    assert "64 (up to 768 elements), 192 (up to 1536), 512 (up to 4096) or 1024 (beyond) below 2^31" in text
+    for dim, threads in ((768, 64), (769, 192), (1536, 192), (1537, 512), (4096, 512), (4097, 1024), (16384, 1024)):
+        most = -(-(1 << 31) // threads)
         assert layer.mamba_residual_norm_bwd_workspace_size(most - 1, dim, 0) > 0
         assert layer.mamba_residual_norm_bwd_workspace_size(most, dim, 0) == 0
