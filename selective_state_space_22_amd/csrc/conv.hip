@@ -29,15 +29,17 @@ constexpr int kGroupBwd = 2;
 template <typename IO>
 constexpr int kGroupStep = sizeof(IO) == 2 ? 2 : 4;
 constexpr int64_t kLeastFwd = 8, kMostFwd = 32, kLeastBwd = 8, kMostBwd = 128;  // tokens per thread
-constexpr int64_t kThreads = 256 * 16 * 64;                                   // threads that fill the chip
+constexpr int64_t kThreads = 256 * 12 * 64;  // threads that run at once (three waves per SIMD)
 
 int64_t groups(int64_t D, int v) { return (D + v - 1) / v; }
 
-// Tokens per thread: as many as leave the chip filled, between `least` and `most`.
+// Tokens per thread, between `least` and `most`: the fewest with which all threads run at once (kThreads), so that
+// no few of them are left for a second round.
 int64_t chunk_of(int64_t batch, int64_t L, int64_t D, int v, int64_t least, int64_t most) {
-  const double t = (double)batch * (double)L * (double)groups(D, v) / (double)kThreads;
-  const int64_t c = t >= (double)most ? most : (int64_t)t / 8 * 8;
-  return c < least ? least : c;
+  const int64_t rows = batch * groups(D, v);  // threads per chunk of the sequence
+  const int64_t n = rows < kThreads ? kThreads / (rows < 1 ? 1 : rows) : 1;
+  const int64_t c = ((L + n - 1) / n + 3) / 4 * 4;
+  return c < least ? least : (c < most ? c : most);
 }
 
 struct Item {

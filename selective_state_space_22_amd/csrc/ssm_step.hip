@@ -257,11 +257,13 @@ struct Lanes {
 
 // sel: (slices, batch, F) part sums of r, B, C; ROWS = kBackRows: joined, one slice.
 template <typename IO, int N, int ROWS>
-__global__ __launch_bounds__(kBack) void ssm_back_kernel(SsmStepArgs a, int tiles, const float* xc, const float* sel,
+__global__ __launch_bounds__(kBack, ROWS == kFewRows ? 1 : 6) void ssm_back_kernel(SsmStepArgs a, int tiles, const float* xc, const float* sel,
                                                              int slices) {
   constexpr int NS = Lanes<N, ROWS>::kStates, LPC = Lanes<N, ROWS>::kPer, RG = Lanes<N, ROWS>::kGroups, RP = Lanes<N, ROWS>::kRowsPer;
   constexpr int CB = kChannels, LD = CB + kPad;
-  constexpr int PRE = 6;  // matrix steps whose weights are loaded ahead
+  // Matrix steps whose weights are loaded ahead.  With few rows that is latency saved; with many it is registers
+  // that other waves need (256 x 5120: 45 us with six steps and two workgroups per CU, 39 with two and three).
+  constexpr int PRE = ROWS == kFewRows ? 6 : 2;
   __shared__ int place[ROWS];
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int RK = (int)((a.R + kStep<IO> - 1) / kStep<IO> * kStep<IO>);
