@@ -15,11 +15,18 @@
 namespace s6 {
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kBlock = 256;            // threads of a row's part
+constexpr int kWide = 1024;            // threads of a row that is a workgroup's alone
 constexpr int V = 4;                   // elements per load
 constexpr int kAhead = 4;              // loads in flight
 constexpr int64_t kPart = 2048;        // fewest elements of a row's part
 constexpr int64_t kFill = 1024;        // workgroups that fill the chip
+// A row that kWide threads read in one round of loads ahead is one workgroup of its own and needs no join, as
+// long as there is a compute unit for each (bf16, 4 drafts: 1 x 8000 in parts 9.2 us a call, alone 7.4; 32 x 12000
+// 8.9, 7.8; beyond the round 1 x 20000 9.3, 10.2 and 32 x 20000 8.8, 11.0; more rows than compute units 1000 x 30000
+// 42, 46).
+constexpr int64_t kAlone = kWide * V * kAhead;
+constexpr int64_t kUnits = 256;
 
 // Ordered bits of a score (larger float, larger integer), then the inverted index; 0: no candidate.
 __device__ __forceinline__ uint64_t key_of(float score, int32_t index) {
@@ -28,6 +35,7 @@ __device__ __forceinline__ uint64_t key_of(float score, int32_t index) {
   return ((uint64_t)o << 32) | (uint32_t)(0xffffffffu - (uint32_t)index);
 }
 
+template <int BLOCK>
 __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* lds) {
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) {
@@ -38,7 +46,7 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* lds) {
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kBlock / 64; ++w) v = lds[w] > v ? lds[w] : v;
+  for (int w = 0; w < BLOCK / 64; ++w) v = lds[w] > v ? lds[w] : v;
   return v;
 }
 
@@ -79,16 +87,16 @@ struct Best {
 };
 
 // The best of elements [lo, hi) of a row, over the workgroup's threads.  q null: weights p.
-template <typename IO>
+template <typename IO, int BLOCK>
 __device__ __forceinline__ uint64_t best_of(const IO* p, const IO* q, const float* noise, int64_t lo, int64_t hi,
                                             uint64_t* lds) {
   Best best;
-  for (int64_t i0 = lo + threadIdx.x * V; i0 < hi; i0 += kBlock * V * kAhead) {
+  for (int64_t i0 = lo + threadIdx.x * V; i0 < hi; i0 += BLOCK * V * kAhead) {
     raw_t<IO, V> rp[kAhead], rq[kAhead];
     raw_t<float, V> rn[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int64_t i = i0 + u * kBlock * V;
+      const int64_t i = i0 + u * BLOCK * V;
       const int nv = hi - i < V ? (int)(hi - i) : V;
       rq[u] = raw_t<IO, V>(0u);
       if (nv == V) {
@@ -108,22 +116,22 @@ __device__ __forceinline__ uint64_t best_of(const IO* p, const IO* q, const floa
       widen<IO, V>(rq[u], fq);
       widen<float, V>(rn[u], fn);
 #pragma unroll
-      for (int k = 0; k < V; ++k) best.offer(fp[k] - fq[k], fn[k], (int32_t)(i0 + u * kBlock * V + k));
+      for (int k = 0; k < V; ++k) best.offer(fp[k] - fq[k], fn[k], (int32_t)(i0 + u * BLOCK * V + k));
     }
   }
-  return block_max(best.key(), lds);
+  return block_max<BLOCK>(best.key(), lds);
 }
 
 // Writes a row's tokens, given the best key of the weights that its drafts leave.
-template <typename IO>
+template <typename IO, int BLOCK>
 __device__ __forceinline__ void finish_row(const VerifyArgs& a, int64_t row, int64_t kept, bool refused, uint64_t key,
                                            uint64_t* lds) {
   if (refused && key == 0) {  // p is nowhere above q: from p itself (a row that rounding alone can make)
-    key = best_of<IO>(static_cast<const IO*>(a.target) + (row * (a.K + 1) + kept) * a.V, static_cast<const IO*>(nullptr),
+    key = best_of<IO, BLOCK>(static_cast<const IO*>(a.target) + (row * (a.K + 1) + kept) * a.V, static_cast<const IO*>(nullptr),
                       a.noise + row * a.V, 0, a.V, lds);
   }
   const int64_t token = key == 0 ? -1 : (int64_t)(0xffffffffu - (uint32_t)key);
-  for (int64_t k = threadIdx.x; k <= a.K; k += kBlock)
+  for (int64_t k = threadIdx.x; k <= a.K; k += BLOCK)
     a.tokens[row * (a.K + 1) + k] = k < kept ? a.drafted[row * a.K + k] : (k == kept ? token : -1);
   if (threadIdx.x == 0) a.accepted[row] = (int32_t)kept;
 }
@@ -134,18 +142,18 @@ __device__ __forceinline__ int64_t count_of(const VerifyArgs& a, int64_t row) {
   return c < 0 ? 0 : (c < a.K ? c : a.K);
 }
 
-template <typename IO>
-__global__ __launch_bounds__(kBlock) void verify_kernel(VerifyArgs a, int parts, int64_t part, uint64_t* keys) {
-  __shared__ uint64_t lds[kBlock / 64];
+template <typename IO, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void verify_kernel(VerifyArgs a, int parts, int64_t part, uint64_t* keys) {
+  __shared__ uint64_t lds[BLOCK / 64];
   const int64_t row = blockIdx.x / (uint32_t)parts;
   const int s = blockIdx.x % (uint32_t)parts;
   const int64_t count = count_of(a, row), kept = kept_drafts<IO>(a, row, count);
   const bool refused = kept < count;
   const int64_t lo = s * part, hi = lo + part < a.V ? lo + part : a.V;
-  const uint64_t key = best_of<IO>(static_cast<const IO*>(a.target) + (row * (a.K + 1) + kept) * a.V,
+  const uint64_t key = best_of<IO, BLOCK>(static_cast<const IO*>(a.target) + (row * (a.K + 1) + kept) * a.V,
                                    refused ? static_cast<const IO*>(a.draft) + (row * a.K + kept) * a.V : nullptr,
                                    a.noise + row * a.V, lo, hi, lds);
-  if (parts == 1) finish_row<IO>(a, row, kept, refused, key, lds);
+  if (parts == 1) finish_row<IO, BLOCK>(a, row, kept, refused, key, lds);
   else if (threadIdx.x == 0) keys[blockIdx.x] = key;
 }
 
@@ -158,12 +166,15 @@ __global__ __launch_bounds__(kBlock) void verify_join_kernel(VerifyArgs a, int p
     const uint64_t k = keys[row * parts + s];
     key = k > key ? k : key;
   }
-  key = block_max(key, lds);
+  key = block_max<kBlock>(key, lds);
   const int64_t count = count_of(a, row), kept = kept_drafts<IO>(a, row, count);
-  finish_row<IO>(a, row, kept, kept < count, key, lds);
+  finish_row<IO, kBlock>(a, row, kept, kept < count, key, lds);
 }
 
+bool alone(int64_t rows, int64_t vocab) { return rows <= kUnits && vocab > kPart && vocab <= kAlone; }
+
 int parts_of(int64_t rows, int64_t vocab) {
+  if (alone(rows, vocab)) return 1;
   int64_t n = (kFill + rows - 1) / (rows < 1 ? 1 : rows);
   const int64_t most = (vocab + kPart - 1) / kPart;
   n = n < most ? n : most;
@@ -174,7 +185,11 @@ template <typename IO>
 hipError_t launch_t(const VerifyArgs& a, uint64_t* keys, hipStream_t s) {
   const int parts = parts_of(a.rows, a.V);
   const int64_t part = ((a.V + parts - 1) / parts + V - 1) / V * V;
-  hipLaunchKernelGGL((verify_kernel<IO>), dim3((unsigned)(a.rows * parts)), dim3(kBlock), 0, s, a, parts, part, keys);
+  if (alone(a.rows, a.V))
+    hipLaunchKernelGGL((verify_kernel<IO, kWide>), dim3((unsigned)a.rows), dim3(kWide), 0, s, a, 1, part, keys);
+  else
+    hipLaunchKernelGGL((verify_kernel<IO, kBlock>), dim3((unsigned)(a.rows * parts)), dim3(kBlock), 0, s, a, parts, part,
+                       keys);
   if (parts > 1)
     hipLaunchKernelGGL((verify_join_kernel<IO>), dim3((unsigned)a.rows), dim3(kBlock), 0, s, a, parts, keys);
   return hipGetLastError();

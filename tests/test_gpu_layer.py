@@ -451,7 +451,8 @@ def _verify_check(c, counts=None):
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,K,V", [(1, 1, 1), (1, 0, 5), (3, 2, 7), (2, 5, 1000), (65, 3, 4099), (1, 4, 50000),
-                                      (2, 70, 33), (1, 130, 9), (4, 3, 2048), (1500, 1, 40)])
+                                      (2, 70, 33), (1, 130, 9), (4, 3, 2048), (1500, 1, 40), (300, 2, 4099),
+                                      (1, 2, 16384), (2, 2, 16385), (256, 1, 2049)])
 def test_verification(rows, K, V, io):
     _verify_check(_verify_case(rows, K, V, io))
 
