@@ -47,6 +47,8 @@ extern "C" {
  *                  where a reset cut them off: the window with which the row goes on
  * Limits: 0 <= batch <= 65535, 0 <= seqlen <= 2^40, 0 <= dim <= 4194304, 2 <= width <= 4
  * (else MAMBA_ERR_UNSUPPORTED), and batch * ceil(dim / 2) * (ceil(seqlen / 32) + 1) < 2^31.
+ * An output that is the very buffer of an input is refused (MAMBA_ERR_OPTION): last_window is
+ * not written over window.
  * seqlen == 0 writes only last_window (= window or zero).
  */
 int mamba_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype, const void* x,
@@ -76,7 +78,7 @@ int mamba_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, in
 /*
  * One token of the convolution for every batch row, in place on the windows.
  *   window       : (nslots, width - 1, dim) I/O type, read and moved on by one token
- *   x, out       : (batch, dim)             I/O type
+ *   x, out       : (batch, dim)             I/O type; out may be x's buffer
  *   slots        : (batch) int32, nullable: row b has window slots[b] (NULL: window b, and
  *                  nslots >= batch).  A negative number, or one of nslots or more, marks an
  *                  idle row: nothing of it is read, its out and every window stay as they
@@ -97,7 +99,8 @@ int mamba_conv_update(int64_t batch, int64_t dim, int64_t width, int io_dtype, i
  * xc, r, B, C and dt in fp32 between them instead of the I/O type.
  *   state        : (nslots, dim, dstate)     float
  *   window       : (nslots, width - 1, dim)  I/O type
- *   x, z, out    : (batch, dim)              I/O type, z nullable (no gate)
+ *   x, z, out    : (batch, dim)              I/O type, z nullable (no gate); out may be the
+ *                  buffer of x or z
  *   conv_weight, conv_bias : (dim, width), (dim) float, conv_bias nullable
  *   W_x          : (dt_rank + 2 * dstate, dim)  I/O type
  *   W_dt         : (dim, dt_rank)            I/O type
@@ -170,8 +173,9 @@ int mamba_residual_norm_bwd(int64_t rows, int64_t dim, int io_dtype, int res_dty
  *     w = max(p_a - q_a, 0) if draft a was refused, or p_a if that is zero everywhere;
  *     w = p_a if all n were kept.
  * With uniforms from [0, 1) and Exp(1) noise, independent, the tokens are distributed as if drawn
- * from the target one by one.  A draft that is no token of the vocabulary is refused.  A NaN
- * probability counts as 0; a noise value of 0 always wins; a negative or NaN one loses against every other.
+ * from the target one by one.  A draft that is no token of the vocabulary is refused, and so is
+ * one whose p or q is NaN; an i where w comes out NaN is not drawn.  A noise value of 0 always
+ * wins; a negative or NaN one loses against every other.
  *   target    : (rows, drafts + 1, vocab) I/O type;  draft : (rows, drafts, vocab) I/O type
  *   drafted   : (rows, drafts) int64;  uniform : (rows, drafts) float;  noise : (rows, vocab) float
  *   counts    : (rows) int32, nullable (drafts; below 0 counts as 0, above drafts as drafts)

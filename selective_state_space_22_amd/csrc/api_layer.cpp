@@ -39,6 +39,15 @@ int check_slots(const char* where, int64_t batch, int64_t nslots, const int32_t*
   return MAMBA_OK;
 }
 
+// An output that is an input's buffer would be read by one thread behind another's write.
+template <int M, int N>
+bool is_one_of(const void* const (&outs)[M], const void* const (&ins)[N]) {
+  for (const void* o : outs)
+    for (const void* i : ins)
+      if (o && o == i) return true;
+  return false;
+}
+
 int check_ssm(const char* where, int64_t batch, int64_t dim, int64_t dstate, int64_t dt_rank, int io) {
   if (!dtype_ok(io)) return fail(MAMBA_ERR_DTYPE, where, "io_dtype");
   if (batch < 0 || dim < 0) return fail(MAMBA_ERR_DIM, where, "negative size");
@@ -114,6 +123,7 @@ int mamba_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, in
   pc.opt(last_window, "last_window");
   if (pc.status != MAMBA_OK) return pc.status;
   if (batch == 0 || dim == 0 || (seqlen == 0 && !last_window)) return MAMBA_OK;
+  if (is_one_of({out, last_window}, {x, window})) return fail(MAMBA_ERR_OPTION, where, "an output is an input's buffer");
   const s6::ConvArgs a{x, weight, bias, window, reset, lengths, out, last_window, batch, seqlen, dim, (int32_t)width,
                        silu != 0};
   const hipError_t e = s6::launch_conv_fwd(a, io_dtype, static_cast<hipStream_t>(stream));
@@ -151,6 +161,8 @@ int mamba_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, in
   if (dim == 0) return MAMBA_OK;
   const size_t need = s6::conv_bwd_ws_bytes(batch, seqlen, dim, width, io_dtype);
   if (need > 0 && (!workspace || workspace_bytes < need)) return fail(MAMBA_ERR_WORKSPACE, where, "workspace");
+  if (is_one_of({dx, dwindow}, {x, window, dout, dlast_window}))
+    return fail(MAMBA_ERR_OPTION, where, "an output is an input's buffer");
   s6::ConvBwdArgs a{};
   a.f = s6::ConvArgs{x, weight, bias, window, reset, nullptr, nullptr, nullptr, batch, seqlen, dim, (int32_t)width,
                      silu != 0};

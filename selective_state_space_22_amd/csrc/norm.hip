@@ -9,10 +9,14 @@
 //     dp = dr alpha scale,   e = dp post [s],   dv = k (e - n mean(e n)),
 //     gate first: dx = dv s, dgate = dv x s'        after: dx = dv, dgate = dp post n s'
 //     dpre = sum dout r' K,   dscale = alpha sum dr p,   dpost = sum dp [s] n.
-// A few dozen operations per element: memory bounds it.  A row stays in the registers of its threads (a wave
-// up to 4096 elements, a workgroup beyond that or where there are few rows), so every tensor is read once and
-// written once; the backward recomputes p and r' from the inputs instead of reading saved ones.  Sums of
-// squares and products are fp32.
+// A few dozen operations per element: memory bounds it.  A row stays in the registers of its threads (part of a
+// wave up to 128 elements, a wave up to 768, a workgroup beyond), so every tensor is read once and written once; the
+// backward recomputes p and r' from the inputs instead of reading saved ones.  Sums of squares and products are
+// fp32.  Measured (a streaming copy reaches 6.1 TB/s):
+//   forward 16384 x 2560 bf16, fp32 residual    115 to 121 us, 587 MB: 5.0 TB/s; bound by memory
+//   forward 16384 x 768 bf16    25 to 30 us, 126 MB: 4.6 TB/s;   4611 x 1101 fp32  16 us, 81 MB: 5.1 TB/s
+//   gradients 16384 x 768 bf16  41 us, 201 MB: 4.9 TB/s;         4611 x 1101 fp32  27 us, 122 MB: 4.5 TB/s
+//   sum over the workgroups' parts 5 us;  one row 1 x 2560 2.6 us: the launch and two sums' latency
 #include <type_traits>
 
 #include "layer_device.h"

@@ -12,10 +12,16 @@
 // dt needs all channels' x_c (three where a tile of rows has many part sums):
 //   front  16 rows x a slice of channels: convolution, then the slice's part of x_c W_x^T on the matrix cores
 //   join   (many rows) the slices' parts of r, B, C added in the order of the slices
-//   back   16 rows x a block of channels: the states' loads are issued first and travel while r W_dt^T is
+//   back   8 rows x a block of channels: the states' loads are issued first and travel while r W_dt^T is
 //          formed on the matrix cores; then the update, four states per lane as in the decode step
 // x_c, r, B, C and dt stay fp32 between: each bf16 matrix operand made of them is split into three bf16 parts
 // (8 + 8 + 8 bits of the 24) whose products are added in fp32, so a token is as exact as in fp32 throughout.
+// (An infinite x_c has no such parts: its row comes out NaN.)
+//
+// Measured, bf16, N = 16, R = 320, W = 4 (a streaming copy reaches 6.1 TB/s):
+//   256 x 5120   front 13 us, join 5, back 39: 186 MB moved, 4.8 TB/s, vector operations 36% of the time; bound by
+//                the states' traffic, the front by the latency of its one round of loads
+//   1 x 5120     front 5.4 us, back 6.9: latency of three dependent rounds of loads
 #include <type_traits>
 
 #include "layer_device.h"
@@ -257,8 +263,8 @@ struct Lanes {
 
 // sel: (slices, batch, F) part sums of r, B, C; ROWS = kBackRows: joined, one slice.
 template <typename IO, int N, int ROWS>
-__global__ __launch_bounds__(kBack, ROWS == kFewRows ? 1 : 6) void ssm_back_kernel(SsmStepArgs a, int tiles, const float* xc, const float* sel,
-                                                             int slices) {
+__global__ __launch_bounds__(kBack, ROWS == kFewRows ? 1 : 6) void ssm_back_kernel(SsmStepArgs a, int tiles, const float* xc,
+                                                                                   const float* sel, int slices) {
   constexpr int NS = Lanes<N, ROWS>::kStates, LPC = Lanes<N, ROWS>::kPer, RG = Lanes<N, ROWS>::kGroups, RP = Lanes<N, ROWS>::kRowsPer;
   constexpr int CB = kChannels, LD = CB + kPad;
   // Matrix steps whose weights are loaded ahead.  With few rows that is latency saved; with many it is registers

