@@ -18,7 +18,7 @@
 // (8 + 8 + 8 bits of the 24) whose products are added in fp32, so a token is as exact as in fp32 throughout.
 // (An infinite x_c has no such parts: its row comes out NaN.)
 //
-// Measured, bf16, N = 16, R = 320, W = 4 (a streaming copy reaches 6.1 TB/s):
+// Measured, bf16, N = 16, R = 160, W = 4 (a streaming copy reaches 6.1 TB/s):
 //   256 x 5120   front 13 us, join 5, back 39: 186 MB moved, 4.8 TB/s, vector operations 36% of the time; bound by
 //                the states' traffic, the front by the latency of its one round of loads
 //   1 x 5120     front 5.4 us, back 6.9: latency of three dependent rounds of loads
