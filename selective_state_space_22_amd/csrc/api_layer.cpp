@@ -133,7 +133,7 @@ int mamba_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, in
 
 size_t mamba_conv_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype) {
   if (check_conv("mamba_conv_bwd_workspace_size", batch, seqlen, dim, width, io_dtype) != MAMBA_OK) return 0;
-  return s6::conv_bwd_ws_bytes(batch, seqlen, dim, width, io_dtype);
+  return s6::conv_bwd_ws_bytes(batch, seqlen, dim, width);
 }
 
 int mamba_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype, const void* x,
@@ -159,7 +159,7 @@ int mamba_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, in
   pc.opt(workspace, "workspace");
   if (pc.status != MAMBA_OK) return pc.status;
   if (dim == 0) return MAMBA_OK;
-  const size_t need = s6::conv_bwd_ws_bytes(batch, seqlen, dim, width, io_dtype);
+  const size_t need = s6::conv_bwd_ws_bytes(batch, seqlen, dim, width);
   if (need > 0 && (!workspace || workspace_bytes < need)) return fail(MAMBA_ERR_WORKSPACE, where, "workspace");
   if (is_one_of({dx, dwindow}, {x, window, dout, dlast_window}))
     return fail(MAMBA_ERR_OPTION, where, "an output is an input's buffer");

@@ -6,14 +6,14 @@
 // where x at negative t is the carried window.  Backward, with dc_t = dout_t SiLU'(c_t):
 //     dx_t = sum_{o <= age_{t+o}} weight_{W-1-o} dc_{t+o},   dweight_{W-1-o} = sum dc_t x_{t-o},   dbias = sum dc_t.
 //
-// A thread owns two or four channels and walks a chunk of tokens with the taps in registers: every input is loaded
+// A thread owns two channels and walks a chunk of tokens with the taps in registers: every input is loaded
 // once (and W - 1 rows again per chunk) in coalesced loads, the next tile of four tokens in flight while one is
 // computed.  Chunks are as short as lets all threads run at once: a token needs what its neighbours load, but no
 // order among chunks.  Measured (a streaming copy reaches 6.1 TB/s; bytes as the formulas need them):
 //   forward 4 x 4096 x 5120 bf16, rows three quarters full   49 us, 294 MB: 6.0 TB/s; bound by memory
 //   forward 8 x 2048 x 1536 bf16, resets   26 us, 101 MB: 3.9 TB/s; 22 vector operations an element, half of the time
 //   gradients of the same                  41 us, 151 MB: 3.7 TB/s; 40 vector operations an element, 61% of the time
-//   3 x 1537 x 1101 fp32                   11 us, 41 MB: 3.7 TB/s; gradients 15 us, 61 MB: 4.2 TB/s (read 30% more
+//   3 x 1537 x 1101 fp32                   12 us, 41 MB: 3.4 TB/s; gradients 14 us, 61 MB: 4.4 TB/s (read 30% more
 //                                          than that: three tokens beside every chunk of eight)
 //   sum over the chunks' parts             4 to 5 us, a launch and its latency
 //   one token 256 x 5120 bf16              6 us, 21 MB: 3.5 TB/s; latency of one round of loads
@@ -29,22 +29,18 @@ constexpr int kBlock = 256;
 // Tokens of a tile: its loads are in flight together while the tile before it is computed.
 constexpr int kTile = 4;
 constexpr int kTileBwd = 4;
-// Channels per thread.
-template <typename IO>
-constexpr int kGroupFwd = sizeof(IO) == 2 ? 2 : 4;
-template <typename IO>
-constexpr int kGroupBwd = 2;
-template <typename IO>
-constexpr int kGroupStep = sizeof(IO) == 2 ? 2 : 4;
+// Channels per thread (two, four: forward 4 x 4096 x 5120 bf16 68, 69 us and fp32 137, 138; forward and gradients
+// 8 x 2048 x 1536 bf16 65, 72 and fp32 106, 118; step 256 x 5120 bf16 5.3, 5.6 and fp32 8.3, 8.1).
+constexpr int kGroup = 2;
 constexpr int64_t kLeastFwd = 8, kMostFwd = 32, kLeastBwd = 8, kMostBwd = 128;  // tokens per thread
 constexpr int64_t kThreads = 256 * 12 * 64;  // threads that run at once (three waves per SIMD)
 
-int64_t groups(int64_t D, int v) { return (D + v - 1) / v; }
+int64_t groups(int64_t D) { return (D + kGroup - 1) / kGroup; }
 
 // Tokens per thread, between `least` and `most`: the fewest with which all threads run at once (kThreads), so that
 // no few of them are left for a second round.
-int64_t chunk_of(int64_t batch, int64_t L, int64_t D, int v, int64_t least, int64_t most) {
-  const int64_t rows = batch * groups(D, v);  // threads per chunk of the sequence
+int64_t chunk_of(int64_t batch, int64_t L, int64_t D, int64_t least, int64_t most) {
+  const int64_t rows = batch * groups(D);  // threads per chunk of the sequence
   const int64_t n = rows < kThreads ? kThreads / (rows < 1 ? 1 : rows) : 1;
   const int64_t c = ((L + n - 1) / n + 3) / 4 * 4;
   return c < least ? least : (c < most ? c : most);
@@ -523,23 +519,19 @@ struct ConvPlan {
   int64_t chunk, nchunks;
 };
 
-int group_fwd(int io) { return io == kIoBF16 ? kGroupFwd<uint16_t> : kGroupFwd<float>; }
-int group_bwd(int io) { return io == kIoBF16 ? kGroupBwd<uint16_t> : kGroupBwd<float>; }
-int group_step(int io) { return io == kIoBF16 ? kGroupStep<uint16_t> : kGroupStep<float>; }
-
-ConvPlan plan_fwd(int64_t batch, int64_t L, int64_t D, int io) {
-  const int64_t c = chunk_of(batch, L, D, group_fwd(io), kLeastFwd, kMostFwd);
+ConvPlan plan_fwd(int64_t batch, int64_t L, int64_t D) {
+  const int64_t c = chunk_of(batch, L, D, kLeastFwd, kMostFwd);
   return {c, (L + c - 1) / c};
 }
 
-ConvPlan plan_conv_bwd(int64_t batch, int64_t L, int64_t D, int io) {
-  const int64_t c = chunk_of(batch, L, D, group_bwd(io), kLeastBwd, kMostBwd);
+ConvPlan plan_conv_bwd(int64_t batch, int64_t L, int64_t D) {
+  const int64_t c = chunk_of(batch, L, D, kLeastBwd, kMostBwd);
   const int64_t n = (L + c - 1) / c;
   return {c, n < 1 ? 1 : n};  // a sequence of no tokens still hands dlast_window on
 }
 
-unsigned blocks(int64_t batch, int64_t n, int64_t D, int v) {
-  return (unsigned)((batch * n * groups(D, v) + kBlock - 1) / kBlock);
+unsigned blocks(int64_t batch, int64_t n, int64_t D) {
+  return (unsigned)((batch * n * groups(D) + kBlock - 1) / kBlock);
 }
 
 template <typename F>
@@ -557,7 +549,7 @@ void by_flags(bool act, bool reset, bool full, F f) {
 
 template <typename IO, int W>
 void fwd_w(const ConvArgs& a, const ConvPlan& p, unsigned grid, hipStream_t s) {
-  constexpr int V = kGroupFwd<IO>;
+  constexpr int V = kGroup;
   by_flags(a.silu, a.reset, a.D >= V, [&](auto act, auto reset, auto full) {
     hipLaunchKernelGGL((conv_fwd_kernel<IO, V, W, decltype(act)::value, decltype(reset)::value, decltype(full)::value>),
                        dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk);
@@ -566,7 +558,7 @@ void fwd_w(const ConvArgs& a, const ConvPlan& p, unsigned grid, hipStream_t s) {
 
 template <typename IO, int W>
 void bwd_w(const ConvBwdArgs& a, const ConvPlan& p, unsigned grid, float* part, hipStream_t s) {
-  constexpr int V = kGroupBwd<IO>;
+  constexpr int V = kGroup;
   by_flags(a.f.silu, a.f.reset, a.f.D >= V, [&](auto act, auto reset, auto full) {
     hipLaunchKernelGGL((conv_bwd_kernel<IO, V, W, decltype(act)::value, decltype(reset)::value, decltype(full)::value>),
                        dim3(grid), dim3(kBlock), 0, s, a, p.nchunks, p.chunk, part);
@@ -590,27 +582,27 @@ hipError_t by_type_and_width(int io, int W, F f) {
 }  // namespace
 
 bool conv_fits(int64_t batch, int64_t L, int64_t D) {
-  // A launch counts its threads in 32 bits.  A thread has two channels or more, and fewer than 32 tokens only where
+  // A launch counts its threads in 32 bits.  A thread has two channels, and fewer than 32 tokens only where
   // that makes no more than kThreads of them; the forward has one item more per row than it has chunks.
-  return (double)batch * (double)groups(D, 2) * (double)((L + 31) / 32 + 1) < 2147483648.0;
+  return (double)batch * (double)groups(D) * (double)((L + 31) / 32 + 1) < 2147483648.0;
 }
 
 hipError_t launch_conv_fwd(const ConvArgs& a, int io, hipStream_t s) {
-  const ConvPlan p = plan_fwd(a.batch, a.L, a.D, io);
-  const unsigned grid = blocks(a.batch, p.nchunks + 1, a.D, group_fwd(io));
+  const ConvPlan p = plan_fwd(a.batch, a.L, a.D);
+  const unsigned grid = blocks(a.batch, p.nchunks + 1, a.D);
   return by_type_and_width(io, a.W, [&](auto t, auto w) { fwd_w<decltype(t), decltype(w)::value>(a, p, grid, s); });
 }
 
-size_t conv_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int64_t W, int io) {
-  return (size_t)batch * (size_t)plan_conv_bwd(batch, L, D, io).nchunks * (size_t)(W + 1) * (size_t)D * sizeof(float);
+size_t conv_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int64_t W) {
+  return (size_t)batch * (size_t)plan_conv_bwd(batch, L, D).nchunks * (size_t)(W + 1) * (size_t)D * sizeof(float);
 }
 
 hipError_t launch_conv_bwd(const ConvBwdArgs& a, int io, void* workspace, hipStream_t s) {
   const ConvArgs& f = a.f;
-  const ConvPlan p = plan_conv_bwd(f.batch, f.L, f.D, io);
+  const ConvPlan p = plan_conv_bwd(f.batch, f.L, f.D);
   float* part = static_cast<float*>(workspace);
   if (f.batch > 0) {
-    const unsigned grid = blocks(f.batch, p.nchunks, f.D, group_bwd(io));
+    const unsigned grid = blocks(f.batch, p.nchunks, f.D);
     const hipError_t e = by_type_and_width(
         io, f.W, [&](auto t, auto w) { bwd_w<decltype(t), decltype(w)::value>(a, p, grid, part, s); });
     if (e != hipSuccess) return e;
@@ -622,10 +614,10 @@ hipError_t launch_conv_bwd(const ConvBwdArgs& a, int io, void* workspace, hipStr
 }
 
 hipError_t launch_conv_step(const ConvStepArgs& a, int io, hipStream_t s) {
-  const unsigned grid = blocks(a.batch, 1, a.D, group_step(io));
+  const unsigned grid = blocks(a.batch, 1, a.D);
   return by_type_and_width(io, a.W, [&](auto t, auto w) {
     using T = decltype(t);
-    hipLaunchKernelGGL((conv_step_kernel<T, kGroupStep<T>, decltype(w)::value>), dim3(grid), dim3(kBlock), 0, s, a);
+    hipLaunchKernelGGL((conv_step_kernel<T, kGroup, decltype(w)::value>), dim3(grid), dim3(kBlock), 0, s, a);
   });
 }
 

@@ -48,7 +48,7 @@ struct ConvStepArgs {
 
 bool conv_fits(int64_t batch, int64_t L, int64_t D);  // false: more work items than a launch can count
 hipError_t launch_conv_fwd(const ConvArgs& a, int io, hipStream_t stream);
-size_t conv_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int64_t W, int io);
+size_t conv_bwd_ws_bytes(int64_t batch, int64_t L, int64_t D, int64_t W);
 hipError_t launch_conv_bwd(const ConvBwdArgs& a, int io, void* workspace, hipStream_t stream);
 hipError_t launch_conv_step(const ConvStepArgs& a, int io, hipStream_t stream);
 

@@ -638,7 +638,8 @@ hipError_t fwd_types(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows up to here keep the sums over rows beside the row.
+// Rows up to here keep the sums over rows beside the row; beyond, those do not fit its registers (forward and gradients
+// 2048 x 4096: 56 us bf16 and 92 fp32 so, 67 and 120 in two passes; 2048 x 8192 bf16: 327 us so, 197 in two passes).
 constexpr int64_t kSumsDim = 4096;
 
 struct NormBwdPlan {

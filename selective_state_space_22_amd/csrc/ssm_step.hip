@@ -250,7 +250,10 @@ __global__ __launch_bounds__(kBlock) void ssm_join_kernel(const float* part, int
 
 constexpr int kChannels = 128;        // channels of a back workgroup
 constexpr int kBack = 4 * kChannels;  // its threads: four lanes per channel at N = 16
-constexpr int kFewRows = 4;           // up to these, the back adds the slices itself
+// Up to these, the back adds the slices itself, once per workgroup, instead of a launch that does it for all (D 5120:
+// 2 rows 11.9 us so, 14.1 with the launch; 4 rows 13.8, 15.4; a tile of 7 rows has 6 rows in 15.6, with the launch 16.1,
+// but 1 to 4 rows 0.4 later).
+constexpr int kFewRows = 4;
 constexpr int kBackRows = 8;          // batch rows of its tile otherwise (at most the matrix instruction's 16)
 
 template <int N, int ROWS>

@@ -22,7 +22,7 @@ constexpr int kWide = 1024;            // threads of a row that is a workgroup's
 constexpr int V = 4;                   // elements per load
 constexpr int kAhead = 4;              // loads in flight
 constexpr int64_t kPart = 2048;        // fewest elements of a row's part
-constexpr int64_t kFill = 1024;        // workgroups that fill the chip
+constexpr int64_t kFill = 1024;        // workgroups that fill the chip (64 x 128000: 512 20.4 us, 1024 19.1, 2048 20.7)
 // A row that kWide threads read in one round of loads ahead is one workgroup of its own and needs no join, as
 // long as there is a compute unit for each (bf16, 4 drafts: 1 x 8000 in parts 9.2 us a call, alone 7.4; 32 x 12000
 // 8.9, 7.8; beyond the round 1 x 20000 9.3, 10.2 and 32 x 20000 8.8, 11.0; more rows than compute units 1000 x 30000
