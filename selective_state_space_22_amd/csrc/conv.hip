@@ -471,11 +471,12 @@ __global__ __launch_bounds__(kBlock) void conv_bwd_kernel(ConvBwdArgs a, int64_t
 }
 
 // dweight and dbias: the part sums of a column (one of (W + 1) D).
+template <int C>
 __global__ __launch_bounds__(1024) void conv_sum_kernel(const float* part, int64_t rows, int64_t D, int W,
                                                         float* dweight, float* dbias) {
-  const int64_t col = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31), cols = (W + 1) * D;
-  const float v = column_sum(part, rows, cols, col);
-  if (threadIdx.x >= 32 || col >= cols) return;
+  const int64_t col = (int64_t)blockIdx.x * C + threadIdx.x % C, cols = (W + 1) * D;
+  const float v = column_sum<C>(part, rows, cols, col);
+  if (threadIdx.x >= C || col >= cols) return;
   const int64_t j = col / D, d = col % D;
   if (j < W) dweight[d * W + j] = v;
   else if (dbias) dbias[d] = v;
@@ -608,8 +609,11 @@ hipError_t launch_conv_bwd(const ConvBwdArgs& a, int io, void* workspace, hipStr
     if (e != hipSuccess) return e;
   }
   const int64_t cols = (f.W + 1) * f.D;
-  hipLaunchKernelGGL(conv_sum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, s, part, f.batch * p.nchunks,
-                     f.D, f.W, a.dweight, a.dbias);
+  by_columns(cols, [&](auto c) {
+    constexpr int C = decltype(c)::value;
+    hipLaunchKernelGGL((conv_sum_kernel<C>), dim3((unsigned)((cols + C - 1) / C)), dim3(1024), 0, s, part,
+                       f.batch * p.nchunks, f.D, f.W, a.dweight, a.dbias);
+  });
   return hipGetLastError();
 }
 

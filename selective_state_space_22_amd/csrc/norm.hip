@@ -417,16 +417,27 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
   const int64_t D = a.D, row = blockIdx.x, at = row * D;
   const float inv = 1.0f / (float)D;
   const bool after_gate = a.gate && !a.gate_first;
+  raw_t<IO, E> xr[NV], gr[NV], dor[NV];
+  raw_t<RES, E> rr[NV], drr[NV];
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    const int64_t e0 = (c * NT + lane) * E;
+    xr[c] = chunk_in<IO, REST>(static_cast<const IO*>(a.x) + at, e0, D);
+    if (a.gate) gr[c] = chunk_in<IO, REST>(static_cast<const IO*>(a.gate) + at, e0, D);
+    if (a.residual) rr[c] = chunk_in<RES, REST>(static_cast<const RES*>(a.residual) + at, e0, D);
+    if (b.dout) dor[c] = chunk_in<IO, REST>(static_cast<const IO*>(b.dout) + at, e0, D);
+    if (b.dres_out) drr[c] = chunk_in<RES, REST>(static_cast<const RES*>(b.dres_out) + at, e0, D);
+  }
   float n[NV][E], f[NV][E], r[NV][E], s1[1] = {0.0f}, s2[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
     const int64_t e0 = (c * NT + lane) * E;
-    widen<IO, E>(chunk_in<IO, REST>(static_cast<const IO*>(a.x) + at, e0, D), n[c]);
+    widen<IO, E>(xr[c], n[c]);
 #pragma unroll
     for (int i = 0; i < E; ++i) f[c][i] = 1.0f;
     if (a.gate) {
       float g[E];
-      widen<IO, E>(chunk_in<IO, REST>(static_cast<const IO*>(a.gate) + at, e0, D), g);
+      widen<IO, E>(gr[c], g);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         if (after_gate) f[c][i] = silu(g[i]);
@@ -461,12 +472,12 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
       for (int i = 0; i < E; ++i) r[c][i] *= w[i];
     }
     if (a.residual) {
-      widen<RES, E>(chunk_in<RES, REST>(static_cast<const RES*>(a.residual) + at, e0, D), w);
+      widen<RES, E>(rr[c], w);
 #pragma unroll
       for (int i = 0; i < E; ++i) r[c][i] += w[i];
     }
     if (b.dout) {
-      widen<IO, E>(chunk_in<IO, REST>(static_cast<const IO*>(b.dout) + at, e0, D), d);
+      widen<IO, E>(dor[c], d);
       weights_in<REST>(a.pre, e0, D, w);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
@@ -489,9 +500,9 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
       float dr[E], w[E], d[E];
 #pragma unroll
       for (int i = 0; i < E; ++i) dr[i] = 0.0f;
-      if (b.dres_out) widen<RES, E>(chunk_in<RES, REST>(static_cast<const RES*>(b.dres_out) + at, e0, D), dr);
+      if (b.dres_out) widen<RES, E>(drr[c], dr);
       if (b.dout) {
-        widen<IO, E>(chunk_in<IO, REST>(static_cast<const IO*>(b.dout) + at, e0, D), d);
+        widen<IO, E>(dor[c], d);
         weights_in<REST>(a.pre, e0, D, w);
 #pragma unroll
         for (int i = 0; i < E; ++i) dr[i] = __builtin_fmaf(K, __builtin_fmaf(-kk, r[c][i], d[i] * w[i]), dr[i]);
@@ -576,11 +587,12 @@ __global__ __launch_bounds__(64 * kColRows) void norm_cols_kernel(NormBwdArgs b,
   chunk_out<float, REST>(out + 2 * D, e0, D, spre);
 }
 
+template <int C>
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64_t rows, int64_t D, float alpha,
                                                         float* dpost, float* dscale, float* dpre) {
-  const int64_t col = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-  const float v = column_sum(part, rows, 3 * D, col);
-  if (threadIdx.x >= 32 || col >= 3 * D) return;
+  const int64_t col = (int64_t)blockIdx.x * C + threadIdx.x % C;
+  const float v = column_sum<C>(part, rows, 3 * D, col);
+  if (threadIdx.x >= C || col >= 3 * D) return;
   if (col < D) {
     if (dpost) dpost[col] = v;
   } else if (col < 2 * D) {
@@ -590,7 +602,8 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64
   }
 }
 
-// Threads and chunks per thread of a row.
+// Threads and chunks per thread of a row: about as many threads as it has chunks of two, since idle ones take a part of the
+// workgroup's registers (forward and gradients of 1892 x 4576 bf16: 640 threads 63 us, 1024 75; 512 with four chunks 65).
 template <typename F>
 void row_shape(int64_t D, F f) {
 #define S6_NORM_SHAPE(nt, nv) f(std::integral_constant<int, nt>(), std::integral_constant<int, nv>())
@@ -604,6 +617,8 @@ void row_shape(int64_t D, F f) {
   else if (D <= 2048) S6_NORM_SHAPE(256, 2);
   else if (D <= 2560) S6_NORM_SHAPE(320, 2);
   else if (D <= 4096) S6_NORM_SHAPE(512, 2);
+  else if (D <= 5120) S6_NORM_SHAPE(640, 2);
+  else if (D <= 6144) S6_NORM_SHAPE(768, 2);
   else if (D <= 8192) S6_NORM_SHAPE(1024, 2);
   else S6_NORM_SHAPE(1024, 4);
 #undef S6_NORM_SHAPE
@@ -719,8 +734,11 @@ hipError_t launch_norm_bwd(const NormBwdArgs& b, int io, int res, void* workspac
       e = bwd_types<float, float>(b, p, part, s);
   }
   if (e != hipSuccess || !(b.dpost || b.dscale || b.dpre)) return e;
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((3 * D + 31) / 32)), dim3(1024), 0, s, part, p.parts, D,
-                     b.f.alpha, b.dpost, b.dscale, b.dpre);
+  by_columns(3 * D, [&](auto c) {
+    constexpr int C = decltype(c)::value;
+    hipLaunchKernelGGL((norm_sum_kernel<C>), dim3((unsigned)((3 * D + C - 1) / C)), dim3(1024), 0, s, part, p.parts, D,
+                       b.f.alpha, b.dpost, b.dscale, b.dpre);
+  });
   return hipGetLastError();
 }
 

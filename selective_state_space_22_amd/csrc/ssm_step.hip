@@ -12,7 +12,7 @@
 // dt needs all channels' x_c (three where a tile of rows has many part sums):
 //   front  16 rows x a slice of channels: convolution, then the slice's part of x_c W_x^T on the matrix cores
 //   join   (many rows) the slices' parts of r, B, C added in the order of the slices
-//   back   8 rows x a block of channels: the states' loads are issued first and travel while r W_dt^T is
+//   back   4 or 8 rows x a block of channels: the states' loads are issued first and travel while r W_dt^T is
 //          formed on the matrix cores; then the update, four states per lane as in the decode step
 // x_c, r, B, C and dt stay fp32 between: each bf16 matrix operand made of them is split into three bf16 parts
 // (8 + 8 + 8 bits of the 24) whose products are added in fp32, so a token is as exact as in fp32 throughout.
@@ -264,7 +264,7 @@ struct Lanes {
   static constexpr int kRowsPer = (ROWS + kGroups - 1) / kGroups;  // rows per lane
 };
 
-// sel: (slices, batch, F) part sums of r, B, C; ROWS = kBackRows: joined, one slice.
+// sel: (slices, batch, F) part sums of r, B, C, or joined, one slice: always so with kBackRows.
 template <typename IO, int N, int ROWS>
 __global__ __launch_bounds__(kBack, ROWS == kFewRows ? 1 : 6) void ssm_back_kernel(SsmStepArgs a, int tiles, const float* xc,
                                                                                    const float* sel, int slices) {
@@ -423,7 +423,7 @@ __global__ __launch_bounds__(kBack, ROWS == kFewRows ? 1 : 6) void ssm_back_kern
 
 struct StepPlan {
   int tiles, back_tiles, slices;
-  bool join;
+  bool join, few;
   size_t off_part, off_sel, bytes;
 };
 
@@ -435,6 +435,11 @@ StepPlan plan_step(int64_t batch, int64_t D, int64_t N, int64_t R) {
   // every back workgroup adds its rows' parts again: cheaper than a launch while they are few
   p.join = batch > kFewRows;
   p.back_tiles = p.join ? (int)((batch + kBackRows - 1) / kBackRows) : 1;
+  // Tiles of few rows also where each then has a compute unit of its own (D 5120: 8 rows 15.6 us so, 16.9 in the larger
+  // tile; 16 rows 17.2, 18.7; beyond, 36 x 4768 28.9, 22.7).
+  const int few_tiles = (int)((batch + kFewRows - 1) / kFewRows);
+  p.few = !p.join || few_tiles * ((D + kChannels - 1) / kChannels) <= 256;
+  if (p.few) p.back_tiles = few_tiles;
   auto al = [](size_t v) { return (v + 255) / 256 * 256; };
   p.off_part = al((size_t)batch * D * 4);
   p.off_sel = p.off_part + al((size_t)p.slices * batch * F * 4);
@@ -475,7 +480,7 @@ hipError_t launch_t(const SsmStepArgs& a, const StepPlan& p, uint8_t* ws, hipStr
   }
   auto go = [&](auto n) {
     constexpr int N = decltype(n)::value;
-    return p.join ? back<IO, N, kBackRows>(a, p, xc, sel, slices, s) : back<IO, N, kFewRows>(a, p, xc, sel, slices, s);
+    return p.few ? back<IO, N, kFewRows>(a, p, xc, sel, slices, s) : back<IO, N, kBackRows>(a, p, xc, sel, slices, s);
   };
   switch (a.N) {
     case 1: return go(std::integral_constant<int, 1>());

@@ -46,7 +46,7 @@ def i32(a):
 
 # rows of one element, of a group and a bit, odd ones; sequences shorter than the taps, of a chunk and a bit
 CONV_SHAPES = [(1, 1, 1), (2, 3, 5), (3, 17, 64), (2, 70, 130), (1, 203, 259), (2, 1, 8), (4, 129, 12), (5, 8, 3),
-               (1, 600, 36)]
+               (1, 600, 36), (2, 40, 700), (2, 4500, 9)]
 
 
 def _conv_case(shape, W, io, flags, seed=0):
@@ -189,7 +189,9 @@ def test_convolution_update_with_slots(io):
 # whose errors add like independent ones: 2 sqrt(dim) 2^-24 for dim up to 768 is 3.3e-6, thrice (r, dt, B C)
 STEP_TOL = 3e-5
 STEP_SHAPES = [(1, 1, 1, 1), (3, 8, 2, 3), (2, 60, 4, 24), (5, 130, 8, 33), (4, 259, 16, 8), (17, 64, 16, 32),
-               (33, 300, 16, 17), (1, 768, 16, 24), (16, 128, 4, 160), (18, 520, 2, 512)]
+               (33, 300, 16, 17), (1, 768, 16, 24), (16, 128, 4, 160), (18, 520, 2, 512),
+               # tiles of eight rows
+               (131, 1030, 16, 33), (517, 130, 4, 24), (1030, 8, 8, 3), (1029, 60, 2, 5), (1027, 5, 1, 2)]
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
@@ -277,7 +279,7 @@ def test_one_token(shape, W, io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
-@pytest.mark.parametrize("shape", [(1, 40, 16, 5), (21, 200, 16, 24), (6, 70, 2, 8)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 40, 16, 5), (21, 200, 16, 24), (6, 70, 2, 8), (517, 130, 16, 40)], ids=str)
 def test_one_token_with_slots(shape, io):
     batch, D, N, R = shape
     rng, c = _step_case(shape, 4, io, seed=1)
@@ -331,7 +333,7 @@ def test_one_token_with_a_zero_state_matrix_and_a_held_state():
 # ------------------------------------------------------------------------------------------ norms
 
 NORM_SHAPES = [(1, 1), (3, 7), (5, 64), (2, 511), (4, 512), (3, 513), (9, 776), (2, 1101), (3, 2050), (2, 2560),
-               (1, 4095), (2, 5000), (1, 8192), (2, 12001), (1, 16384)]
+               (1, 4095), (2, 4097), (2, 5000), (3, 5121), (2, 6144), (2, 6145), (1, 8192), (2, 12001), (1, 16384)]
 NORM_FLAGS = ["", "p", "gPsrp", "aPsrp", "gr", "aPp", "sr", "gsrp"]
 
 
@@ -394,7 +396,7 @@ def test_norm_gradients(shape, flags, io, res):
         assert ref.close(host(got[k]), v, m, "bf16" if got[k].dtype == torch.bfloat16 else "f32") <= 1, k
 
 
-@pytest.mark.parametrize("rows,D", [(2049, 40), (2500, 520), (4097, 1101), (2100, 2560), (2048, 4096)])
+@pytest.mark.parametrize("rows,D", [(2049, 40), (2500, 520), (4097, 1101), (2100, 2560), (2048, 4096), (300, 4609), (70, 5124), (40, 6147)])
 def test_norm_of_many_rows_is_that_of_few(rows, D):
     import selective_state_space_22_amd as lib
 
