@@ -183,7 +183,7 @@ __device__ __forceinline__ void conv_chunk(const ConvArgs& a, const Item& it, in
   IO* out = static_cast<IO*>(a.out) + (it.b * a.L + t0) * D + it.d0;
   const IO* x = static_cast<const IO*>(a.x) + (it.b * a.L + t0) * D + it.d0;
   const uint8_t* reset = RESET ? a.reset + it.b * a.L + t0 : nullptr;
-  const int n = (int)((t1 < len ? t1 : len) - t0);  // tokens of the chunk that exist
+  const int n = chunk_tokens(t0, t1, len);
   if (n > 0) {
     float w[W][V], bias[V], row[W - 1 + T][V];  // row: the W - 1 inputs before the tile, then the tile
     load_weights<V, W, FULL>(a.weight, a.bias, it.d0, it.nv, w, bias);

@@ -12,6 +12,13 @@ namespace s6 {
 
 // ---------------------------------------------------------------- short convolution (conv.hip)
 
+// Tokens of the chunk [t0, t1) that a row of len tokens has.  Clamped in 64 bits: the row may end more than 2^31
+// tokens before the chunk.
+__host__ __device__ constexpr int chunk_tokens(int64_t t0, int64_t t1, int64_t len) {
+  const int64_t n = (t1 < len ? t1 : len) - t0;
+  return n > 0 ? (int)n : 0;
+}
+
 struct ConvArgs {
   const void* x;
   const float* weight;     // (D, W)
