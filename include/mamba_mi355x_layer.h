@@ -49,7 +49,7 @@ extern "C" {
  * (else MAMBA_ERR_UNSUPPORTED), and batch * ceil(dim / 2) * (ceil(seqlen / 32) + 1) < 2^31.
  * An output that is the very buffer of an input is refused (MAMBA_ERR_OPTION): last_window is
  * not written over window.
- * seqlen == 0 writes only last_window (= window or zero).
+ * seqlen == 0 writes only last_window (= window or zero), and needs no x, weight and out.
  */
 int mamba_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype, const void* x,
                    const float* weight, const float* bias, const void* window, const uint8_t* reset,
@@ -67,7 +67,8 @@ int mamba_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, in
  *   dbias        : (dim)                    float, nullable
  *   dwindow      : (batch, width - 1, dim)  I/O type, nullable; defined also when window is NULL
  *   workspace    : mamba_conv_bwd_workspace_size() bytes of scratch
- * Limits as for the forward.  seqlen == 0 writes dweight = dbias = 0 and dwindow = dlast_window (or 0).
+ * Limits as for the forward.  seqlen == 0 writes dweight = dbias = 0 and dwindow = dlast_window (or 0), and
+ * needs no x, weight, dout and dx.
  */
 size_t mamba_conv_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype);
 int mamba_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype, const void* x,

@@ -528,7 +528,7 @@ ConvPlan plan_fwd(int64_t batch, int64_t L, int64_t D) {
 ConvPlan plan_conv_bwd(int64_t batch, int64_t L, int64_t D) {
   const int64_t c = chunk_of(batch, L, D, kLeastBwd, kMostBwd);
   const int64_t n = (L + c - 1) / c;
-  return {c, n < 1 ? 1 : n};  // a sequence of no tokens still hands dlast_window on
+  return {c, n < 1 ? 1 : n};
 }
 
 unsigned blocks(int64_t batch, int64_t n, int64_t D) {
@@ -602,7 +602,20 @@ hipError_t launch_conv_bwd(const ConvBwdArgs& a, int io, void* workspace, hipStr
   const ConvArgs& f = a.f;
   const ConvPlan p = plan_conv_bwd(f.batch, f.L, f.D);
   float* part = static_cast<float*>(workspace);
-  if (f.batch > 0) {
+  const int64_t rows = f.L > 0 ? f.batch * p.nchunks : 0;  // of part sums
+  if (f.L == 0) {
+    // no tokens: what the forward did was to hand the window on, and so does dlast_window go; no weight is read
+    if (f.batch > 0 && a.dwindow) {
+      ConvArgs copy{};
+      copy.window = a.dlast;
+      copy.last = a.dwindow;
+      copy.batch = f.batch;
+      copy.D = f.D;
+      copy.W = f.W;
+      const hipError_t e = launch_conv_fwd(copy, io, s);
+      if (e != hipSuccess) return e;
+    }
+  } else if (f.batch > 0) {
     const unsigned grid = blocks(f.batch, p.nchunks, f.D);
     const hipError_t e = by_type_and_width(
         io, f.W, [&](auto t, auto w) { bwd_w<decltype(t), decltype(w)::value>(a, p, grid, part, s); });
@@ -611,8 +624,8 @@ hipError_t launch_conv_bwd(const ConvBwdArgs& a, int io, void* workspace, hipStr
   const int64_t cols = (f.W + 1) * f.D;
   by_columns(cols, [&](auto c) {
     constexpr int C = decltype(c)::value;
-    hipLaunchKernelGGL((conv_sum_kernel<C>), dim3((unsigned)((cols + C - 1) / C)), dim3(1024), 0, s, part,
-                       f.batch * p.nchunks, f.D, f.W, a.dweight, a.dbias);
+    hipLaunchKernelGGL((conv_sum_kernel<C>), dim3((unsigned)((cols + C - 1) / C)), dim3(1024), 0, s, part, rows,
+                       f.D, f.W, a.dweight, a.dbias);
   });
   return hipGetLastError();
 }

@@ -45,3 +45,26 @@ def test_a_length_in_a_row_of_more_than_2_31_tokens(cut, length):
         assert torch.equal(out[:, at], part)
     assert torch.equal(last, plast)
     assert torch.count_nonzero(out[:, length:]) == 0
+
+
+@pytest.mark.parametrize("dtype,io", [(torch.float32, 0), (BF, 1)])
+def test_gradients_of_no_tokens_read_no_weight(dtype, io):
+    import selective_state_space_22_amd as lib
+    from selective_state_space_22_amd import layer
+
+    batch, D, W = 3, 37, 4
+    dlast, bad = _randn(batch, W - 1, D, dtype=dtype), torch.full((D, W), float("nan"), device="cuda")
+    x = torch.empty((batch, 0, D), device="cuda", dtype=dtype)
+    for given in (dlast, None):
+        g = lib.mamba_conv_bwd(x, bad, x, bias=bad[:, 0].contiguous(), dlast_window=given)
+        assert torch.equal(g["dwindow"], torch.zeros_like(dlast) if given is None else dlast)
+        assert not g["dweight"].any() and not g["dbias"].any()
+    # through the C ABI with no weight at all
+    dweight, dbias, dwindow = torch.ones((D, W), device="cuda"), torch.ones(D, device="cuda"), torch.ones_like(dlast)
+    need = lib.mamba_conv_bwd_workspace_size(batch, 0, D, W, io)
+    ws = torch.empty(max(need, 1), device="cuda", dtype=torch.uint8)
+    assert layer._lib().mamba_conv_bwd(
+        batch, 0, D, W, io, None, None, None, None, None, 1, None, dlast.data_ptr(), None, dweight.data_ptr(),
+        dbias.data_ptr(), dwindow.data_ptr(), ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(dwindow, dlast) and not dweight.any() and not dbias.any()
