@@ -72,21 +72,31 @@ def _run(cmd: list[str], verbose: bool) -> None:
         raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd[-3:])}")
 
 
+def _build_bind(verbose: bool) -> None:
+    _run(bind_command(BIND + ".tmp"), verbose)
+    os.replace(BIND + ".tmp", BIND)
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source to an object (in parallel), then link the library.
-    Every call compiles every source."""
+    Every call compiles every source.  The library needs no torch: without it the module _layer, which only
+    torch programs load, is left out; where it fails for another reason the library is in place when this raises."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     objs = [os.path.join(OBJ_DIR, os.path.splitext(s)[0] + ".o") for s in SOURCES]
     jobs = max(1, min(len(SOURCES), int(os.environ.get("MAX_JOBS", os.cpu_count() or 1))))
     with ThreadPoolExecutor(max_workers=jobs) as pool:
-        bind = pool.submit(_run, bind_command(BIND + ".tmp"), verbose)
+        bind = pool.submit(_build_bind, verbose)
         list(pool.map(lambda so: _run(compile_command(os.path.join(CSRC, so[0]), so[1]), verbose),
                       zip(SOURCES, objs)))
-        bind.result()
-    tmp = LIB + ".tmp"
-    _run(link_command(objs, tmp), verbose)
-    os.replace(tmp, LIB)
-    os.replace(BIND + ".tmp", BIND)
+        tmp = LIB + ".tmp"
+        _run(link_command(objs, tmp), verbose)
+        os.replace(tmp, LIB)
+        try:
+            bind.result()
+        except ImportError as e:
+            sys.stderr.write(f"{os.path.basename(BIND)} was not built: {e}\n")
+        except Exception as e:
+            raise RuntimeError(f"{LIB} is built, {os.path.basename(BIND)} is not: {e}") from e
     return LIB
 
 
