@@ -568,8 +568,10 @@ __global__ __launch_bounds__(64 * kColRows) void norm_cols_kernel(NormBwdArgs b,
       const float f = after_gate ? post[i] * s[i] : post[i];
       const float q = n * f;
       r[i] = __builtin_fmaf(asc[i], q, r[i]);
-      spre[i] = __builtin_fmaf(d[i], r[i] * st.y, spre[i]);
-      dr[i] = __builtin_fmaf(st.y, __builtin_fmaf(-st.z, r[i], d[i] * pre[i]), dr[i]);
+      if (b.dout) {  // else r' reaches no gradient, also where it is no number
+        spre[i] = __builtin_fmaf(d[i], r[i] * st.y, spre[i]);
+        dr[i] = __builtin_fmaf(st.y, __builtin_fmaf(-st.z, r[i], d[i] * pre[i]), dr[i]);
+      }
       sscale[i] = __builtin_fmaf(dr[i], q, sscale[i]);
       const float dp = dr[i] * asc[i];
       spost[i] = __builtin_fmaf(after_gate ? dp * s[i] : dp, n, spost[i]);

@@ -68,3 +68,21 @@ def test_gradients_of_no_tokens_read_no_weight(dtype, io):
         dbias.data_ptr(), dwindow.data_ptr(), ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert torch.equal(dwindow, dlast) and not dweight.any() and not dbias.any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("D", [64, 1101, 4096, 4099, 16384])
+def test_a_residual_that_no_norm_reads_reaches_no_gradient(D, bad):
+    import selective_state_space_22_amd as lib
+
+    x, dres, gate, w = (_randn(3, D, seed=s) for s in range(4))
+    residual = _randn(3, D, seed=5)
+    dirty = residual.clone()
+    dirty[1, D // 2], dirty[2, D - 1] = bad, bad
+    for kw in ({}, {"post_weight": w[0].clone()}, {"gate": gate, "scale": w[1].clone()},
+               {"gate": gate, "gate_first": False, "post_weight": w[0].clone(), "scale": w[1].clone()}):
+        want = lib.mamba_residual_norm_bwd(x, dresidual_out=dres, residual=residual, **kw)
+        got = lib.mamba_residual_norm_bwd(x, dresidual_out=dres, residual=dirty, **kw)
+        assert sorted(got) == sorted(want)
+        for k in want:
+            assert torch.equal(got[k], want[k]), k
