@@ -345,7 +345,10 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
       float dx[E], dg[E], f[E];
       factor(c, f);
 #pragma unroll
-      for (int i = 0; i < E; ++i) dx[i] = k * __builtin_fmaf(-n[c][i], m, r[c][i] * f[i]);
+      for (int i = 0; i < E; ++i) dx[i] = r[c][i] * f[i];
+      if (a.post)  // else x itself reaches no gradient of its own, also where it is no number
+#pragma unroll
+        for (int i = 0; i < E; ++i) dx[i] = k * __builtin_fmaf(-n[c][i], m, dx[i]);
       if (a.gate) {
         if (first_gate) {
           float x[E];
@@ -575,7 +578,8 @@ __global__ __launch_bounds__(64 * kColRows) void norm_cols_kernel(NormBwdArgs b,
       sscale[i] = __builtin_fmaf(dr[i], q, sscale[i]);
       const float dp = dr[i] * asc[i];
       spost[i] = __builtin_fmaf(after_gate ? dp * s[i] : dp, n, spost[i]);
-      const float dv = st.x * __builtin_fmaf(-n, st.w, dp * f);
+      float dv = dp * f;
+      if (a.post) dv = st.x * __builtin_fmaf(-n, st.w, dv);
       dx[i] = first_gate ? dv * s[i] : dv;
       dg[i] = (first_gate ? dv * x[i] : dp * post[i] * n) * slope[i];
     }

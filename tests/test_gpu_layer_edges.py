@@ -86,3 +86,22 @@ def test_a_residual_that_no_norm_reads_reaches_no_gradient(D, bad):
         assert sorted(got) == sorted(want)
         for k in want:
             assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("D", [64, 768, 1101, 4096, 4099, 16384])
+def test_a_block_that_no_norm_reads_does_not_reach_its_own_gradient(D, bad):
+    # p = x SiLU(gate): dx = dr alpha scale SiLU(gate) has no x in it
+    import selective_state_space_22_amd as lib
+
+    x, dres, gate, w = (_randn(3, D, seed=s) for s in range(4))
+    dirty = x.clone()
+    dirty[1, D // 2], dirty[2, D - 1] = bad, bad
+    for kw in ({}, {"gate": gate}, {"gate": gate, "gate_first": False, "scale": w[1].clone()}):
+        want = lib.mamba_residual_norm_bwd(x, dresidual_out=dres, alpha=0.7, **kw)
+        got = lib.mamba_residual_norm_bwd(dirty, dresidual_out=dres, alpha=0.7, **kw)
+        assert torch.equal(got["dx"], want["dx"]), list(kw)
+        for k in ("dgate", "dscale"):  # these do hold x: only where it is no number
+            if k in want:
+                same = torch.isfinite(dirty) if k == "dgate" else torch.isfinite(dirty).all(0)
+                assert torch.equal(got[k][same], want[k][same]) and not torch.isfinite(got[k][~same]).any(), k
