@@ -302,7 +302,7 @@ __global__ __launch_bounds__(NT* rows_of(NT)) void norm_bwd_kernel(NormBwdArgs b
     if (b.dout) {
       row_sum<NT, 2>(s2, lds);
       K = rsqrtf(__builtin_fmaf(s2[0], inv, a.eps));
-      kk = K * K * (s2[1] * inv);
+      kk = K * (K * (s2[1] * inv));  // K * K alone may overflow
     }
     // dr, the sums over rows, dp (kept in r) and mean(e n), e = dp f
     s1[0] = 0.0f;
@@ -493,7 +493,7 @@ __global__ __launch_bounds__(NT) void norm_stats_kernel(NormBwdArgs b, float4* s
   if (b.dout) {
     row_sum<NT, 2>(s2, lds);
     K = rsqrtf(__builtin_fmaf(s2[0], inv, a.eps));
-    kk = K * K * (s2[1] * inv);
+    kk = K * (K * (s2[1] * inv));
   }
   s1[0] = 0.0f;
   if (a.post) {

@@ -1,5 +1,8 @@
 """The layer operators where lengths, pointers and values are out of the ordinary."""
+import numpy as np
 import pytest
+
+import layer_ref as ref
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -105,3 +108,22 @@ def test_a_block_that_no_norm_reads_does_not_reach_its_own_gradient(D, bad):
             if k in want:
                 same = torch.isfinite(dirty) if k == "dgate" else torch.isfinite(dirty).all(0)
                 assert torch.equal(got[k][same], want[k][same]) and not torch.isfinite(got[k][~same]).any(), k
+
+
+@pytest.mark.parametrize("eps", [1e-38, 1e-40, 1e-44])
+@pytest.mark.parametrize("D", [64, 768, 1101, 4099])
+def test_norm_gradients_of_zero_rows_at_the_smallest_eps(D, eps):
+    # 1 / rms is 1e19 to 1e22: its square is past the range of fp32, the gradients are not
+    import selective_state_space_22_amd as lib
+
+    eps = float(np.float32(eps))
+    x, pre, post = np.zeros((3, D)), np.full(D, 1.5), np.full(D, 0.5)
+    dout = np.asarray(np.random.default_rng(D).normal(size=(3, D)) * 1e-20, np.float32).astype(float)
+    dout[0] = 0
+    on = lambda a: torch.from_numpy(a).float().cuda()  # noqa: E731
+    for kw in ({}, {"post": post}):
+        want = ref.norm_bwd(x, pre, dout, eps=eps, **kw)
+        got = lib.mamba_residual_norm_bwd(on(x), on(pre), on(dout), eps=eps, **{k + "_weight": on(v) for k, v in kw.items()})
+        assert sorted(got) == sorted(want)
+        for k, (v, m) in want.items():
+            assert ref.close(got[k].double().cpu().numpy(), v, m, "f32") <= 1, k
