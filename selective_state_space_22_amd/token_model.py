@@ -183,12 +183,18 @@ class TokenModel(torch.nn.Module):
     @torch.no_grad()
     def speculate(self, ids, rounds, draft, drafts=4, temperature=1.0, generator=None):
         """ids (batch, L) continued by rounds of up to drafts + 1 tokens, distributed as this model's own: draft (a
-        TokenModel of the same vocabulary) proposes, this one verifies.  Returns a list of tokens per row."""
+        TokenModel of the same vocabulary) proposes, this one verifies.  temperature as for generate, for both.
+        Returns a list of tokens per row.  An example of the rule: this model too steps through every draft, one
+        by one, so that no time is saved over generate."""
         rows, vocab = ids.shape[0], self.table.shape[0]
         models, place = (self, draft), torch.arange(rows, device=ids.device)
 
         def probabilities(logits):
-            return torch.softmax(logits.float() / temperature, -1)
+            v = logits.float()
+            if not temperature > 0:  # as in mamba_sample: greedy
+                return torch.nn.functional.one_hot(v.argmax(-1), vocab).float()
+            v = v - v.amax(-1, keepdim=True)  # at most 0: what a small temperature makes infinite has no weight
+            return torch.softmax(torch.where(v == 0, v, v / temperature), -1)
 
         def copy(state):
             return tuple(t.clone() for t in state) if isinstance(state, tuple) else state.clone()
