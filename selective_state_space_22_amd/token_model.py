@@ -221,8 +221,9 @@ class TokenModel(torch.nn.Module):
                 for kept, s in zip(states, state):
                     kept.append(copy(s))
             uniform = torch.rand((rows, drafts), device=ids.device, generator=generator)
-            tokens, accepted = mamba_draft_verify(torch.stack(ps, 1), torch.stack(qs, 1), torch.stack(drawn, 1), uniform,
-                                                  noise())
+            q_all = torch.stack(qs, 1) if qs else p.new_empty((rows, 0, vocab))
+            ids_all = torch.stack(drawn, 1) if qs else ids.new_empty((rows, 0))
+            tokens, accepted = mamba_draft_verify(torch.stack(ps, 1), q_all, ids_all, uniform, noise())
             for row, line, n in zip(said, tokens.tolist(), accepted.tolist()):
                 row.extend(line[: n + 1])
             # the states behind the kept drafts, then the token drawn in the refused one's place

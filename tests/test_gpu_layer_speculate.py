@@ -26,3 +26,12 @@ def test_no_temperature_is_greedy(temperature):
     said = model.speculate(ids, 4, draft, drafts=2, temperature=temperature, generator=torch.Generator("cuda").manual_seed(1))
     for got, line in zip(said, want):
         assert 4 <= len(got) <= 12 and got == line[:len(got)]
+
+
+def test_rounds_of_no_drafts_are_a_token_each():
+    model, draft, ids = _models()
+    want = model.generate(ids, 5, top_k=1).tolist()
+    assert model.speculate(ids, 5, draft, drafts=0, temperature=0.0) == want
+    assert model.speculate(ids, 0, draft) == [[]] * 4
+    said = model.speculate(ids, 3, draft, drafts=0, generator=torch.Generator("cuda").manual_seed(1))
+    assert [len(r) for r in said] == [3] * 4 and all(0 <= t < 30 for r in said for t in r)
