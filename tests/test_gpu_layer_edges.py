@@ -127,3 +127,95 @@ def test_norm_gradients_of_zero_rows_at_the_smallest_eps(D, eps):
         assert sorted(got) == sorted(want)
         for k, (v, m) in want.items():
             assert ref.close(got[k].double().cpu().numpy(), v, m, "f32") <= 1, k
+
+
+@pytest.mark.parametrize("D", [4097, 5000, 6144, 16383])
+def test_norm_of_long_rows_in_place(D):
+    import selective_state_space_22_amd as lib
+
+    x, gate, res, dout, dres = (_randn(37, D, dtype=BF, seed=s) for s in range(5))
+    pre, post, scale = (_randn(D, seed=s) for s in range(3))
+    args = {"gate": gate, "post_weight": post, "scale": scale}
+    out, r = lib.mamba_residual_norm_fwd(x, pre, residual=res, **args)
+    g = lib.mamba_residual_norm_bwd(x, pre, dout, dresidual_out=dres, residual=res, **args)
+    x2, res2 = x.clone(), res.clone()
+    lib.mamba_residual_norm_fwd(x2, pre, residual=res2, out=res2, residual_out=x2, **args)
+    assert torch.equal(res2, out) and torch.equal(x2, r)
+    x3, gate3, dres3 = x.clone(), gate.clone(), dres.clone()
+    got = lib.mamba_residual_norm_bwd(x3, pre, dout, dresidual_out=dres3, residual=res, **{**args, "gate": gate3},
+                                      grads={"dx": gate3, "dgate": x3, "dresidual": dres3})
+    for k, v in g.items():
+        assert torch.equal(got[k], v), k
+
+
+def _token(batch, D, N, R, W, dtype, places=None, seed=0):
+    """The arguments of mamba_conv_ssm_update."""
+    places = batch if places is None else places
+    return {"state": _randn(places, D, N, seed=seed), "window": _randn(places, W - 1, D, dtype=dtype, seed=seed + 1),
+            "x": _randn(batch, D, dtype=dtype, seed=seed + 2), "conv_weight": _randn(D, W, seed=seed + 3) / 2,
+            "W_x": _randn(R + 2 * N, D, dtype=dtype, seed=seed + 4) / D ** 0.5,
+            "W_dt": _randn(D, R, dtype=dtype, seed=seed + 5) / R ** 0.5,
+            "A": -torch.rand((D, N), generator=torch.Generator("cuda").manual_seed(seed + 6), device="cuda") * N - 0.1,
+            "conv_bias": _randn(D, seed=seed + 7) / 8, "z": _randn(batch, D, dtype=dtype, seed=seed + 8),
+            "dt_bias": _randn(D, seed=seed + 9) - 3, "Dskip": _randn(D, seed=seed + 10)}
+
+
+@pytest.mark.parametrize("io,dtype", [("f32", torch.float32), ("bf16", BF)])
+@pytest.mark.parametrize("shape", [(1, 130, 16, 5), (5, 261, 4, 9), (33, 300, 16, 17), (517, 130, 8, 24)], ids=str)
+def test_one_token_of_three_taps(shape, io, dtype):
+    import selective_state_space_22_amd as lib
+
+    t = _token(*shape, 3, dtype)
+    v = {k: a.double().cpu().numpy() for k, a in t.items()}
+    want = ref.conv_ssm_step(v["state"], v["window"], v["x"], v["conv_weight"], v["conv_bias"], v["W_x"], v["W_dt"], v["A"],
+                             v["z"], v["dt_bias"], v["Dskip"])
+    out = lib.mamba_conv_ssm_update(**t)
+    # 1.4e-5 of the input weight and three sums of at most 300 terms, as in test_gpu_layer.py
+    for got, w, tol in ((t["state"], want[0], 3e-5), (out, want[2], 9e-5 + ref.HALF[io])):
+        off = np.abs(got.double().cpu().numpy() - w) / np.maximum(np.abs(w), np.sqrt(np.mean(w * w)))
+        assert off.max() <= tol
+    assert np.array_equal(t["window"].double().cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_one_token_of_the_largest_batch(dtype):
+    import selective_state_space_22_amd as lib
+
+    batch = 65535
+    t = _token(batch, 8, 2, 3, 4, dtype)
+    pieces = [slice(0, 3), slice(3, 4), slice(4, 1000), slice(batch - 17, batch)]
+    rows = ("state", "window", "x", "z")
+    parts = [{k: v[p].clone() if k in rows else v for k, v in t.items()} for p in pieces]
+    out = lib.mamba_conv_ssm_update(**t)
+    step = lib.mamba_conv_update(t["window"].clone(), t["x"], t["conv_weight"], bias=t["conv_bias"])
+    for p, part in zip(pieces, parts):
+        assert torch.equal(lib.mamba_conv_ssm_update(**part), out[p])
+        assert torch.equal(part["state"], t["state"][p]) and torch.equal(part["window"], t["window"][p])
+        assert torch.equal(lib.mamba_conv_update(part["window"], part["x"], t["conv_weight"], bias=t["conv_bias"]), step[p])
+
+
+@pytest.mark.parametrize("batch", [3, 40, 600])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_row_that_is_no_number_stays_its_own(batch, bad):
+    import selective_state_space_22_amd as lib
+
+    t = _token(batch, 140, 16, 20, 4, BF)
+    dirty = {k: v.clone() for k, v in t.items()}
+    dirty["x"][1, 7], dirty["state"][2, 5, 3], dirty["window"][0, 2, 139] = bad, bad, bad
+    out, got = lib.mamba_conv_ssm_update(**t), lib.mamba_conv_ssm_update(**dirty)
+    assert torch.equal(got[3:], out[3:]) and torch.equal(dirty["state"][3:], t["state"][3:])
+    # a state's own channel, and no other of its row
+    other = torch.arange(140, device="cuda") != 5
+    assert torch.equal(got[2, other], out[2, other]) and torch.equal(dirty["state"][2, other], t["state"][2, other])
+    assert not torch.isfinite(got[:2]).any()
+
+
+def test_pools_of_no_places_leave_every_row_idle():
+    import selective_state_space_22_amd as lib
+
+    for batch in (2, 300):
+        t = _token(batch, 70, 16, 9, 4, BF, places=0)
+        slots = torch.arange(batch, dtype=torch.int32, device="cuda") - 1
+        out = torch.full_like(t["x"], 7.0)
+        assert (lib.mamba_conv_ssm_update(**t, slots=slots, out=out) == 7).all()
+        assert (lib.mamba_conv_update(t["window"], t["x"], t["conv_weight"], slots=slots, out=out) == 7).all()
