@@ -8,13 +8,16 @@
 //
 // A thread owns two channels and walks a chunk of tokens with the taps in registers: every input is loaded
 // once (and W - 1 rows again per chunk) in coalesced loads, the next tile of four tokens in flight while one is
-// computed.  Chunks are as short as lets all threads run at once: a token needs what its neighbours load, but no
-// order among chunks.  Measured (a streaming copy reaches 6.1 TB/s; bytes as the formulas need them):
-//   forward 4 x 4096 x 5120 bf16, rows three quarters full   49 us, 294 MB: 6.0 TB/s; bound by memory
+// computed.  Chunks are as short as a count of threads allows (kThreads): a token needs what its neighbours load, but
+// no order among chunks.  Measured (a streaming copy reaches 6.1 TB/s; bytes as the formulas need them):
+//   forward 4 x 4096 x 5120 bf16, rows three quarters full   49 us, 294 MB: 6.0 TB/s; bound by memory (60 a call
+//                                          where the inputs change from call to call)
 //   forward 8 x 2048 x 1536 bf16, resets   26 us, 101 MB: 3.9 TB/s; 22 vector operations an element, half of the time
 //   gradients of the same                  41 us, 151 MB: 3.7 TB/s; 40 vector operations an element, 61% of the time
-//   3 x 1537 x 1101 fp32                   12 us, 41 MB: 3.4 TB/s; gradients 14 us, 61 MB: 4.4 TB/s (read 30% more
-//                                          than that: three tokens beside every chunk of eight)
+//   3 x 1537 x 1101 fp32                   12 us, 41 MB: 3.4 TB/s; gradients 14 us, 61 MB: 4.4 TB/s.  These read 53 MB
+//                                          where the formulas need 41: with three taps a chunk (here 16 tokens) reads
+//                                          four rows of x and two of dout beside its own, 19%; the other 10% have
+//                                          not been explained
 //   sum over the chunks' parts             4 to 5 us, a launch and its latency
 //   one token 256 x 5120 bf16              6 us, 21 MB: 3.5 TB/s; latency of one round of loads
 #include <type_traits>
@@ -33,11 +36,15 @@ constexpr int kTileBwd = 4;
 // 8 x 2048 x 1536 bf16 65, 72 and fp32 106, 118; step 256 x 5120 bf16 5.3, 5.6 and fp32 8.3, 8.1).
 constexpr int kGroup = 2;
 constexpr int64_t kLeastFwd = 8, kMostFwd = 32, kLeastBwd = 8, kMostBwd = 128;  // tokens per thread
-constexpr int64_t kThreads = 256 * 12 * 64;  // threads that run at once (three waves per SIMD)
+// Threads that a launch is split into where the sequences are long enough: three waves per SIMD, fewer than the
+// registers of either kernel let run at once (forward 50 to 77: 6 to 8 waves; gradients 76 to 138: 3 to 6), since
+// every chunk reads its neighbours' tokens again.  2, 3, 4, 6 waves: forward and gradients 8 x 2048 x 1536 bf16 69.5, 66,
+// 68, 70 us and 3 x 1537 x 1101 fp32 30.5, 29, 31, 31.5; the latter's forward alone 12.1, 11.5, 11.1, 10.3.
+constexpr int64_t kThreads = 256 * 12 * 64;
 
 int64_t groups(int64_t D) { return (D + kGroup - 1) / kGroup; }
 
-// Tokens per thread, between `least` and `most`: the fewest with which all threads run at once (kThreads), so that
+// Tokens per thread, between `least` and `most`: the fewest with which there are no more than kThreads threads, so that
 // no few of them are left for a second round.
 int64_t chunk_of(int64_t batch, int64_t L, int64_t D, int64_t least, int64_t most) {
   const int64_t rows = batch * groups(D);  // threads per chunk of the sequence

@@ -70,8 +70,8 @@ __device__ __forceinline__ raw_t<T, V> narrow(const float (&f)[V]) {
   return v;
 }
 
-// sigma(v) = 1 / (1 + e^-v), and SiLU'(v) = sigma (1 + v (1 - sigma)).  Like SiLU itself, the slope at
-// -infinity is no number.
+// sigma(v) = 1 / (1 + e^-v), and SiLU'(v) = sigma (1 + v (1 - sigma)).  The slope is no number at either infinity, SiLU
+// itself only at -infinity.
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-v * kLog2e)); }
 __device__ __forceinline__ float silu_slope(float v) {
   const float s = sigmoid(v);

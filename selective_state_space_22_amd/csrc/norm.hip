@@ -608,8 +608,9 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64
   }
 }
 
-// Threads and chunks per thread of a row: about as many threads as it has chunks of two, since idle ones take a part of the
-// workgroup's registers (forward and gradients of 1892 x 4576 bf16: 640 threads 63 us, 1024 75; 512 with four chunks 65).
+// Threads and chunks per thread of a row, in steps: a row just above one leaves threads idle, which take a part of the
+// workgroup's registers all the same (forward and gradients of 1892 x 4576 bf16: 640 threads 67 us, 1024 78, 512 with four
+// chunks 69).  The widest steps are 2561 to 4096 and 8193 to 16384 elements, where up to 37% and a half of them idle.
 template <typename F>
 void row_shape(int64_t D, F f) {
 #define S6_NORM_SHAPE(nt, nv) f(std::integral_constant<int, nt>(), std::integral_constant<int, nv>())
@@ -626,7 +627,7 @@ void row_shape(int64_t D, F f) {
   else if (D <= 5120) S6_NORM_SHAPE(640, 2);
   else if (D <= 6144) S6_NORM_SHAPE(768, 2);
   else if (D <= 8192) S6_NORM_SHAPE(1024, 2);
-  else S6_NORM_SHAPE(1024, 4);
+  else S6_NORM_SHAPE(1024, 4);  // fp32 rows that E does not divide spill four registers (700 x 12003 111 us, 12004 104)
 #undef S6_NORM_SHAPE
 }
 
@@ -673,8 +674,12 @@ NormBwdPlan plan_norm_bwd(int64_t rows, int64_t D) {
   NormBwdPlan p{0, 0, 0, 0};
   if (D <= kSumsDim) {
     row_shape(D, [&](auto nt, auto nv) {
-      // as many workgroups as run at once: with more than one chunk a thread's registers leave two waves per SIMD
-      // (16384 x 768 bf16: 512 workgroups 38 us, 640 53, 768 48, 1024 44)
+      // Workgroups that stay: four a compute unit with one chunk a thread, else two, or one of more than 256 threads.  Two
+      // waves per SIMD are what the registers of three chunks leave (225 to 250; 16384 x 768 bf16: 512 workgroups 38 us,
+      // 640 53, 768 48, 1024 44); those of two chunks (156 to 190) leave two or three.  Forward and gradients in bf16 or,
+      // marked, fp32 with this count, 1.5 and 2 times it: 16384 x 512 38.2, 38.0, 43 us; 9000 x 1024 f 73.5, 79, 78.6;
+      // 4611 x 1101 f 47.0, 45.2, 51.5; 8192 x 1536 87.7, 79.0, 91; 5000 x 2048 49.7, 48.5, 54.6; 4096 x 2560 96, 112, 100;
+      // 2048 x 4096 43.3, 50, 49.  One chunk, half of it, this count and twice: 40000 x 250 56.7, 48.7, 51.
       const int64_t most = 256 * (nv == 1 ? 4 : (nt * rows_of(nt) <= 256 ? 2 : 1));
       p.parts = (rows + rows_of(nt) - 1) / rows_of(nt);
       p.parts = p.parts < most ? p.parts : most;

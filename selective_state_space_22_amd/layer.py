@@ -94,7 +94,8 @@ def mamba_conv_bwd(x, weight, dout, bias=None, window=None, reset=None, silu=Tru
 
 def mamba_conv_update(window, x, weight, bias=None, slots=None, silu=True, out=None):
     """One token of mamba_conv_fwd in place on window (nslots, W - 1, D); x: (batch, D).  slots: (batch,) int32,
-    the window of each row (None: row b has window b), negative for an idle row, whose out is left as it was."""
+    the window of each row (None: row b has window b), negative for an idle row, whose out is left as it was (without
+    ``out``: as the new tensor's memory was)."""
     return _native().conv_update(window, x, weight, bias, slots, silu, out)
 
 
@@ -106,7 +107,7 @@ def mamba_conv_ssm_update(state, window, x, conv_weight, W_x, W_dt, A, conv_bias
                           Dskip=None, slots=None, out=None, workspace=None):
     """One token of a layer from its input projection on, in place on state (nslots, D, N) float32 and window
     (nslots, W - 1, D): the convolution with SiLU, the selection projections (W_x (R + 2N, D), W_dt (D, R)) and
-    the state update, with fp32 values between them.  x, z: (batch, D); slots as for mamba_conv_update."""
+    the state update, with fp32 values between them.  x, z: (batch, D); slots and out as for mamba_conv_update."""
     return _native().conv_ssm_update(state, window, x, conv_weight, W_x, W_dt, A, conv_bias, z, dt_bias, Dskip, slots, out,
                                      workspace)
 
