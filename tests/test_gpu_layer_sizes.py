@@ -53,7 +53,8 @@ class Conv:
         if self.reset is not None:  # a long stretch without any, and some one after the other
             self.reset[:, L // 3: L // 3 + 300] = False
             self.reset[:, 37:43] = True
-        self.full = torch.cat([torch.zeros_like(self.x[:, :W - 1]) if self.window is None else self.window, self.x], 1).double()
+        before = self.x.new_zeros((b, W - 1, D)) if self.window is None else self.window
+        self.full = torch.cat([before, self.x], 1).double()
         document = torch.zeros((b, L), device="cuda", dtype=torch.int64) if self.reset is None else self.reset.long().cumsum(1)
         self.of = torch.cat([document.new_zeros((b, W - 1)), document], 1)
         self.L = L
